@@ -59,11 +59,14 @@ def listed():
         # a batch of prompts through the shared expert's gate/up
         dict(name="linear 8192 tokens", op="linear", M=8192, N=4096, K=4096, dtype="bf16", out="bf16"),
         # one decoded token at 6 of 256 experts, gate/up
-        dict(name="experts 1 token", op="moe", T=1, k=6, E=256, N=4096, K=4096, slots=False, dtype="bf16"),
+        dict(name="experts 1 token", op="moe", T=1, k=6, E=256, N=4096, K=4096, slots=False, dtype="bf16",
+             out="f32"),
         # a 512-token prompt at the down projection: each pair its own input, about 12 pairs per expert
-        dict(name="experts 512 tokens", op="moe", T=512, k=6, E=256, N=4096, K=2048, slots=True, dtype="bf16"),
+        dict(name="experts 512 tokens", op="moe", T=512, k=6, E=256, N=4096, K=2048, slots=True, dtype="bf16",
+             out="f32"),
         # a batch of prompts on one device's share of the experts, about 384 pairs per expert
-        dict(name="experts 4096 tokens", op="moe", T=4096, k=6, E=64, N=2048, K=4096, slots=False, dtype="bf16"),
+        dict(name="experts 4096 tokens", op="moe", T=4096, k=6, E=64, N=2048, K=4096, slots=False, dtype="bf16",
+             out="bf16"),
     ]
 
 
@@ -93,7 +96,8 @@ def _draw(rng):
                     dtype=rng.choice(["f32", "bf16", "f16"]), out=rng.choice(["f32", "bf16", "f16"]))
     E = rng.choice([8, 16, 60, 64, 128, 256])
     return dict(op=op, T=_log(rng, 1, 4096), k=rng.randint(1, min(8, E // 2)), E=E, N=_log(rng, 128, 4096),
-                K=16 * _log(rng, 16, 256), slots=rng.random() < 0.4, dtype=rng.choice(["f32", "bf16"]))
+                K=16 * _log(rng, 16, 256), slots=rng.random() < 0.4, dtype=rng.choice(["f32", "bf16"]),
+                out=rng.choice(["f32", "f32", "bf16", "f16"]))
 
 
 def draw(rng):
@@ -285,7 +289,7 @@ def _plain_linear(codes, scales, x, out):
     return (_widen(q, s) @ _widen(codes, scales)[0].t()).to(TYPES[out])
 
 
-def _plain_moe(codes, scales, x, ids, slots):
+def _plain_moe(codes, scales, x, ids, slots, out):
     T, k = ids.shape
     N, K = codes.shape[1:]
     q, s = _plain_quantize(x)
@@ -302,7 +306,7 @@ def _plain_moe(codes, scales, x, ids, slots):
     y = torch.bmm(w, buf.transpose(1, 2).contiguous())
     res = torch.empty(T * k, N, device=x.device)
     res[order] = y.transpose(1, 2)[at[order], rank]
-    return res.view(T, k, N)
+    return res.view(T, k, N).to(TYPES[out])
 
 
 def run(state):
@@ -325,7 +329,8 @@ def run(state):
         w = q.Fp8Weights(state["codes"], state["scales"])
         if op == "linear":
             return {"y": q.fp8_linear(w, state["x"], out_dtype=TYPES[case["out"]])}
-        return {"y": q.moe_fp8(w, state["x"], state["ids"], x_slots=state["slots"])}
+        return {"y": q.moe_fp8(w, state["x"], state["ids"], x_slots=state["slots"],
+                               out_dtype=TYPES[case["out"]])}
     if op == "router":
         return _plain_router(state["logits"], state["bias"], case)
     if op == "router_grad":
@@ -335,7 +340,7 @@ def run(state):
         return {"codes": codes, "scales": scales}
     if op == "linear":
         return {"y": _plain_linear(state["codes"], state["scales"], state["x"], case["out"])}
-    return {"y": _plain_moe(state["codes"], state["scales"], state["x"], state["ids"], state["slots"])}
+    return {"y": _plain_moe(state["codes"], state["scales"], state["x"], state["ids"], state["slots"], case["out"])}
 
 
 # ---------------------------------------------------------------------------
@@ -363,7 +368,7 @@ def work(case):
     T, k, E = case["T"], case["k"], case["E"]
     P = T * k
     used = E * (1.0 - (1.0 - k / E) ** T)  # experts that some token takes, about
-    b = used * expert + T * (k if case["slots"] else 1) * K * BYTES[case["dtype"]] + P * 4 + P * N * 4
+    b = used * expert + T * (k if case["slots"] else 1) * K * BYTES[case["dtype"]] + P * 4 + P * N * BYTES[case["out"]]
     return {"bytes": b, "flops": 2 * P * N * K}
 
 
