@@ -27,11 +27,13 @@ __all__ = [
     "row_bytes", "plane_offsets", "pack_relayout", "unpack_relayout", "dequant", "moe_gemv",
     "route", "grouped_gemm", "prefill_workspace_bytes", "moe_prefill", "floor_gemv",
     "floor_dequant", "stream_read", "stream_write", "library_path",
+    "router_topk", "router_topk_grad", "Fp8Weights", "fp8_quantize", "fp8_linear",
+    "fp8_linear_workspace_bytes", "moe_fp8", "moe_fp8_workspace_bytes",
 ]
 
 IQ2_KS, IQ2_K, IQ1_S_R4 = 1, 2, 3
 FORMAT_NAMES = {"iq2_ks": IQ2_KS, "iq2_k": IQ2_K, "iq1_s_r4": IQ1_S_R4}
-_F32, _F16, _BF16 = 0, 1, 2
+_F32, _F16, _BF16, _E4M3 = 0, 1, 2, 3
 _DT = {torch.float32: _F32, torch.float16: _F16, torch.bfloat16: _BF16}
 
 _E_ARG, _E_FORMAT, _E_SHAPE, _E_WIDTH, _E_ROWS4, _E_SIZE, _E_TABLE, _E_HIP = -1, -2, -3, -4, -5, -6, -7, -8
@@ -62,6 +64,12 @@ class _Weights(ctypes.Structure):
                 ("in_", ctypes.c_int64), ("streams", ctypes.c_void_p), ("streams_bytes", ctypes.c_size_t)]
 
 
+class _Fp8Weights(ctypes.Structure):
+    _fields_ = [("experts", ctypes.c_int64), ("out", ctypes.c_int64), ("in_", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("codes_bytes", ctypes.c_size_t), ("scales", ctypes.c_void_p),
+                ("scales_count", ctypes.c_size_t)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -71,7 +79,8 @@ def _load():
         raise ImportError(f"{_LIB_PATH} is not built; run `python dequant_iqk_moe_amd/build.py`")
     L = ctypes.CDLL(_LIB_PATH)
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-    W = ctypes.POINTER(_Weights)
+    f32 = ctypes.c_float
+    W, F = ctypes.POINTER(_Weights), ctypes.POINTER(_Fp8Weights)
     sig = {
         "iqk_row_bytes": (sz, [i32, i64]),
         "iqk_plane_offsets": (i32, [i32, i64, i64, p, p]),
@@ -98,6 +107,13 @@ def _load():
         "iqk_floor_dequant": (i32, [W, i64, i64, i32, p, p]),
         "iqk_stream_read": (i32, [p, sz, p, sz, p]),
         "iqk_stream_write": (i32, [p, sz, ctypes.c_uint32, i32, p]),
+        "iqk_router_topk": (i32, [p, i32, i64, i64, i32, i32, p, i32, i32, i32, i32, f32, p, p, p]),
+        "iqk_router_topk_grad": (i32, [p, i32, p, p, i64, i64, i32, i32, i32, f32, p, p]),
+        "iqk_fp8_quantize": (i32, [p, i32, i64, i64, p, p, p]),
+        "iqk_fp8_linear_workspace": (i32, [F, i64, p]),
+        "iqk_fp8_linear": (i32, [F, p, i32, p, i64, p, sz, p, i32, p]),
+        "iqk_moe_fp8_workspace": (i32, [F, i64, i32, i32, p]),
+        "iqk_moe_fp8": (i32, [F, p, i32, p, i32, p, i64, i32, i32, p, sz, p, i32, p]),
         "iqk_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -511,4 +527,180 @@ def moe_prefill_fused(w: Weights, x: torch.Tensor, ids: torch.Tensor, values=Non
                                       _ids(ids), T, k, int(bool(sorted)),
                                       _dev(workspace, "workspace", torch.uint8), workspace.numel(),
                                       _dev(y, "y", torch.float32, T * k * w.out), _stream(stream)))
+    return y
+
+
+# ---------------------------------------------------------------------------
+# expert selection
+# ---------------------------------------------------------------------------
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+def _scoring(name: str) -> int:
+    if name not in _SCORING:
+        raise IqkValueError(_E_ARG, f"scoring must be one of {sorted(_SCORING)}, got {name!r}")
+    return _SCORING[name]
+
+
+def _logits(logits: torch.Tensor):
+    if logits.dim() != 2 or logits.dtype not in _DT:
+        raise IqkValueError(_E_ARG, "logits must be [T, E] in float32, float16 or bfloat16")
+    return _dev(logits, "logits"), _DT[logits.dtype]
+
+
+def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: torch.Tensor | None = None,
+                n_group: int = 1, topk_group: int = 1, group_top: int = 1, renorm: bool = True, scale: float = 1.0,
+                ids: torch.Tensor | None = None, weights: torch.Tensor | None = None, stream=None):
+    """The k experts of each token and their weights, (ids int32 [T, k],
+    weights float32 [T, k]), from router logits [T, E].  scoring: "softmax"
+    or "sigmoid"; bias [E] (float32) shifts the choice only; n_group > 1 keeps
+    the best topk_group groups of experts, by the best or (group_top=2) the
+    best two of each; renorm divides the weights by their sum."""
+    lp, dt = _logits(logits)
+    T, E = logits.shape
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _check(_lib.iqk_router_topk(lp, dt, T, E, k, _scoring(scoring), _dev(bias, "bias", torch.float32, E), n_group,
+                                topk_group, group_top, int(bool(renorm)), scale,
+                                _dev(ids, "ids", torch.int32, T * k), _dev(weights, "weights", torch.float32, T * k),
+                                _stream(stream)))
+    return ids, weights
+
+
+def router_topk_grad(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, scoring: str = "softmax",
+                     renorm: bool = True, scale: float = 1.0, d_logits: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Gradient of router_topk's weights with respect to the logits (of their
+    dtype), the chosen ids held fixed."""
+    lp, dt = _logits(logits)
+    T, E = logits.shape
+    ip = _ids(ids)
+    if ids.shape[0] != T:
+        raise IqkValueError(_E_SIZE, f"ids has {ids.shape[0]} rows, logits {T}")
+    k = ids.shape[1]
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _check(_lib.iqk_router_topk_grad(lp, dt, ip, _dev(d_weights, "d_weights", torch.float32, T * k), T, E, k,
+                                     _scoring(scoring), int(bool(renorm)), scale,
+                                     _dev(d_logits, "d_logits", logits.dtype, T * E), _stream(stream)))
+    return d_logits
+
+
+# ---------------------------------------------------------------------------
+# products in 8-bit floating point, a scale for each block of 128
+# ---------------------------------------------------------------------------
+
+_XDT = {**_DT, torch.float8_e4m3fn: _E4M3}
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+@dataclass
+class Fp8Weights:
+    """8-bit weights: codes [experts, out, in] (torch.float8_e4m3fn) with
+    scales [experts, ceil(out / 128), ceil(in / 128)] (float32), one per
+    128 x 128 block."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def __post_init__(self):
+        if self.codes.dim() != 3 or self.codes.dtype != torch.float8_e4m3fn:
+            raise IqkValueError(_E_ARG, "codes must be float8_e4m3fn [experts, out, in]")
+        self.experts, self.out, self.in_features = self.codes.shape
+        if self.scales.dtype != torch.float32 or tuple(self.scales.shape) != (
+                self.experts, _blocks(self.out), _blocks(self.in_features)):
+            raise IqkValueError(_E_SIZE, "scales must be float32 [experts, ceil(out / 128), ceil(in / 128)]")
+
+    def _c(self) -> _Fp8Weights:
+        cp, sp = _dev(self.codes, "codes"), _dev(self.scales, "scales")
+        return _Fp8Weights(self.experts, self.out, self.in_features, cp, self.codes.numel(), sp, self.scales.numel())
+
+
+def fp8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """x [..., n] -> (codes float8_e4m3fn [..., n], scales float32
+    [..., ceil(n / 128)]), one scale per 1 x 128 block."""
+    if x.dtype not in _DT:
+        raise IqkValueError(_E_ARG, "x must be float32, float16 or bfloat16")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise IqkValueError(_E_ARG, "x must be [..., n] with n > 0")
+    n = x.shape[-1]
+    rows = x.numel() // n
+    if codes is None:
+        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty((*x.shape[:-1], _blocks(n)), dtype=torch.float32, device=x.device)
+    _check(_lib.iqk_fp8_quantize(_dev(x, "x"), _DT[x.dtype], rows, n,
+                                 _dev(codes, "codes", torch.float8_e4m3fn, rows * n),
+                                 _dev(scales, "scales", torch.float32, rows * _blocks(n)), _stream(stream)))
+    return codes, scales
+
+
+def _fp8_x(x: torch.Tensor, x_scales: torch.Tensor | None, rows: int, n: int):
+    if x.dtype not in _XDT:
+        raise IqkValueError(_E_ARG, "x must be float32, float16, bfloat16 or float8_e4m3fn")
+    return (_dev(x, "x", None, rows * n), _XDT[x.dtype],
+            _dev(x_scales, "x_scales", torch.float32, rows * _blocks(n)))
+
+
+def fp8_linear_workspace_bytes(w: Fp8Weights, M: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.iqk_fp8_linear_workspace(ctypes.byref(_Fp8Weights(w.experts, w.out, w.in_features)), M,
+                                         ctypes.byref(b)))
+    return b.value
+
+
+def fp8_linear(w: Fp8Weights, x: torch.Tensor, x_scales: torch.Tensor | None = None, out_dtype=torch.float32,
+               workspace: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [..., out] = x [..., in] times one expert's 8-bit weights.  x in a
+    float type is quantized on the way (as fp8_quantize does); codes come
+    with their x_scales."""
+    n = w.in_features
+    if x.dim() == 0 or x.shape[-1] != n:
+        raise IqkValueError(_E_SIZE, f"x must be [..., {n}]")
+    M = x.numel() // n
+    xp, xdt, sp = _fp8_x(x, x_scales, M, n)
+    if y is None:
+        y = torch.empty((*x.shape[:-1], w.out), dtype=out_dtype, device=x.device)
+    if y.dtype not in _DT:
+        raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
+    if workspace is None and xdt != _E4M3:
+        workspace = torch.empty(fp8_linear_workspace_bytes(w, M), dtype=torch.uint8, device=x.device)
+    cw = w._c()
+    _check(_lib.iqk_fp8_linear(ctypes.byref(cw), xp, xdt, sp, M, _dev(workspace, "workspace", torch.uint8),
+                               0 if workspace is None else workspace.numel(), _dev(y, "y", None, M * w.out),
+                               _DT[y.dtype], _stream(stream)))
+    return y
+
+
+def moe_fp8_workspace_bytes(w: Fp8Weights, T: int, k: int, x_slots: int = 1) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.iqk_moe_fp8_workspace(ctypes.byref(_Fp8Weights(w.experts, w.out, w.in_features)), T, k, x_slots,
+                                      ctypes.byref(b)))
+    return b.value
+
+
+def moe_fp8(w: Fp8Weights, x: torch.Tensor, ids: torch.Tensor, x_slots: int = 1,
+            x_scales: torch.Tensor | None = None, sorted: bool = False, out_dtype=torch.float32,
+            workspace: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The routed projection over 8-bit experts: y [T, k, out].  x [T *
+    x_slots, in] as in fp8_linear; pairs with an invalid id get NaN rows."""
+    ip = _ids(ids)
+    T, k = ids.shape
+    xp, xdt, sp = _fp8_x(x, x_scales, T * x_slots, w.in_features)
+    if y is None:
+        y = torch.empty((T, k, w.out), dtype=out_dtype, device=x.device)
+    if y.dtype not in _DT:
+        raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
+    if workspace is None:
+        workspace = torch.empty(moe_fp8_workspace_bytes(w, T, k, x_slots), dtype=torch.uint8, device=x.device)
+    cw = w._c()
+    _check(_lib.iqk_moe_fp8(ctypes.byref(cw), xp, xdt, sp, x_slots, ip, T, k, int(bool(sorted)),
+                            _dev(workspace, "workspace", torch.uint8), workspace.numel(),
+                            _dev(y, "y", None, T * k * w.out), _DT[y.dtype], _stream(stream)))
     return y

@@ -27,7 +27,10 @@ PER_FILE = {
     "iqk_fused.hip": [],
     "iqk_glue.hip": [],
     "iqk_noalloc.hip": [],
+    "iqk_router.hip": [],
+    "iqk_fp8.hip": [],
     "iqk_host.cpp": [],
+    "iqk_layer_host.cpp": [],
     "iqk_relayout.cpp": [],
     "iqk_status.cpp": [],
 }

@@ -59,6 +59,7 @@ struct RouteLaunch {
     int32_t *counts, *offsets, *perm;
     float* ynan = nullptr;  // if set: rows [P, yout] of the call's output, NaN for pairs with an invalid id
     int64_t yout = 0;
+    int yhalf = 0;  // 1: the rows of ynan are of a 16-bit type
 };
 
 struct GemmLaunch {
@@ -86,6 +87,60 @@ struct FusedLaunch {
     int64_t* plan;        // device int64[E + 1] (scratch: per-expert cost prefix)
     float* y;
 };
+
+// Expert selection from router logits, and its gradient.
+struct RouterLaunch {
+    const void* logits;  // [T, E] of dtype
+    int dtype;
+    int64_t T;
+    int E, k, scoring;
+    const float* bias;  // [E] or null
+    int n_group, topk_group, group_top, renorm;
+    float scale;
+    int32_t* ids;    // [T, k]
+    float* weights;  // [T, k]
+};
+
+struct RouterGradLaunch {
+    const void* logits;
+    int dtype;
+    const int32_t* ids;
+    const float* d_weights;
+    int64_t T;
+    int E, k, scoring, renorm;
+    float scale;
+    void* d_logits;  // [T, E] of dtype
+};
+
+// Block quantization of activations to e4m3.
+struct Fp8QuantLaunch {
+    const void* x;  // [rows, n] of x_dtype
+    int x_dtype;
+    int64_t rows, n;
+    uint8_t* codes;  // [rows, n]
+    float* scales;   // [rows, ceil(n / 128)]
+};
+
+// The 8-bit product, dense (ids, offsets and perm null: M rows of x) or over
+// routed pairs: per pair (ids) or grouped by expert (offsets, perm).
+struct Fp8Launch {
+    int64_t E, out, n;
+    const uint8_t* codes;  // [E, out, n]
+    const float* scales;   // [E, ceil(out / 128), ceil(n / 128)]
+    const void* x;         // [rows, n] of x_dtype
+    int x_dtype;
+    const float* x_scales;  // [rows, ceil(n / 128)] for e4m3 x
+    int64_t M;              // rows of y: tokens, or pairs
+    int x_slots, k;
+    const int32_t *ids, *offsets, *perm;
+    void* y;  // [M, out] of y_dtype
+    int y_dtype;
+};
+
+hipError_t launch_router(const RouterLaunch& a, hipStream_t s);
+hipError_t launch_router_grad(const RouterGradLaunch& a, hipStream_t s);
+hipError_t launch_fp8_quantize(const Fp8QuantLaunch& a, hipStream_t s);
+hipError_t launch_fp8_product(const Fp8Launch& a, hipStream_t s);
 
 hipError_t launch_dequant(const DequantLaunch& a, bool floor_variant, hipStream_t s);
 hipError_t launch_fused_prefill(const FusedLaunch& a, hipStream_t s);

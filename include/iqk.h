@@ -75,7 +75,8 @@ extern "C" {
 #endif
 
 typedef enum { IQK_IQ2_KS = 1, IQK_IQ2_K = 2, IQK_IQ1_S_R4 = 3 } iqk_format;
-typedef enum { IQK_F32 = 0, IQK_F16 = 1, IQK_BF16 = 2 } iqk_dtype;
+typedef enum { IQK_F32 = 0, IQK_F16 = 1, IQK_BF16 = 2, IQK_E4M3 = 3 } iqk_dtype; /* E4M3: 8-bit products only */
+typedef enum { IQK_SOFTMAX = 0, IQK_SIGMOID = 1 } iqk_scoring;
 typedef enum {
     IQK_OK = 0,
     IQK_E_ARG = -1,     /* null pointer, negative size, bad enum, bad count */
@@ -339,6 +340,97 @@ int iqk_stream_read(const void* buf, size_t bytes, uint32_t* sink, size_t sink_w
  * shape of the bf16 producer (each wave stores the 8 KiB it decoded).
  * Other values of `runs` fail with IQK_E_ARG. */
 int iqk_stream_write(void* buf, size_t bytes, uint32_t value, int runs, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Expert selection: from a router's logits to the `ids` and `route_w` that
+ * the routed calls above take ("Surface" takes both as inputs).
+ *
+ * logits: device [T, E] of dtype (IQK_F32, IQK_F16 or IQK_BF16).  Scores, in
+ * float32: IQK_SOFTMAX s_e = exp(l_e - max l) / sum exp(l - max l);
+ * IQK_SIGMOID s_e = 1 / (1 + exp(-l_e)).  The choice goes by c_e = s_e +
+ * bias[e] when bias (device float32 [E], may be null) is given, else by the
+ * logit itself.  With n_group > 1 the experts form n_group groups of
+ * E / n_group consecutive ids; a group counts its best c (group_top = 1) or
+ * the sum of its best two (group_top = 2; of the scores when there is no
+ * bias), and only the best topk_group groups stay.  ids (device int32
+ * [T, k]): the k largest c of what stays, in falling order.  Equal values, of
+ * groups and of experts, go to the lowest index.  weights (device float32
+ * [T, k]): scale * s_j, divided by the sum of the k chosen scores if renorm
+ * is 1 (all zero where that sum is zero).  The bias takes no part in them.
+ *
+ * Masks and special values: an expert whose logit or bias is -inf is never
+ * chosen (a -inf logit also has score zero; the type's lowest finite value is
+ * an ordinary logit).  Slots no expert is left for repeat slot 0 at weight
+ * zero, so a weighted sum over the slots stays right; a row with no expert at
+ * all gets ids -1 and weights zero.  A row with a NaN logit, and with +inf
+ * under IQK_SOFTMAX, and every row under a NaN bias, gets ids -1 and weights
+ * NaN (the routed calls make such rows NaN).
+ * Limits: E <= 1024, k <= min(64, E), n_group <= 64, T <= 2^30 (IQK_E_ARG). */
+int iqk_router_topk(const void* logits, int dtype, int64_t T, int64_t E, int k, int scoring, const float* bias,
+                    int n_group, int topk_group, int group_top, int renorm, float scale,
+                    int32_t* ids, float* weights, void* stream);
+
+/* Gradient of iqk_router_topk's weights with respect to the logits, the
+ * choice held fixed: d_logits [T, E] (of dtype, every element written) from
+ * d_weights = dL/dweights (device float32 [T, k]) and the forward call's
+ * ids.  renorm, scoring and scale as in the forward call; the bias and the
+ * groups only make the choice and have no gradient.  A slot whose id lies
+ * outside [0, E), and one that repeats slot 0, takes no part.  float32
+ * arithmetic, one rounding to dtype; deterministic. */
+int iqk_router_topk_grad(const void* logits, int dtype, const int32_t* ids, const float* d_weights, int64_t T,
+                         int64_t E, int k, int scoring, int renorm, float scale, void* d_logits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products in 8-bit floating point (e4m3: sign, 4 exponent bits of bias 7, 3
+ * fraction bits, largest value 448, codes 0x7F and 0xFF are NaN) with a
+ * float32 scale for each block of 128: the layer's always-on (shared) expert
+ * and whole layers kept in 8 bits beside the IQ_K ones.
+ *
+ * Weights: codes [experts, out, in] and scales [experts, ceil(out / 128),
+ * ceil(in / 128)], device, dense, row-major: the weight is code * scale of
+ * its 128 x 128 block (edge blocks are partial).  in % 16 == 0
+ * (IQK_E_SHAPE); out and in <= 2^20, out * in < 2^31, experts <= 16384;
+ * codes 16-byte aligned. */
+typedef struct iqk_fp8_weights {
+    int64_t experts, out, in;
+    const void* codes;
+    size_t codes_bytes;    /* experts * out * in */
+    const float* scales;
+    size_t scales_count;   /* experts * ceil(out / 128) * ceil(in / 128) */
+} iqk_fp8_weights;
+
+/* Quantization of activations: x device [rows, n] (IQK_F32, IQK_F16 or
+ * IQK_BF16) -> codes [rows, n], scales float32 [rows, ceil(n / 128)].  Per
+ * 1 x 128 block: a = max(max |x|, 2^-100), scale = a / 448, code =
+ * e4m3(x * (448 / a)), the quotients and the product rounded to float32, the
+ * code to nearest even.  A NaN in x gives a NaN code; an infinity gives a NaN
+ * code and an infinite scale.  n % 16 == 0 (IQK_E_SHAPE), n <= 2^20, rows <=
+ * 2^24; x and codes 16-byte aligned. */
+int iqk_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, uint8_t* codes, float* scales,
+                     void* stream);
+
+/* y[m, o] = sum_b x_scale[m, b] * w_scale[o / 128, b] * sum over block b of
+ * x_code[m, i] * w_code[o, i]; y device [M, out] of y_dtype (IQK_F32,
+ * IQK_F16 or IQK_BF16), one rounding to nearest even.  w->experts must be 1.
+ * x: device [M, in], IQK_E4M3 with x_scales [M, ceil(in / 128)], or a float
+ * type with x_scales null, which the call quantizes as iqk_fp8_quantize does.
+ * workspace (16-byte aligned, iqk_fp8_linear_workspace bytes) holds the
+ * quantized x; it may be null for IQK_E4M3 x.  Accuracy against the product
+ * of the same codes and scales: 2e-6 in norm for a float32 y; 16-bit results
+ * are off by their rounding.  A NaN or infinity in a row of x makes that row of
+ * y NaN or infinite and no other.  x 16-byte aligned; M <= 2^24. */
+int iqk_fp8_linear_workspace(const iqk_fp8_weights* w, int64_t M, size_t* bytes);
+int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const float* x_scales, int64_t M,
+                   void* workspace, size_t ws_bytes, void* y, int y_dtype, void* stream);
+
+/* The same product at routed pairs, y[t, j, :] = W_{ids[t, j]} x[t, s, :]
+ * (s and x_slots as in iqk_moe_gemv): y device [T, k, out] of y_dtype.  ids,
+ * sorted and the NaN rows of invalid ids as in iqk_moe_prefill; x, x_scales
+ * (rows t * x_slots + s) and accuracy as in iqk_fp8_linear.  T * k <= 2^24. */
+int iqk_moe_fp8_workspace(const iqk_fp8_weights* w, int64_t T, int k, int x_slots, size_t* bytes);
+int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const float* x_scales, int x_slots,
+                const int32_t* ids, int64_t T, int k, int sorted, void* workspace, size_t ws_bytes,
+                void* y, int y_dtype, void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* iqk_last_error(void);
