@@ -41,6 +41,32 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
     if constexpr (DT == IQK_BF16) ((uint16_t*)y)[i] = bf16_bits(v);
 }
 
+// 16 consecutive results, of which `left` are inside the row (`whole`: rows
+// of y are multiples of 16 bytes long and aligned)
+template <int DT>
+__device__ __forceinline__ void store16(void* y, int64_t i, const float (&v)[16], bool whole, int left) {
+    if (whole) {
+        if constexpr (DT == IQK_F32) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *(float4*)((float*)y + i + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if constexpr (DT == IQK_BF16) w[q] = bf16_bits(v[2 * q]) | ((uint32_t)bf16_bits(v[2 * q + 1]) << 16);
+                else w[q] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * q], (_Float16)v[2 * q + 1]});
+            }
+            *(uint4*)((uint16_t*)y + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            *(uint4*)((uint16_t*)y + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+            if (q < left) store_y<DT>(y, i + q, v[q]);
+    }
+}
+
 // 8 consecutive activations as float32
 template <int DT>
 __device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[8]) {
@@ -200,6 +226,242 @@ __global__ __launch_bounds__(64 * kWaves) void fp8_rows_kernel(ProductParams p) 
     }
 }
 
+// ---------------------------------------------------------------------------
+// tiled product
+// ---------------------------------------------------------------------------
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+struct TileParams {
+    const uint8_t* W;
+    const float* sw;
+    const uint8_t* x;
+    const float* sx;
+    int64_t M;
+    int out, n, k, x_slots, E;
+    const int32_t *offsets, *perm, *tiles;  // grouped: tiles[e] = 256- or 128-row tiles of x before expert e
+    void* y;
+};
+
+// 16 bytes per lane from memory straight into LDS: lane l's go to dst + 16 l
+// (dst the same in every lane).  Written as an instruction because the
+// compiler takes every later LDS read to depend on the builtin's copy and
+// waits for it at once; the kernel waits for its copies before the barrier
+// that publishes them.  The instruction has no register result.
+__device__ __forceinline__ void lds_copy16(const uint8_t* base, uint32_t off, uint8_t* dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void lds_copy16(const uint8_t* src, uint8_t* dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+}
+
+// The 16-byte chunk of a 128-byte tile row is kept at slot chunk ^ key(row),
+// so that eight neighbouring lanes of a fragment read eight slots.  A
+// fragment's 16 lanes read weight rows 16 (l / 4) + l % 4 + const (keyed by
+// the row's bits 0, 1 and 4) and x rows l + const (by its bits 0 to 2).
+__device__ __forceinline__ int wkey(int r) { return (r & 3) | ((r >> 2) & 4); }
+__device__ __forceinline__ int xkey(int r) { return r & 7; }
+
+template <int TM, int TN, int WM, int WN, int YT, bool GROUPED>
+__global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(TileParams p) {
+    constexpr int kNW = (TM / WM) * (TN / WN);  // waves
+    constexpr int kI = WN / 16, kJ = WM / 16;   // a wave's tiles of weight rows and of x rows
+    constexpr int kRowsPerCopy = 8 * kNW;       // rows one copy instruction of all waves covers
+    constexpr int kCW = TN / kRowsPerCopy, kCX = TM / kRowsPerCopy;
+    __shared__ uint8_t sh[2][(TN + TM) * 128];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int li = lane & 15, g = lane >> 4;
+    const int nb = (p.n + kBlock - 1) / kBlock;
+    const int ntn = (p.out + TN - 1) / TN;
+
+    // which tile: the tiles of one XCD (workgroups b with equal b % 8) are neighbours
+    int e = 0;
+    int64_t m0, count = p.M, begin = 0;
+    int n0;
+    {
+        const int64_t tiles_m = GROUPED ? p.tiles[p.E] : (p.M + TM - 1) / TM;
+        const int64_t total = tiles_m * ntn, per = (total + 7) / 8;
+        const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+        if ((int64_t)(blockIdx.x >> 3) >= per || id >= total) return;
+        if constexpr (GROUPED) {
+            const int t = (int)(id / ntn);
+            n0 = (int)(id - (int64_t)t * ntn) * TN;
+            // the expert of tile t: the last e with tiles[e] <= t, 64 candidates at a time
+            int lo = 0, span = p.E;
+            while (span > 1) {
+                const int step = (span + 63) / 64;
+                const int c = lo + lane * step;
+                const uint64_t le = __ballot(c < lo + span && p.tiles[c < p.E ? c : p.E] <= t);
+                const int last = 63 - __builtin_clzll(le);
+                const int nlo = lo + last * step;
+                span = min(step, lo + span - nlo);
+                lo = nlo;
+            }
+            e = __builtin_amdgcn_readfirstlane(lo);
+            begin = p.offsets[e];
+            count = p.offsets[e + 1] - begin;
+            m0 = (int64_t)(t - p.tiles[e]) * TM;
+        } else {
+            // bands of 8 tiles of x by all of the weights' tiles
+            const int64_t band = id / (8 * ntn), in = id - band * 8 * ntn;
+            const int64_t rows = min((int64_t)8, tiles_m - band * 8);
+            m0 = (band * 8 + in % rows) * TM;
+            n0 = (int)(in / rows) * TN;
+        }
+    }
+
+    // copies: lane l of a copy moves slot l & 7 of row l >> 3 of its wave's
+    // eight rows; rows past the end repeat the last, their results are dropped
+    const int crow = wave * 8 + (lane >> 3);
+    const int nob = (p.out + kBlock - 1) / kBlock;
+    auto wchunk = [&](int c) { return 16 * ((lane & 7) ^ wkey(c * kRowsPerCopy + crow)); };
+    auto xchunk = [&](int c) { return 16 * ((lane & 7) ^ xkey(c * kRowsPerCopy + crow)); };
+    // row i of the tile's x rows, as a row of p.x, and as a row of y
+    auto pair_of = [&](int i) { return p.perm[begin + min(m0 + i, count - 1)]; };
+    auto row_of = [&](int i) -> int64_t {
+        if constexpr (GROUPED) return p.x_slots == 1 ? pair_of(i) / p.k : pair_of(i);
+        else return min(m0 + i, count - 1);
+    };
+    const uint8_t* wbase = p.W + ((int64_t)e * p.out + n0) * p.n;
+    const uint8_t* xbase = GROUPED ? p.x : p.x + m0 * p.n;  // (dense: offsets inside the tile fit 32 bits)
+    uint32_t woff[kCW], xoff[kCX];
+    const uint8_t* xsrc[kCX];
+#pragma unroll
+    for (int c = 0; c < kCW; ++c)
+        woff[c] = (uint32_t)(min(c * kRowsPerCopy + crow, p.out - 1 - n0) * p.n + wchunk(c));
+#pragma unroll
+    for (int c = 0; c < kCX; ++c) {
+        if constexpr (GROUPED) xsrc[c] = p.x + row_of(c * kRowsPerCopy + crow) * p.n + xchunk(c);
+        else xoff[c] = (uint32_t)((int)(row_of(c * kRowsPerCopy + crow) - m0) * p.n + xchunk(c));
+    }
+    auto copy_w = [&](int c, int k0, uint8_t* d) { lds_copy16(wbase + k0, woff[c], d); };
+    auto copy_x = [&](int c, int k0, uint8_t* d) {
+        if constexpr (GROUPED) lds_copy16(xsrc[c] + k0, d);
+        else lds_copy16(xbase + k0, xoff[c], d);
+    };
+    auto copy_block = [&](int b, uint8_t* dst) {
+        const int k0 = b * kBlock;
+        uint8_t* base = dst + wave * 1024;
+        if (k0 + kBlock <= p.n) {
+#pragma unroll
+            for (int c = 0; c < kCW; ++c) copy_w(c, k0, base + c * kRowsPerCopy * 128);
+#pragma unroll
+            for (int c = 0; c < kCX; ++c) copy_x(c, k0, base + (TN + c * kRowsPerCopy) * 128);
+        } else {  // the partial last block: chunks past the depth are zero
+#pragma unroll
+            for (int c = 0; c < kCW; ++c) {
+                uint8_t* d = base + c * kRowsPerCopy * 128;
+                if (k0 + wchunk(c) < p.n) copy_w(c, k0, d);
+                else *(uint4*)(d + lane * 16) = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int c = 0; c < kCX; ++c) {
+                uint8_t* d = base + (TN + c * kRowsPerCopy) * 128;
+                if (k0 + xchunk(c) < p.n) copy_x(c, k0, d);
+                else *(uint4*)(d + lane * 16) = make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+
+    const int wn = (wave % (TN / WN)) * WN, wm = (wave / (TN / WN)) * WM;  // this wave's part of the tile
+    // scales: one per 128 weight rows (a wave's rows lie in one block), one per row of x
+    const float* sw = p.sw + ((int64_t)e * nob + min((n0 + wn) / kBlock, nob - 1)) * nb;
+    const float* sx = GROUPED ? p.sx : p.sx + m0 * nb;
+    using Offset = std::conditional_t<GROUPED, int64_t, uint32_t>;
+    Offset sxo[kJ];
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) sxo[j] = (Offset)((row_of(wm + 16 * j + li) - (GROUPED ? 0 : m0)) * nb);
+
+    f32x4 acc[kI][kJ];
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // fragment rows: lane li of tile i reads weight row 64 (i / 4) + 16 (li / 4) + 4 (i % 4) + li % 4, so that a
+    // result lane's four rows of four neighbouring tiles are 16 consecutive rows
+    const int arow = wn + 16 * (li >> 2) + (li & 3);
+    const int brow = wm + li;
+    const int aoff = arow * 128 + 16 * (g ^ wkey(16 * (li >> 2) + (li & 3)));
+    const int boff = (TN + brow) * 128 + 16 * (g ^ xkey(li));
+    auto frag = [&](const uint8_t* s, int off) {
+        const uint4 a = *(const uint4*)(s + off), b = *(const uint4*)(s + (off ^ 64));
+        return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    };
+
+    float sxn[kJ], swn, f[kJ], fp[kJ];
+    f32x4 d[2][kJ];  // products of a tile row on their way to the sums, added while the next row's are made
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) fp[j] = 0.f, d[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    copy_block(0, sh[0]);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) sxn[j] = sx[sxo[j]];
+    swn = sw[0];
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    for (int b = 0; b < nb; ++b) {
+        const uint8_t* cur = sh[b & 1];
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) f[j] = sxn[j] * swn;
+        if (b + 1 < nb) {
+            copy_block(b + 1, sh[(b + 1) & 1]);
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) sxn[j] = sx[sxo[j] + (b + 1)];
+            swn = sw[b + 1];
+        }
+        i32x8 af[2], bf[kJ];
+        af[0] = frag(cur, aoff);
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) bf[j] = frag(cur, boff + j * 2048);
+#pragma unroll
+        for (int i = 0; i < kI; ++i) {
+            // (the key's bits are those of the row inside its 64: tiles i and i + 4 are 64 rows apart, tiles i and
+            // i + 1 four rows, which no key bit looks at)
+            if (i + 1 < kI) af[(i + 1) & 1] = frag(cur, aoff + ((i + 1) >> 2) * 8192 + ((i + 1) & 3) * 512);
+            constexpr int kLast = kI - 1;
+            const int ip = i ? i - 1 : kLast;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                d[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    af[i & 1], bf[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[ip][j][q] = __builtin_fmaf(d[(i + 1) & 1][j][q], i ? f[j] : fp[j], acc[ip][j][q]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) fp[j] = f[j];
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+    }
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[kI - 1][j][q] = __builtin_fmaf(d[1][j][q], fp[j], acc[kI - 1][j][q]);
+
+    // result lane (li, g) holds, of x row 16 j + li, weight rows 64 (i / 4) + 16 g + 4 (i % 4) + q
+    const bool whole = (p.out & 15) == 0 && ((uintptr_t)p.y & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+        const int i = wm + 16 * j + li;
+        if (m0 + i >= count) continue;
+        int64_t yrow = m0 + i;
+        if constexpr (GROUPED) yrow = pair_of(i);
+#pragma unroll
+        for (int h = 0; h < kI / 4; ++h) {
+            const int o = n0 + wn + 64 * h + 16 * g;
+            if (o >= p.out) continue;
+            float v[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) v[q] = acc[4 * h + (q >> 2)][j][q & 3];
+            store16<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
+        }
+    }
+}
+
 template <class F>
 void by_y(int dt, F f) {
     if (dt == IQK_F32) f(std::integral_constant<int, IQK_F32>{});
@@ -222,6 +484,25 @@ hipError_t launch_fp8_quantize(const Fp8QuantLaunch& a, hipStream_t s) {
 hipError_t launch_fp8_product(const Fp8Launch& a, hipStream_t s) {
     ProductParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.E, (int)a.out, (int)a.n,
                     a.k, a.x_slots, a.ids, a.offsets, a.perm, a.y};
+    if (!a.offsets && a.y_dtype != IQK_F32 && a.M > 32) {
+        TileParams t{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots, 1,
+                     nullptr, nullptr, nullptr, a.y};
+        const int64_t big = ((a.M + 255) / 256) * ((a.out + 255) / 256);
+        by_y(a.y_dtype, [&](auto yt) {
+            constexpr int YT = decltype(yt)::value;
+            if constexpr (YT != IQK_F32) {
+                if (big >= 160) {
+                    hipLaunchKernelGGL((fp8_tile_kernel<256, 256, 64, 128, YT, false>), dim3((unsigned)((big + 7) / 8 * 8)),
+                                       dim3(512), 0, s, t);
+                } else {
+                    const int64_t tiles = ((a.M + 127) / 128) * ((a.out + 127) / 128);
+                    hipLaunchKernelGGL((fp8_tile_kernel<128, 128, 64, 64, YT, false>), dim3((unsigned)((tiles + 7) / 8 * 8)),
+                                       dim3(256), 0, s, t);
+                }
+            }
+        });
+        return hipGetLastError();
+    }
     const unsigned gx = (unsigned)((a.out + 15) / 16);
     by_y(a.y_dtype, [&](auto yt) {
         constexpr int YT = decltype(yt)::value;
