@@ -244,17 +244,25 @@ struct TileParams {
 };
 
 // 16 bytes per lane from memory straight into LDS: lane l's go to dst + 16 l
-// (dst the same in every lane).  Written as an instruction because the
+// (an LDS address, the same in every lane).  Written as an instruction because the
 // compiler takes every later LDS read to depend on the builtin's copy and
 // waits for it at once; the kernel waits for its copies before the barrier
 // that publishes them.  The instruction has no register result.
-__device__ __forceinline__ void lds_copy16(const uint8_t* base, uint32_t off, uint8_t* dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst);
+__device__ __forceinline__ void lds_copy16(const uint8_t* base, uint32_t off, uint32_t dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
 }
-__device__ __forceinline__ void lds_copy16(const uint8_t* src, uint8_t* dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst);
+__device__ __forceinline__ void lds_copy16(const uint8_t* src, uint32_t dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+}
+
+// Waits for this wave's copies and LDS accesses, then for the other waves'.
+__device__ __forceinline__ void publish() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // The 16-byte chunk of a 128-byte tile row is kept at slot chunk ^ key(row),
@@ -336,31 +344,32 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         if constexpr (GROUPED) xsrc[c] = p.x + row_of(c * kRowsPerCopy + crow) * p.n + xchunk(c);
         else xoff[c] = (uint32_t)((int)(row_of(c * kRowsPerCopy + crow) - m0) * p.n + xchunk(c));
     }
-    auto copy_w = [&](int c, int k0, uint8_t* d) { lds_copy16(wbase + k0, woff[c], d); };
-    auto copy_x = [&](int c, int k0, uint8_t* d) {
+    auto copy_w = [&](int c, int k0, uint32_t d) { lds_copy16(wbase + k0, woff[c], d); };
+    auto copy_x = [&](int c, int k0, uint32_t d) {
         if constexpr (GROUPED) lds_copy16(xsrc[c] + k0, d);
         else lds_copy16(xbase + k0, xoff[c], d);
     };
-    auto copy_block = [&](int b, uint8_t* dst) {
+    const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sh[0][0];
+    auto copy_block = [&](int b) {
         const int k0 = b * kBlock;
-        uint8_t* base = dst + wave * 1024;
+        const uint32_t at = (b & 1) * (TN + TM) * 128 + wave * 1024;
         if (k0 + kBlock <= p.n) {
 #pragma unroll
-            for (int c = 0; c < kCW; ++c) copy_w(c, k0, base + c * kRowsPerCopy * 128);
+            for (int c = 0; c < kCW; ++c) copy_w(c, k0, sh0 + at + c * kRowsPerCopy * 128);
 #pragma unroll
-            for (int c = 0; c < kCX; ++c) copy_x(c, k0, base + (TN + c * kRowsPerCopy) * 128);
+            for (int c = 0; c < kCX; ++c) copy_x(c, k0, sh0 + at + (TN + c * kRowsPerCopy) * 128);
         } else {  // the partial last block: chunks past the depth are zero
 #pragma unroll
             for (int c = 0; c < kCW; ++c) {
-                uint8_t* d = base + c * kRowsPerCopy * 128;
-                if (k0 + wchunk(c) < p.n) copy_w(c, k0, d);
-                else *(uint4*)(d + lane * 16) = make_uint4(0, 0, 0, 0);
+                const uint32_t d = at + c * kRowsPerCopy * 128;
+                if (k0 + wchunk(c) < p.n) copy_w(c, k0, sh0 + d);
+                else *(uint4*)(&sh[0][0] + d + lane * 16) = make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int c = 0; c < kCX; ++c) {
-                uint8_t* d = base + (TN + c * kRowsPerCopy) * 128;
-                if (k0 + xchunk(c) < p.n) copy_x(c, k0, d);
-                else *(uint4*)(d + lane * 16) = make_uint4(0, 0, 0, 0);
+                const uint32_t d = at + (TN + c * kRowsPerCopy) * 128;
+                if (k0 + xchunk(c) < p.n) copy_x(c, k0, sh0 + d);
+                else *(uint4*)(&sh[0][0] + d + lane * 16) = make_uint4(0, 0, 0, 0);
             }
         }
     };
@@ -368,6 +377,9 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     const int wn = (wave % (TN / WN)) * WN, wm = (wave / (TN / WN)) * WM;  // this wave's part of the tile
     // scales: one per 128 weight rows (a wave's rows lie in one block), one per row of x
     const float* sw = p.sw + ((int64_t)e * nob + min((n0 + wn) / kBlock, nob - 1)) * nb;
+    // (a vector load: a scalar load in flight would make every wait for an LDS read a wait for all of them)
+    uint32_t swo = 0;
+    asm("" : "+v"(swo));
     const float* sx = GROUPED ? p.sx : p.sx + m0 * nb;
     using Offset = std::conditional_t<GROUPED, int64_t, uint32_t>;
     Offset sxo[kJ];
@@ -391,56 +403,71 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
     };
 
+    // Instruction t = i kJ + j of a block multiplies tile row i by x tile j.  Its product is added to the sums two
+    // instructions later (kLag: it is done by then), and a tile row is read two rows before its first use.
+    constexpr int kLag = 2, kRing = 4, kT = kI * kJ;
+    static_assert(kT % kRing == 0, "a block's first products follow the last block's in the ring");
     float sxn[kJ], swn, f[kJ], fp[kJ];
-    f32x4 d[2][kJ];  // products of a tile row on their way to the sums, added while the next row's are made
+    f32x4 d[kRing];
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) fp[j] = 0.f, d[1][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    copy_block(0, sh[0]);
+    for (int j = 0; j < kJ; ++j) fp[j] = 0.f;
+#pragma unroll
+    for (int t = 0; t < kRing; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int t, const float* w) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            acc[t / kJ][t % kJ][q] = __builtin_fmaf(d[t % kRing][q], w[t % kJ], acc[t / kJ][t % kJ][q]);
+    };
+copy_block(0);
 #pragma unroll
     for (int j = 0; j < kJ; ++j) sxn[j] = sx[sxo[j]];
-    swn = sw[0];
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_s_barrier();
+    swn = sw[swo];
+    publish();
     for (int b = 0; b < nb; ++b) {
         const uint8_t* cur = sh[b & 1];
 #pragma unroll
         for (int j = 0; j < kJ; ++j) f[j] = sxn[j] * swn;
         if (b + 1 < nb) {
-            copy_block(b + 1, sh[(b + 1) & 1]);
+            copy_block(b + 1);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) sxn[j] = sx[sxo[j] + (b + 1)];
-            swn = sw[b + 1];
+            swn = sw[swo + (b + 1)];
         }
-        i32x8 af[2], bf[kJ];
-        af[0] = frag(cur, aoff);
+        // (the key's bits are those of the row inside its 64: tile rows i and i + 4 are 64 rows apart, i and i + 1
+        // four rows, which no key bit looks at)
+        auto afrag = [&](int i) { return frag(cur, aoff + (i >> 2) * 8192 + (i & 3) * 512); };
+        i32x8 af[3], bf[kJ];
+        af[0] = afrag(0);
+        bf[0] = frag(cur, boff);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) bf[j] = frag(cur, boff + j * 2048);
+        for (int j = 1; j < kJ; ++j) {
+            bf[j] = frag(cur, boff + j * 2048);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        af[1] = afrag(1);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < kI; ++i) {
-            // (the key's bits are those of the row inside its 64: tiles i and i + 4 are 64 rows apart, tiles i and
-            // i + 1 four rows, which no key bit looks at)
-            if (i + 1 < kI) af[(i + 1) & 1] = frag(cur, aoff + ((i + 1) >> 2) * 8192 + ((i + 1) & 3) * 512);
-            constexpr int kLast = kI - 1;
-            const int ip = i ? i - 1 : kLast;
+            if (i + 2 < kI) af[(i + 2) % 3] = afrag(i + 2);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
-                d[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    af[i & 1], bf[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    acc[ip][j][q] = __builtin_fmaf(d[(i + 1) & 1][j][q], i ? f[j] : fp[j], acc[ip][j][q]);
+                const int t = i * kJ + j;
+                const f32x4 r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    af[i % 3], bf[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                __builtin_amdgcn_sched_barrier(0);
+                if (t >= kLag) add(t - kLag, f);
+                else add(kT - kLag + t, fp);
+                d[t % kRing] = r;
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
 #pragma unroll
         for (int j = 0; j < kJ; ++j) fp[j] = f[j];
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
+        publish();
     }
 #pragma unroll
-    for (int j = 0; j < kJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[kI - 1][j][q] = __builtin_fmaf(d[1][j][q], fp[j], acc[kI - 1][j][q]);
+    for (int t = kT - kLag; t < kT; ++t) add(t, fp);
 
     // result lane (li, g) holds, of x row 16 j + li, weight rows 64 (i / 4) + 16 g + 4 (i % 4) + q
     const bool whole = (p.out & 15) == 0 && ((uintptr_t)p.y & 15) == 0;
