@@ -28,7 +28,9 @@ PER_FILE = {
     "iqk_glue.hip": [],
     "iqk_noalloc.hip": [],
     "iqk_router.hip": [],
-    "iqk_fp8.hip": [],
+    "iqk_fp8_prep.hip": [],
+    "iqk_fp8_rows.hip": [],
+    "iqk_fp8_tile.hip": [],
     "iqk_host.cpp": [],
     "iqk_layer_host.cpp": [],
     "iqk_relayout.cpp": [],

@@ -1,0 +1,140 @@
+// iqk_fp8_device.h -- device helpers of the 8-bit products: e4m3 conversions,
+// loads of activations and stores of results.
+//
+//   y[m, o] = sum_b sx[m, b] * sw[o / 128, b] * sum_{i in block b} qx[m, i] * qw[o, i]
+//
+// Quantization of one 1 x 128 block: a = max(max |x|, 2^-100), sx = a / 448,
+// qx = e4m3(x * (448 / a)), each step rounded to nearest even (the reciprocal
+// and the product to float32); 448 is the largest e4m3 value, and the floor
+// keeps the reciprocal finite and an all-zero block zero.
+//
+// Sums.  Every e4m3 value is a float16 value, and the float16 matrix
+// instructions sum such products exactly to float32 rounding (5e-9 of a
+// block's norm measured).  The 8-bit matrix instructions run twice as fast,
+// but align the products of a step to the largest and drop what falls below
+// it (1.7e-5 of the norm measured, 5e-5 on operands over e4m3's whole range):
+// less than a 16-bit result resolves, more than a float32 result may be off.
+// So float32 results are summed on the former everywhere, 16-bit results on
+// the latter where the matrix rate is what bounds the product.
+#pragma once
+
+#include <type_traits>
+
+#include "iqk_device.h"
+
+namespace iqk {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kBlock = 128;              // values per scale
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 0x1p-100f;
+
+__device__ __forceinline__ uint16_t bf16_bits(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0x7FC0u;
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+template <int DT>
+__device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
+    if constexpr (DT == IQK_F32) ((float*)y)[i] = v;
+    if constexpr (DT == IQK_F16) ((_Float16*)y)[i] = (_Float16)v;
+    if constexpr (DT == IQK_BF16) ((uint16_t*)y)[i] = bf16_bits(v);
+}
+
+// 16 consecutive results, of which `left` are inside the row (`whole`: rows
+// of y are multiples of 16 bytes long and aligned)
+template <int DT>
+__device__ __forceinline__ void store16(void* y, int64_t i, const float (&v)[16], bool whole, int left) {
+    if (whole) {
+        if constexpr (DT == IQK_F32) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *(float4*)((float*)y + i + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if constexpr (DT == IQK_BF16) w[q] = bf16_bits(v[2 * q]) | ((uint32_t)bf16_bits(v[2 * q + 1]) << 16);
+                else w[q] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * q], (_Float16)v[2 * q + 1]});
+            }
+            *(uint4*)((uint16_t*)y + i) = make_uint4(w[0], w[1], w[2], w[3]);
+            *(uint4*)((uint16_t*)y + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
+            if (q < left) store_y<DT>(y, i + q, v[q]);
+    }
+}
+
+// 8 consecutive activations as float32
+template <int DT>
+__device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[8]) {
+    if constexpr (DT == IQK_F32) {
+        const float4 a = *(const float4*)((const float*)x + i), b = *(const float4*)((const float*)x + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 a = *(const uint4*)((const uint16_t*)x + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (DT == IQK_BF16) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            } else {
+                const f16x2 h = __builtin_bit_cast(f16x2, w[j]);
+                v[2 * j] = (float)h[0];
+                v[2 * j + 1] = (float)h[1];
+            }
+        }
+    }
+}
+
+// e4m3 codes of 8 values already multiplied by 448 / a
+__device__ __forceinline__ uint2 to_e4m3(const float (&v)[8]) {
+    uint2 q;
+    q.x = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+    q.x = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], q.x, true);
+    q.y = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);
+    q.y = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], q.y, true);
+    return q;
+}
+
+// float16 values of 8 e4m3 codes (exact; a NaN code gives NaN)
+__device__ __forceinline__ f16x8 widen(uint32_t lo, uint32_t hi) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+
+// max(largest |v| of the 16 lanes of a row, 2^-100): the block's amax, in
+// every lane (rotations within the row of 16)
+__device__ __forceinline__ float block_amax(const float (&v)[8]) {
+    float a = kAmaxFloor;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(v[j]));
+    auto ror = [](float x, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    a = fmaxf(a, ror(a, std::integral_constant<int, 0x128>{}));
+    a = fmaxf(a, ror(a, std::integral_constant<int, 0x124>{}));
+    a = fmaxf(a, ror(a, std::integral_constant<int, 0x122>{}));
+    a = fmaxf(a, ror(a, std::integral_constant<int, 0x121>{}));
+    return a;
+}
+
+// f(std::integral_constant<int, dtype>) for a float type of the C ABI
+template <class F>
+void by_float(int dt, F f) {
+    if (dt == IQK_F32) f(std::integral_constant<int, IQK_F32>{});
+    else if (dt == IQK_F16) f(std::integral_constant<int, IQK_F16>{});
+    else f(std::integral_constant<int, IQK_BF16>{});
+}
+
+}  // namespace iqk

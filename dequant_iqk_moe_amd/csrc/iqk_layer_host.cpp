@@ -87,6 +87,18 @@ size_t quantized_bytes(int64_t rows, int64_t n) {
     return round256((size_t)(rows * n)) + round256((size_t)(rows * blocks128(n)) * 4);
 }
 
+// Rows of x up to which the dense product passes over the weights once
+// without tiles.
+constexpr int64_t kRowsPass = 64;
+// Rows per expert up to which the routed product does.
+constexpr double kGroupedRows = 48;
+
+// Whether the routed product takes each pair by itself: no grouping, one
+// launch, an expert's weights read once for each of its pairs.
+bool pair_by_pair(int64_t P, int64_t E, int64_t n) {
+    return P <= std::max<int64_t>(8, E / 4) && P <= 4096 && iqk::fp8_few_fits(1, n);
+}
+
 // Quantizes the rows of a product's x into `ws` and points L at the result.
 hipError_t quantize_into(iqk::Fp8Launch* L, int64_t rows, uint8_t* ws, hipStream_t s) {
     iqk::Fp8QuantLaunch Q{L->x, L->x_dtype, rows, L->n, ws, (float*)(ws + round256((size_t)(rows * L->n)))};
@@ -171,12 +183,16 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
     if (rc) return rc;
     hipStream_t s = (hipStream_t)stream;
     iqk::Fp8Launch L{1, w->out, w->in, (const uint8_t*)w->codes, w->scales, x, x_dtype, x_scales, M, 1, 1,
-                     nullptr, nullptr, nullptr, y, y_dtype};
-    if (quantize) {
-        hipError_t e = quantize_into(&L, M, (uint8_t*)workspace, s);
-        if (e != hipSuccess) return hip_fail(e, "quantize launch");
+                     nullptr, nullptr, nullptr, nullptr, y, y_dtype};
+    hipError_t e;
+    if (iqk::fp8_few_fits(M, w->in)) {
+        e = iqk::launch_fp8_few(L, s);
+    } else {
+        if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace, s)) != hipSuccess)
+            return hip_fail(e, "quantize launch");
+        e = M <= kRowsPass ? iqk::launch_fp8_rows(L, (int)((M + 15) / 16), s)
+                           : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows(M, M, w->out, y_dtype == IQK_F32), s);
     }
-    hipError_t e = iqk::launch_fp8_product(L, s);
     if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
     return ok();
 }
@@ -187,8 +203,9 @@ int iqk_moe_fp8_workspace(const iqk_fp8_weights* w, int64_t T, int k, int x_slot
     if (rc) return rc;
     if (T < 0 || k <= 0 || T > kMaxRows / k) return fail(IQK_E_ARG, "T * k must lie in [0, 2^24]");
     if (x_slots != 1 && x_slots != k) return fail(IQK_E_ARG, "x_slots must be 1 or k");
-    *bytes = round256((size_t)w->experts * 4) + round256((size_t)(w->experts + 1) * 4) +
-             round256((size_t)std::max<int64_t>(T * k, 1) * 4) + quantized_bytes(T * x_slots, w->in);
+    const size_t E = (size_t)w->experts, P = (size_t)std::max<int64_t>(T * k, 1);
+    *bytes = round256(E * 4) + 2 * round256((E + 1) * 4) + round256(P * 4) +
+             round256((size_t)iqk::fp8_group_slices(P) * E * 4) + quantized_bytes(T * x_slots, w->in);
     return ok();
 }
 
@@ -208,27 +225,56 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
     rc = check_workspace(workspace, ws_bytes, need);
     if (rc) return rc;
     const int64_t E = w->experts, P = T * k;
-    uint8_t* ws = (uint8_t*)workspace;
-    int32_t* counts = (int32_t*)ws;
-    ws += round256((size_t)E * 4);
-    int32_t* offsets = (int32_t*)ws;
-    ws += round256((size_t)(E + 1) * 4);
-    int32_t* perm = (int32_t*)ws;
-    ws += round256((size_t)P * 4);
     hipStream_t s = (hipStream_t)stream;
     iqk::Fp8Launch L{E, w->out, w->in, (const uint8_t*)w->codes, w->scales, x, x_dtype, x_scales, P, x_slots, k,
-                     ids, offsets, perm, y, y_dtype};
-    iqk::RouteLaunch RL{ids, P, E, sorted, counts, offsets, perm};
-    RL.ynan = (float*)y;  // rows of pairs with an invalid id: NaN
-    RL.yout = w->out;
-    RL.yhalf = y_dtype != IQK_F32;
-    hipError_t e = iqk::launch_route(RL, s);
-    if (e != hipSuccess) return hip_fail(e, "route launch");
-    if (x_dtype != IQK_E4M3) {
-        e = quantize_into(&L, T * x_slots, ws, s);
-        if (e != hipSuccess) return hip_fail(e, "quantize launch");
+                     ids, nullptr, nullptr, nullptr, y, y_dtype};
+    hipError_t e;
+    if (pair_by_pair(P, E, w->in)) {
+        e = iqk::launch_fp8_few(L, s);
+        if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
+        return ok();
     }
-    e = iqk::launch_fp8_product(L, s);
+    uint8_t* ws = (uint8_t*)workspace;
+    auto take = [&](size_t bytes) {
+        uint8_t* at = ws;
+        ws += round256(bytes);
+        return at;
+    };
+    const double per_expert = (double)P / (double)E;
+    const bool tiled = per_expert > kGroupedRows;
+    const int tile = iqk::fp8_tile_rows((int64_t)per_expert, P, w->out, y_dtype == IQK_F32);
+    iqk::Fp8GroupLaunch G{};
+    G.ids = ids;
+    G.P = P;
+    G.E = (int)E;
+    G.tile = tile;
+    G.counts = (int32_t*)take((size_t)E * 4);
+    G.offsets = (int32_t*)take((size_t)(E + 1) * 4);
+    G.tiles = (int32_t*)take((size_t)(E + 1) * 4);
+    G.perm = (int32_t*)take((size_t)P * 4);
+    G.hist = (int32_t*)take((size_t)iqk::fp8_group_slices(P) * E * 4);
+    G.y = y;
+    G.out = (int)w->out;
+    G.y_half = y_dtype != IQK_F32;
+    iqk::Fp8QuantLaunch Q{x, x_dtype, T * x_slots, w->in, ws, (float*)(ws + round256((size_t)(T * x_slots * w->in)))};
+    e = iqk::launch_fp8_prep(G, Q, s);
+    if (e != hipSuccess) return hip_fail(e, "grouping launch");
+    if (x_dtype != IQK_E4M3) {
+        L.x = Q.codes;
+        L.x_scales = Q.scales;
+        L.x_dtype = IQK_E4M3;
+    }
+    L.ids = nullptr;
+    L.offsets = G.offsets;
+    L.perm = G.perm;
+    L.tiles = G.tiles;
+    if (tiled) {
+        e = iqk::launch_fp8_tile(L, tile, s);
+    } else {
+        // rows a pass holds: what most experts have (their counts spread like a square root)
+        const int passes = (int)std::ceil((per_expert + 2.0 * std::sqrt(per_expert)) / 16.0);
+        e = iqk::launch_fp8_rows(L, passes, s);
+    }
     if (e != hipSuccess) return hip_fail(e, "8-bit grouped product launch");
     return ok();
 }

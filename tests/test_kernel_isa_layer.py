@@ -5,7 +5,7 @@ import pytest
 from test_kernel_isa import _device_asm, _kernels, pytestmark  # noqa: F401
 
 
-@pytest.mark.parametrize("src", ["iqk_router.hip", "iqk_fp8.hip"])
+@pytest.mark.parametrize("src", ["iqk_router.hip", "iqk_fp8_prep.hip", "iqk_fp8_rows.hip", "iqk_fp8_tile.hip"])
 def test_no_scratch(src, tmp_path):
     _, meta = _kernels(_device_asm(src, tmp_path))
     assert meta, "no kernels found"
