@@ -44,28 +44,26 @@ __device__ __forceinline__ void store_y(void* y, int64_t i, float v) {
     if constexpr (DT == IQK_BF16) ((uint16_t*)y)[i] = bf16_bits(v);
 }
 
-// 16 consecutive results, of which `left` are inside the row (`whole`: rows
-// of y are multiples of 16 bytes long and aligned)
+// 8 consecutive results, of which `left` are inside the row (`whole`: all of
+// them are, at 16-byte addresses)
 template <int DT>
-__device__ __forceinline__ void store16(void* y, int64_t i, const float (&v)[16], bool whole, int left) {
+__device__ __forceinline__ void store8(void* y, int64_t i, const float (&v)[8], bool whole, int left) {
     if (whole) {
         if constexpr (DT == IQK_F32) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *(float4*)((float*)y + i + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            *(float4*)((float*)y + i) = make_float4(v[0], v[1], v[2], v[3]);
+            *(float4*)((float*)y + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
         } else {
-            uint32_t w[8];
+            uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
                 if constexpr (DT == IQK_BF16) w[q] = bf16_bits(v[2 * q]) | ((uint32_t)bf16_bits(v[2 * q + 1]) << 16);
                 else w[q] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * q], (_Float16)v[2 * q + 1]});
             }
             *(uint4*)((uint16_t*)y + i) = make_uint4(w[0], w[1], w[2], w[3]);
-            *(uint4*)((uint16_t*)y + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         }
     } else {
 #pragma unroll
-        for (int q = 0; q < 16; ++q)
+        for (int q = 0; q < 8; ++q)
             if (q < left) store_y<DT>(y, i + q, v[q]);
     }
 }
@@ -128,6 +126,42 @@ __device__ __forceinline__ float block_amax(const float (&v)[8]) {
     a = fmaxf(a, ror(a, std::integral_constant<int, 0x121>{}));
     return a;
 }
+
+// 16 bytes per lane from memory straight into LDS: lane l's go to dst + 16 l
+// (an LDS address, the same in every lane).  Written as an instruction because the
+// compiler takes every later LDS read to depend on the builtin's copy and
+// waits for it at once; the kernel waits for its copies before the barrier
+// that publishes them.  The instruction has no register result.
+__device__ __forceinline__ void lds_copy16(const uint8_t* base, uint32_t off, uint32_t dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void lds_copy16(const uint8_t* src, uint32_t dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+}
+
+// The same for 4 bytes per lane.
+__device__ __forceinline__ void lds_copy4(const float* src, uint32_t dst) {
+    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
+}
+
+// Waits for this wave's LDS accesses and all but its last `LATER` memory
+// accesses, then for the other waves'.
+template <int LATER = 0>
+__device__ __forceinline__ void publish() {
+    static_assert(LATER < 64, "six bits of the wait's operand");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (LATER & 15) | (LATER >> 4) << 14);  // vmcnt(LATER) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The 16-byte chunk c of a 128-byte row r in LDS is kept at slot c ^ key(r), so
+// that eight neighbouring lanes of a fragment, which read chunk c of eight
+// rows, read eight slots.  Rows of x: lane l reads row l + const.
+__device__ __forceinline__ int xkey(int r) { return r & 7; }
 
 // f(std::integral_constant<int, dtype>) for a float type of the C ABI
 template <class F>

@@ -52,7 +52,7 @@ struct RowsParams {
     const float* sx;
     int64_t M;
     int E, out, n, k, x_slots;
-    const int32_t *ids, *offsets, *perm;
+    const int32_t* ids;
     void* y;
 };
 
@@ -167,61 +167,45 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(RowsParams p) {
 // more rows of x, quantized before: 16 NT rows in a pass over the weights
 // ---------------------------------------------------------------------------
 
-// A workgroup owns 16 RT weight rows; it holds the sums of 16 NT rows of x and
+// A workgroup owns 16 weight rows; it holds the sums of 16 NT rows of x and
 // requests the next block's weights and x while it multiplies the last ones.
+// (One weight tile per workgroup and the depth split over its waves: the dense
+// product of few rows has no other way to occupy the card.)
 constexpr int kRowsWaves = 4;
 
-template <int NT, int RT, int YT, bool GROUPED>
-__global__ __launch_bounds__(64 * kRowsWaves, NT * RT >= 8 ? 2 : (NT * RT >= 4 ? 3 : 4)) void fp8_rows_kernel(RowsParams p) {
-    __shared__ float4 red[kRowsWaves][RT * NT][64];
+template <int NT, int YT>
+__global__ __launch_bounds__(64 * kRowsWaves, NT >= 4 ? 3 : 4) void fp8_rows_kernel(RowsParams p) {
+    __shared__ float4 red[kRowsWaves][NT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & 15, g = lane >> 4;
     const int n = p.n, nb = (n + kBlock - 1) / kBlock;
-    const int row0 = blockIdx.x * 16 * RT;
-    int e = 0;
-    int64_t begin = 0, count = p.M;
-    if constexpr (GROUPED) {
-        e = blockIdx.y;
-        begin = p.offsets[e];
-        count = p.offsets[e + 1] - begin;
-        if (count == 0) return;
-    }
-    const int left = min(16 * RT, p.out - row0);
-    Rsrc wr[RT];  // one per tile: a lane's offset is the same in all of them, rows past the last read zero
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-        wr[i] = make_rsrc(p.W + ((int64_t)e * p.out + row0 + 16 * i) * n, (uint32_t)max(0, min(16, left - 16 * i)) * (uint32_t)n);
+    const int row0 = blockIdx.x * 16;
+    const int64_t count = p.M;
+    const int left = min(16, p.out - row0);
+    const Rsrc wr = make_rsrc(p.W + (int64_t)row0 * n, (uint32_t)left * (uint32_t)n);  // (rows past the last read zero)
     const uint32_t woff = (uint32_t)li * (uint32_t)n;
-    const int nob = (p.out + kBlock - 1) / kBlock;
-    const float* sw = p.sw + ((int64_t)e * nob + row0 / kBlock) * nb;  // (16 RT divides 128)
+    const float* sw = p.sw + (int64_t)(row0 / kBlock) * nb;
     for (int64_t m0 = 0; m0 < count; m0 += 16 * NT) {
         const uint8_t* xr[NT];
         const float* sx[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            int64_t r = min(m0 + 16 * t + li, count - 1);  // rows past the last repeat it, their results are dropped
-            if constexpr (GROUPED) {
-                r = p.perm[begin + r];
-                if (p.x_slots == 1) r /= p.k;
-            }
+            const int64_t r = min(m0 + 16 * t + li, count - 1);  // rows past the last repeat it, their results are dropped
             xr[t] = (const uint8_t*)p.x + r * n;
             sx[t] = p.sx + r * nb;
         }
-        f32x4 acc[RT][NT];
+        f32x4 acc[NT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         struct Stage {
-            Frag w[RT], x[NT];
+            Frag w, x[NT];
             float f[NT];
         } st[2];
         // (blocks past the last, which the loop requests and multiplies like any other, have zero weights)
         auto request = [&](int b, Stage& s) {
             const int c0 = b * kBlock + 16 * g, c1 = c0 + 64;
             const uint32_t o0 = c0 < n ? woff + c0 : kOob, o1 = c1 < n ? woff + c1 : kOob;
-#pragma unroll
-            for (int i = 0; i < RT; ++i) s.w[i] = Frag{ld128(wr[i], o0), ld128(wr[i], o1)};
+            s.w = Frag{ld128(wr, o0), ld128(wr, o1)};
             // a chunk of x past the depth meets zero weights; its row's first bytes are read instead of the next
             // row's, which could be NaN
             const int x0 = c0 < n ? c0 : 0, x1 = c1 < n ? c1 : 0, sb = min(b, nb - 1);
@@ -234,29 +218,11 @@ __global__ __launch_bounds__(64 * kRowsWaves, NT * RT >= 8 ? 2 : (NT * RT >= 4 ?
             }
         };
         auto multiply = [&](const Stage& s) {
-            // the smaller side is widened once and held, the other one tile at a time
-            if constexpr (NT <= RT) {
-                Wide x[NT];
+            const Wide w = widen_frag(s.w);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) x[t] = widen_frag(s.x[t]);
-#pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const Wide w = widen_frag(s.w[i]);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) add_scaled(acc[i][t], block_product(w, x[t]), s.f[t]);
-                    __builtin_amdgcn_sched_barrier(0);  // (else all tiles are widened at once, and registers run out)
-                }
-            } else {
-                Wide w[RT];
-#pragma unroll
-                for (int i = 0; i < RT; ++i) w[i] = widen_frag(s.w[i]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const Wide x = widen_frag(s.x[t]);
-#pragma unroll
-                    for (int i = 0; i < RT; ++i) add_scaled(acc[i][t], block_product(w[i], x), s.f[t]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+            for (int t = 0; t < NT; ++t) {
+                add_scaled(acc[t], block_product(w, widen_frag(s.x[t])), s.f[t]);
+                __builtin_amdgcn_sched_barrier(0);  // (else all tiles are widened at once, and registers run out)
             }
         };
         request(wave, st[0]);
@@ -267,25 +233,19 @@ __global__ __launch_bounds__(64 * kRowsWaves, NT * RT >= 8 ? 2 : (NT * RT >= 4 ?
             multiply(st[1]);
         }
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                red[wave][i * NT + t][lane] = make_float4(acc[i][t][0], acc[i][t][1], acc[i][t][2], acc[i][t][3]);
+        for (int t = 0; t < NT; ++t) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
         __syncthreads();
-        // RT neighbouring threads write the 16 RT results of one row of x: thread u takes 16 of them
-        for (int u = threadIdx.x; u < 16 * NT * RT * 4; u += 64 * kRowsWaves) {
-            const int q = u % (4 * RT), r = u / (4 * RT);  // four results of row r of the pass
-            const int o = 4 * q;
+        // four neighbouring threads write the 16 results of one row of x
+        for (int u = threadIdx.x; u < 16 * NT * 4; u += 64 * kRowsWaves) {
+            const int q = u & 3, r = u >> 2, o = 4 * q;
             if (m0 + r >= count || o >= left) continue;
             float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int w = 0; w < kRowsWaves; ++w) {
-                const float4 a = red[w][(q >> 2) * NT + (r >> 4)][16 * (q & 3) + (r & 15)];
+                const float4 a = red[w][r >> 4][16 * q + (r & 15)];
                 v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
             }
-            int64_t yrow = m0 + r;
-            if constexpr (GROUPED) yrow = p.perm[begin + yrow];
-            const int64_t at = yrow * p.out + row0 + o;
+            const int64_t at = (m0 + r) * p.out + row0 + o;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (o + j < left) store_y<YT>(p.y, at + j, v[j]);
@@ -296,16 +256,12 @@ __global__ __launch_bounds__(64 * kRowsWaves, NT * RT >= 8 ? 2 : (NT * RT >= 4 ?
 
 RowsParams rows_params(const Fp8Launch& a) {
     return RowsParams{a.codes, a.scales, a.x, a.x_scales, a.M, (int)a.E, (int)a.out, (int)a.n, a.k, a.x_slots,
-                      a.ids, a.offsets, a.perm, a.y};
+                      a.ids, a.y};
 }
 
-template <int NT, int RT, int YT>
+template <int NT, int YT>
 void rows_launch(const RowsParams& p, hipStream_t s) {
-    const unsigned gx = (unsigned)((p.out + 16 * RT - 1) / (16 * RT));
-    if (p.offsets)
-        hipLaunchKernelGGL((fp8_rows_kernel<NT, RT, YT, true>), dim3(gx, (unsigned)p.E), dim3(64 * kRowsWaves), 0, s, p);
-    else
-        hipLaunchKernelGGL((fp8_rows_kernel<NT, RT, YT, false>), dim3(gx, 1), dim3(64 * kRowsWaves), 0, s, p);
+    hipLaunchKernelGGL((fp8_rows_kernel<NT, YT>), dim3((unsigned)((p.out + 15) / 16)), dim3(64 * kRowsWaves), 0, s, p);
 }
 
 }  // namespace
@@ -332,20 +288,11 @@ hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s) {
 
 hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s) {
     const RowsParams p = rows_params(a);
-    // 64 weight rows per workgroup where that still leaves every CU a few of
-    // them (x is read and widened once for four times the weights), else 16
-    const bool wide = (a.out + 63) / 64 * (a.offsets ? a.E : 1) >= 512;
     by_float(a.y_dtype, [&](auto yt) {
         constexpr int YT = decltype(yt)::value;
-        if (wide) {
-            if (passes16 <= 1) rows_launch<1, 4, YT>(p, s);
-            else if (passes16 <= 2) rows_launch<2, 4, YT>(p, s);
-            else rows_launch<4, 2, YT>(p, s);
-        } else {
-            if (passes16 <= 1) rows_launch<1, 1, YT>(p, s);
-            else if (passes16 <= 2) rows_launch<2, 1, YT>(p, s);
-            else rows_launch<4, 1, YT>(p, s);
-        }
+        if (passes16 <= 1) rows_launch<1, YT>(p, s);
+        else if (passes16 <= 2) rows_launch<2, YT>(p, s);
+        else rows_launch<4, YT>(p, s);
     });
     return hipGetLastError();
 }

@@ -1,14 +1,29 @@
-// iqk_fp8_tile.hip -- the 8-bit product for many rows, tile by tile.
+// iqk_fp8_tile.hip -- the 8-bit product tile by tile.
+//
+// A workgroup owns TM rows of x by TN weight rows.  Each block of 128 of the
+// depth goes from memory straight into LDS, kStages - 1 blocks ahead, as 128
+// bytes per row with their 16-byte chunks permuted (xkey, wkey) so that a
+// fragment's reads meet no bank twice; the block's scales go along.  Every
+// block's products start at zero and are added to the float32 sums with the
+// product of the two scales.
+//
+// EXACT widens the fragments to float16 in registers and uses
+// v_mfma_f32_16x16x32_f16; otherwise one v_mfma_scale_f32_16x16x128_f8f6f4
+// (both scales 2^0) takes a whole block.
+//
+// What bounds it.  256 x 256 tiles of 16-bit results: the LDS, which every wave
+// reads 24 KiB of per block for 32 matrix instructions.  Small TM: the bytes of
+// the weights; the copies need no registers, so as many are in flight as the
+// LDS holds, and each is whole 128-byte lines, where fragments loaded by their
+// lanes would ask for halves of 16 lines at a time (512-token case of 256
+// experts: 445 us that way, 64 lines of x staged in LDS).
 #include <algorithm>
+#include <cmath>
 
 #include "iqk_fp8_device.h"
 
 namespace iqk {
 namespace {
-
-// ---------------------------------------------------------------------------
-// tiled product
-// ---------------------------------------------------------------------------
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
@@ -19,55 +34,50 @@ struct TileParams {
     const float* sx;
     int64_t M;
     int out, n, k, x_slots, E;
-    const int32_t *offsets, *perm, *tiles;  // grouped: tiles[e] = 256- or 128-row tiles of x before expert e
+    const int32_t *offsets, *perm, *tiles;  // grouped: tiles[e] = TM-row tiles of x before expert e
     void* y;
 };
 
-// 16 bytes per lane from memory straight into LDS: lane l's go to dst + 16 l
-// (an LDS address, the same in every lane).  Written as an instruction because the
-// compiler takes every later LDS read to depend on the builtin's copy and
-// waits for it at once; the kernel waits for its copies before the barrier
-// that publishes them.  The instruction has no register result.
-__device__ __forceinline__ void lds_copy16(const uint8_t* base, uint32_t off, uint32_t dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
-}
-__device__ __forceinline__ void lds_copy16(const uint8_t* src, uint32_t dst) {
-    const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+// What copies past the depth read.
+__device__ const uint4 g_zero = {0, 0, 0, 0};
+
+// Key of a tile's weight rows: a fragment's 16 lanes read rows
+// 4 G (l / 4) + l % 4 + const for groups of G = min(kI, 4) tiles, so bits 0, 1
+// and log2(4 G) of the row tell eight neighbouring lanes apart.
+template <int G>
+__device__ __forceinline__ int wkey(int r) {
+    constexpr int kBit = G == 1 ? 2 : (G == 2 ? 3 : 4);
+    return (r & 3) | (((r >> kBit) & 1) << 2);
 }
 
-// Waits for this wave's copies and LDS accesses, then for the other waves'.
-__device__ __forceinline__ void publish() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-}
+template <int TM, int TN, int WM, int WN, int S>
+struct TileShape {
+    static constexpr int kWaves = (TM / WM) * (TN / WN);
+    static constexpr int kI = WN / 16, kJ = WM / 16;     // a wave's tiles of weight rows and of rows of x
+    static constexpr int kG = kI < 4 ? kI : 4;           // tiles whose rows are dealt out four at a time
+    static constexpr int kRowsPerCopy = 8 * kWaves;      // rows one copy instruction of all waves covers
+    static constexpr int kCW = TN / kRowsPerCopy;
+    static constexpr int kCX = (TM + kRowsPerCopy - 1) / kRowsPerCopy;
+    static constexpr int kCopies = kCW + kCX + 1;        // memory instructions of a wave per block
+    static constexpr int kX = TN * 128, kScales = kX + kCX * kRowsPerCopy * 128;  // offsets in a stage
+    static constexpr int kStage = kScales + kWaves * 256;
+    static_assert(TM + (TN + 127) / 128 <= 64 * kWaves, "one scale per lane");
+    static_assert(S * kStage <= 160 * 1024, "LDS");
+};
 
-// The 16-byte chunk of a 128-byte tile row is kept at slot chunk ^ key(row),
-// so that eight neighbouring lanes of a fragment read eight slots.  A
-// fragment's 16 lanes read weight rows 16 (l / 4) + l % 4 + const (keyed by
-// the row's bits 0, 1 and 4) and x rows l + const (by its bits 0 to 2).
-__device__ __forceinline__ int wkey(int r) { return (r & 3) | ((r >> 2) & 4); }
-__device__ __forceinline__ int xkey(int r) { return r & 7; }
-
-template <int TM, int TN, int WM, int WN, int YT, bool GROUPED, bool EXACT>
+template <int TM, int TN, int WM, int WN, int S, int YT, bool GROUPED, bool EXACT>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(TileParams p) {
-    constexpr int kNW = (TM / WM) * (TN / WN);  // waves
-    constexpr int kI = WN / 16, kJ = WM / 16;   // a wave's tiles of weight rows and of x rows
-    constexpr int kRowsPerCopy = 8 * kNW;       // rows one copy instruction of all waves covers
-    constexpr int kCW = TN / kRowsPerCopy, kCX = TM / kRowsPerCopy;
-    __shared__ uint8_t sh[2][(TN + TM) * 128];
+    using Sh = TileShape<TM, TN, WM, WN, S>;
+    constexpr int kI = Sh::kI, kJ = Sh::kJ, kG = Sh::kG;
+    __shared__ __align__(16) uint8_t sh[S * Sh::kStage];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & 15, g = lane >> 4;
-    const int nb = (p.n + kBlock - 1) / kBlock;
+    const int nb = (p.n + kBlock - 1) / kBlock, nob = (p.out + kBlock - 1) / kBlock;
     const int ntn = (p.out + TN - 1) / TN;
 
     // which tile: the tiles of one XCD (workgroups b with equal b % 8) are neighbours
-    int e = 0;
+    int e = 0, n0;
     int64_t m0, count = p.M, begin = 0;
-    int n0;
     {
         const int64_t tiles_m = GROUPED ? p.tiles[p.E] : (p.M + TM - 1) / TM;
         const int64_t total = tiles_m * ntn, per = (total + 7) / 8;
@@ -81,9 +91,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
             while (span > 1) {
                 const int step = (span + 63) / 64;
                 const int c = lo + lane * step;
-                const uint64_t le = __ballot(c < lo + span && p.tiles[c < p.E ? c : p.E] <= t);
-                const int last = 63 - __builtin_clzll(le);
-                const int nlo = lo + last * step;
+                const uint64_t le = __ballot(c < lo + span && p.tiles[min(c, p.E)] <= t);
+                const int nlo = lo + (63 - __builtin_clzll(le)) * step;
                 span = min(step, lo + span - nlo);
                 lo = nlo;
             }
@@ -100,89 +109,79 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         }
     }
 
-    // copies: lane l of a copy moves slot l & 7 of row l >> 3 of its wave's
-    // eight rows; rows past the end repeat the last, their results are dropped
-    const int crow = wave * 8 + (lane >> 3);
-    const int nob = (p.out + kBlock - 1) / kBlock;
-    static_assert(kRowsPerCopy % 32 == 0, "a lane's chunk is the same in all of its copies");
-    const int wch = 16 * ((lane & 7) ^ wkey(crow)), xch = 16 * ((lane & 7) ^ xkey(crow));
-    // row i of the tile's x rows, as a row of p.x, and as a row of y
+    // row i of the tile's rows of x, as a row of p.x; rows past the last
+    // repeat it, their results are dropped
     auto pair_of = [&](int i) { return p.perm[begin + min(m0 + i, count - 1)]; };
     auto row_of = [&](int i) -> int64_t {
         if constexpr (GROUPED) return p.x_slots == 1 ? pair_of(i) / p.k : pair_of(i);
         else return min(m0 + i, count - 1);
     };
+
+    // copies: lane l of a copy moves slot l & 7 of row l >> 3 of its wave's eight rows
+    const int crow = wave * 8 + (lane >> 3);
+    static_assert(Sh::kRowsPerCopy % 32 == 0, "a lane's chunk is the same in all of its copies");
+    const int wch = 16 * ((lane & 7) ^ wkey<kG>(crow)), xch = 16 * ((lane & 7) ^ xkey(crow));
     const uint8_t* wbase = p.W + ((int64_t)e * p.out + n0) * p.n;
     const uint8_t* xbase = GROUPED ? p.x : p.x + m0 * p.n;  // (dense: offsets inside the tile fit 32 bits)
-    uint32_t woff[kCW], xoff[kCX];  // (grouped: xoff is the row of x, multiplied out at each copy)
+    uint32_t woff[Sh::kCW], xoff[Sh::kCX];                  // (grouped: xoff is the row of x, multiplied out at each copy)
 #pragma unroll
-    for (int c = 0; c < kCW; ++c)
-        woff[c] = (uint32_t)(min(c * kRowsPerCopy + crow, p.out - 1 - n0) * p.n + wch);
+    for (int c = 0; c < Sh::kCW; ++c)
+        woff[c] = (uint32_t)(min(c * Sh::kRowsPerCopy + crow, p.out - 1 - n0) * p.n + wch);
 #pragma unroll
-    for (int c = 0; c < kCX; ++c) {
-        const int64_t row = row_of(c * kRowsPerCopy + crow);
+    for (int c = 0; c < Sh::kCX; ++c) {
+        const int64_t row = row_of(min(c * Sh::kRowsPerCopy + crow, TM - 1));
         xoff[c] = GROUPED ? (uint32_t)row : (uint32_t)((int)(row - m0) * p.n + xch);
     }
-    auto copy_w = [&](int c, int k0, uint32_t d) { lds_copy16(wbase + k0, woff[c], d); };
-    auto copy_x = [&](int c, int k0, uint32_t d) {
-        if constexpr (GROUPED) lds_copy16(xbase + ((uint64_t)xoff[c] * (uint32_t)p.n + (uint32_t)(k0 + xch)), d);
-        else lds_copy16(xbase + k0, xoff[c], d);
+    auto xsrc = [&](int c, int k0) {
+        if constexpr (GROUPED) return xbase + ((uint64_t)xoff[c] * (uint32_t)p.n + (uint32_t)(k0 + xch));
+        else return xbase + k0 + xoff[c];
     };
-    const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&sh[0][0];
-    auto copy_block = [&](int b) {
+    // scales: of row u of x in lane u < TM of the workgroup, then of the tile's blocks of 128 weight rows
+    const float* sptr;
+    {
+        const int u = wave * 64 + lane;
+        if (u < TM) sptr = p.sx + row_of(u) * nb;
+        else sptr = p.sw + ((int64_t)e * nob + min(n0 / kBlock + min(u - TM, (TN + 127) / 128 - 1), nob - 1)) * nb;
+    }
+    const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)sh;
+    auto copy_block = [&](int b, int slot) {
         const int k0 = b * kBlock;
-        const uint32_t at = (b & 1) * (TN + TM) * 128 + wave * 1024;
+        const uint32_t at = sh0 + slot * Sh::kStage + wave * 1024;
         if (k0 + kBlock <= p.n) {
 #pragma unroll
-            for (int c = 0; c < kCW; ++c) copy_w(c, k0, sh0 + at + c * kRowsPerCopy * 128);
+            for (int c = 0; c < Sh::kCW; ++c) lds_copy16(wbase + k0, woff[c], at + c * Sh::kRowsPerCopy * 128);
 #pragma unroll
-            for (int c = 0; c < kCX; ++c) copy_x(c, k0, sh0 + at + (TN + c * kRowsPerCopy) * 128);
-        } else {  // the partial last block: chunks past the depth are zero
-#pragma unroll
-            for (int c = 0; c < kCW; ++c) {
-                const uint32_t d = at + c * kRowsPerCopy * 128;
-                if (k0 + wch < p.n) copy_w(c, k0, sh0 + d);
-                else *(uint4*)(&sh[0][0] + d + lane * 16) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < Sh::kCX; ++c) {
+                const uint32_t d = at + Sh::kX + c * Sh::kRowsPerCopy * 128;
+                if constexpr (GROUPED) lds_copy16(xsrc(c, k0), d);
+                else lds_copy16(xbase + k0, xoff[c], d);
             }
+        } else {  // the partial last block (as many instructions as any other: the waits count them)
 #pragma unroll
-            for (int c = 0; c < kCX; ++c) {
-                const uint32_t d = at + (TN + c * kRowsPerCopy) * 128;
-                if (k0 + xch < p.n) copy_x(c, k0, sh0 + d);
-                else *(uint4*)(&sh[0][0] + d + lane * 16) = make_uint4(0, 0, 0, 0);
-            }
+            for (int c = 0; c < Sh::kCW; ++c)
+                lds_copy16(k0 + wch < p.n ? wbase + k0 + woff[c] : (const uint8_t*)&g_zero, at + c * Sh::kRowsPerCopy * 128);
+#pragma unroll
+            for (int c = 0; c < Sh::kCX; ++c)
+                lds_copy16(k0 + xch < p.n ? xsrc(c, k0) : (const uint8_t*)&g_zero,
+                           at + Sh::kX + c * Sh::kRowsPerCopy * 128);
         }
+        lds_copy4(sptr + b, sh0 + slot * Sh::kStage + Sh::kScales + wave * 256);
     };
 
     const int wn = (wave % (TN / WN)) * WN, wm = (wave / (TN / WN)) * WM;  // this wave's part of the tile
-    // scales: one per 128 weight rows (a wave's rows lie in one block), one per row of x
-    const float* sw = p.sw + ((int64_t)e * nob + min((n0 + wn) / kBlock, nob - 1)) * nb;
-    // (a vector load: a scalar load in flight would make every wait for an LDS read a wait for all of them)
-    uint32_t swo = 0;
-    asm("" : "+v"(swo));
-    const float* sx = GROUPED ? p.sx : p.sx + m0 * nb;
-    uint32_t sxo[kJ];  // (grouped: the row of x)
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int64_t row = row_of(wm + 16 * j + li);
-        sxo[j] = GROUPED ? (uint32_t)row : (uint32_t)((row - m0) * nb);
-    }
-    auto x_scale = [&](int j, int b) {
-        if constexpr (GROUPED) return sx[(uint64_t)sxo[j] * (uint32_t)nb + (uint32_t)b];
-        else return sx[sxo[j] + (uint32_t)b];
-    };
-
+    const bool busy = m0 + wm < count;                                     // whether any of its rows of x is there
     f32x4 acc[kI][kJ];
 #pragma unroll
     for (int i = 0; i < kI; ++i)
 #pragma unroll
         for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // fragment rows: lane li of tile i reads weight row 64 (i / 4) + 16 (li / 4) + 4 (i % 4) + li % 4, so that a
-    // result lane's four rows of four neighbouring tiles are 16 consecutive rows
-    const int arow = wn + 16 * (li >> 2) + (li & 3);
-    const int brow = wm + li;
-    const int aoff = arow * 128 + 16 * (g ^ wkey(16 * (li >> 2) + (li & 3)));
-    const int boff = (TN + brow) * 128 + 16 * (g ^ xkey(li));
+    // lane li of tile i reads weight row 64 (i / 4) + 4 G (li / 4) + 4 (i % 4) + li % 4, so that a result lane's
+    // four rows of G neighbouring tiles are 4 G consecutive rows
+    const int afirst = 4 * kG * (li >> 2) + (li & 3);
+    const int aoff = (wn + afirst) * 128 + 16 * (g ^ wkey<kG>(afirst));
+    const int boff = Sh::kX + (wm + li) * 128 + 16 * (g ^ xkey(li));
+    const int soff = Sh::kScales + 4 * (wm + li), swoff = Sh::kScales + 4 * (TM + wn / kBlock);
     auto frag = [&](const uint8_t* s, int off) {
         const uint4 a = *(const uint4*)(s + off), b = *(const uint4*)(s + (off ^ 64));
         return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
@@ -190,10 +189,10 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
 
     // Instruction t = i kJ + j of a block multiplies tile row i by x tile j.  Its product is added to the sums two
     // instructions later (kLag: it is done by then), and a tile row is read kAhead rows before its first use.
-    constexpr int kAhead = GROUPED && TM * TN > 128 * 128 ? 1 : 2;  // (two would spill where rows are gathered)
+    constexpr int kAhead = kI < 4 ? 1 : (GROUPED && TM * TN > 128 * 128 ? 1 : 2);  // (two would spill there)
     constexpr int kLag = 2, kRing = 4, kT = kI * kJ;
-    static_assert(kT % kRing == 0, "a block's first products follow the last block's in the ring");
-    float sxn[kJ], swn, f[kJ], fp[kJ];
+    static_assert(EXACT || kT % kRing == 0, "a block's first products follow the last block's in the ring");
+    float f[kJ], fp[kJ];
     f32x4 d[kRing];
 #pragma unroll
     for (int j = 0; j < kJ; ++j) fp[j] = 0.f;
@@ -204,87 +203,91 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         for (int q = 0; q < 4; ++q)
             acc[t / kJ][t % kJ][q] = __builtin_fmaf(d[t % kRing][q], w[t % kJ], acc[t / kJ][t % kJ][q]);
     };
-copy_block(0);
+
+    constexpr int kBehind = (S - 2) * Sh::kCopies;  // copies that may still be on their way when a block is published
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) sxn[j] = x_scale(j, 0);
-    swn = sw[swo];
-    publish();
+    for (int b = 0; b < S - 1; ++b)
+        if (b < nb) copy_block(b, b);
+    if (nb >= S - 1) publish<kBehind>();
+    else publish<0>();
+    int slot = 0;
     for (int b = 0; b < nb; ++b) {
-        const uint8_t* cur = sh[b & 1];
+        const uint8_t* cur = sh + slot * Sh::kStage;
+        if (b + S - 1 < nb) copy_block(b + S - 1, slot == 0 ? S - 1 : slot - 1);
+        if (busy) {
+            // (tiles i and i + 4 are 64 rows apart, i and i + 1 four rows, which no bit of the key looks at)
+            auto afrag = [&](int i) { return frag(cur, aoff + (i >> 2) * 8192 + (i & 3) * 512); };
+            i32x8 af[kAhead + 1], bf[kJ];
+            af[0] = afrag(0);
+            bf[0] = frag(cur, boff);
+            const float fw = *(const float*)(cur + swoff);
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) f[j] = sxn[j] * swn;
-        if (b + 1 < nb) {
-            copy_block(b + 1);
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) sxn[j] = x_scale(j, b + 1);
-            swn = sw[swo + (b + 1)];
-        }
-        // (the key's bits are those of the row inside its 64: tile rows i and i + 4 are 64 rows apart, i and i + 1
-        // four rows, which no key bit looks at)
-        auto afrag = [&](int i) { return frag(cur, aoff + (i >> 2) * 8192 + (i & 3) * 512); };
-        i32x8 af[kAhead + 1], bf[kJ];
-        af[0] = afrag(0);
-        bf[0] = frag(cur, boff);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 1; j < kJ; ++j) {
-            bf[j] = frag(cur, boff + j * 2048);
+            for (int j = 0; j < kJ; ++j) f[j] = *(const float*)(cur + soff + 64 * j);
             __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (kAhead > 1) af[1] = afrag(1);
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (EXACT) {
-            f16x8 xw[kJ][4];
 #pragma unroll
-            for (int j = 0; j < kJ; ++j)
+            for (int j = 1; j < kJ; ++j) {
+                bf[j] = frag(cur, boff + j * 2048);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if constexpr (kAhead > 1) af[1] = afrag(1);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) xw[j][h] = widen(bf[j][2 * h], bf[j][2 * h + 1]);
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-                if (i + kAhead < kI) af[(i + kAhead) % (kAhead + 1)] = afrag(i + kAhead);
-                f16x8 ww[4];
-#pragma unroll
-                for (int h = 0; h < 4; ++h) ww[h] = widen(af[i % (kAhead + 1)][2 * h], af[i % (kAhead + 1)][2 * h + 1]);
-                f32x4 r[kJ];
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) r[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int h = 0; h < 4; ++h)
-#pragma unroll
-                    for (int j = 0; j < kJ; ++j) r[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ww[h], xw[j][h], r[j], 0, 0, 0);
+            for (int j = 0; j < kJ; ++j) f[j] *= fw;
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (EXACT) {
+                f16x8 xw[kJ][4];
 #pragma unroll
                 for (int j = 0; j < kJ; ++j)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(r[j][q], f[j], acc[i][j][q]);
-            }
-        } else {
+                    for (int h = 0; h < 4; ++h) xw[j][h] = widen(bf[j][2 * h], bf[j][2 * h + 1]);
 #pragma unroll
-            for (int i = 0; i < kI; ++i) {
-                if (i + kAhead < kI) af[(i + kAhead) % (kAhead + 1)] = afrag(i + kAhead);
+                for (int i = 0; i < kI; ++i) {
+                    if (i + kAhead < kI) af[(i + kAhead) % (kAhead + 1)] = afrag(i + kAhead);
+                    f16x8 ww[4];
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) {
-                    const int t = i * kJ + j;
-                    const f32x4 r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        af[i % (kAhead + 1)], bf[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (t >= kLag) add(t - kLag, f);
-                    else add(kT - kLag + t, fp);
-                    d[t % kRing] = r;
-                    __builtin_amdgcn_sched_barrier(0);
+                    for (int h = 0; h < 4; ++h) ww[h] = widen(af[i % (kAhead + 1)][2 * h], af[i % (kAhead + 1)][2 * h + 1]);
+                    f32x4 r[kJ];
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) r[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int j = 0; j < kJ; ++j) r[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ww[h], xw[j][h], r[j], 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(r[j][q], f[j], acc[i][j][q]);
                 }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kI; ++i) {
+                    if (i + kAhead < kI) af[(i + kAhead) % (kAhead + 1)] = afrag(i + kAhead);
+#pragma unroll
+                    for (int j = 0; j < kJ; ++j) {
+                        const int t = i * kJ + j;
+                        const f32x4 r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            af[i % (kAhead + 1)], bf[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (t >= kLag) add(t - kLag, f);
+                        else add(kT - kLag + t, fp);
+                        d[t % kRing] = r;
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) fp[j] = f[j];
             }
         }
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) fp[j] = f[j];
-        publish();
+        if (b + S - 1 < nb) publish<kBehind>();
+        else publish<0>();
+        slot = slot == S - 1 ? 0 : slot + 1;
     }
     if constexpr (!EXACT) {
 #pragma unroll
         for (int t = kT - kLag; t < kT; ++t) add(t, fp);
     }
 
-    // result lane (li, g) holds, of x row 16 j + li, weight rows 64 (i / 4) + 16 g + 4 (i % 4) + q
-    const bool whole = (p.out & 15) == 0 && ((uintptr_t)p.y & 15) == 0;
+    // result lane (li, g) holds, of row 16 j + li of x, weight rows 64 h + 4 G g + 4 i + q of its wave's
+    const bool whole = (p.out & 7) == 0 && ((uintptr_t)p.y & 15) == 0;
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
         const int i = wm + 16 * j + li;
@@ -292,50 +295,76 @@ copy_block(0);
         int64_t yrow = m0 + i;
         if constexpr (GROUPED) yrow = pair_of(i);
 #pragma unroll
-        for (int h = 0; h < kI / 4; ++h) {
-            const int o = n0 + wn + 64 * h + 16 * g;
-            if (o >= p.out) continue;
-            float v[16];
+        for (int h = 0; h < kI / kG; ++h) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) v[q] = acc[4 * h + (q >> 2)][j][q & 3];
-            store16<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
+            for (int u = 0; u < kG / 2; ++u) {
+                const int o = n0 + wn + 64 * h + 4 * kG * g + 8 * u;
+                if (o >= p.out) continue;
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = acc[4 * h + 2 * u + (q >> 2)][j][q & 3];
+                store8<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
+            }
         }
     }
 }
 
-// TM x TN tiles by waves of WM x WN
-template <int TM, int TN, int WM, int WN, bool EXACT>
-void tile_launch(const Fp8Launch& a, hipStream_t s) {
+// TM x TN tiles by waves of WM x WN, S stages
+template <int TM, int TN, int WM, int WN, int S, bool EXACT, int YT, bool GROUPED>
+hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
+    using Sh = TileShape<TM, TN, WM, WN, S>;
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
                        (int)a.E, a.offsets, a.perm, a.tiles, a.y};
     // (grouped: each expert's last tile may be partial)
-    const int64_t tiles = (a.M + TM - 1) / TM + (a.offsets ? std::min<int64_t>(a.E, a.M) : 0);
+    const int64_t tiles = (a.M + TM - 1) / TM + (GROUPED ? std::min<int64_t>(a.E, a.M) : 0);
     const int64_t total = tiles * ((a.out + TN - 1) / TN);
-    const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * (TM / WM) * (TN / WN));
-    by_float(a.y_dtype, [&](auto yt) {
-        constexpr int YT = decltype(yt)::value;
-        if constexpr ((YT == IQK_F32) == EXACT) {
-            if (a.offsets) hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, YT, true, EXACT>), grid, block, 0, s, p);
-            else hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, YT, false, EXACT>), grid, block, 0, s, p);
-        }
-    });
+    hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT>), dim3((unsigned)((total + 7) / 8 * 8)),
+                       dim3(64 * Sh::kWaves), 0, s, p);
+    return hipGetLastError();
+}
+
+template <int YT, bool GROUPED>
+hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
+    constexpr bool F32 = YT == IQK_F32;
+    if constexpr (GROUPED) {
+        // few rows per expert: the weights stream through, exact sums cost nothing there
+        if (tile == 16) return tile_launch<16, 128, 16, 32, 4, true, YT, true>(a, s);
+        if (tile == 32) return tile_launch<32, 128, 32, 32, 4, true, YT, true>(a, s);
+        if (tile == 64) return tile_launch<64, 128, 32, 64, 2, true, YT, true>(a, s);
+    } else {
+        if (tile == 64) return tile_launch<64, 64, 32, 32, 4, F32, YT, false>(a, s);
+    }
+    if constexpr (!F32) {
+        if (tile == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, GROUPED>(a, s);
+    }
+    return tile_launch<128, 128, 64, 64, 2, F32, YT, GROUPED>(a, s);
 }
 
 }  // namespace
 
-int fp8_tile_rows(int64_t rows_per_expert, int64_t M, int64_t out, bool exact) {
-    if (exact) return 128;
-    // 256 x 256 tiles move half the bytes per product that 128 x 128 ones do;
-    // they are taken where they fill most of the 256 CUs and most of themselves
-    const bool fill = (M + 255) / 256 * ((out + 255) / 256) >= 160;
-    return fill && rows_per_expert >= 192 ? 256 : 128;
+int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact) {
+    auto count = [&](int64_t t) { return (M + t - 1) / t * ((out + t - 1) / t); };
+    if (grouped) {
+        // rows a tile holds: what most experts have (their counts spread like a square root)
+        const double most = rows_per_expert + 2.0 * std::sqrt(rows_per_expert);
+        if (most <= 16) return 16;
+        if (most <= 32) return 32;
+        if (most <= 64) return 64;
+        return !exact && rows_per_expert >= 192 && count(256) >= 160 ? 256 : 128;
+    }
+    // 256 x 256 tiles move half the bytes per product that 128 x 128 ones do, and those half of what 64 x 64 do;
+    // the largest is taken that gives most of the 256 CUs a tile
+    if (!exact && count(256) >= 160) return 256;
+    return count(128) >= 160 ? 128 : 64;
 }
 
 hipError_t launch_fp8_tile(const Fp8Launch& a, int tile, hipStream_t s) {
-    if (a.y_dtype == IQK_F32) tile_launch<128, 128, 64, 64, true>(a, s);
-    else if (tile == 256) tile_launch<256, 256, 64, 128, false>(a, s);
-    else tile_launch<128, 128, 64, 64, false>(a, s);
-    return hipGetLastError();
+    hipError_t e = hipSuccess;
+    by_float(a.y_dtype, [&](auto yt) {
+        constexpr int YT = decltype(yt)::value;
+        e = a.offsets ? tile_choose<YT, true>(a, tile, s) : tile_choose<YT, false>(a, tile, s);
+    });
+    return e;
 }
 
 }  // namespace iqk

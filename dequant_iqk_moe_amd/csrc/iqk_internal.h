@@ -164,7 +164,7 @@ hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s);
 // e4m3 x: 16 * min(passes16, 4) rows in a pass over the weights
 hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s);
 // e4m3 x, many rows; tile = fp8_tile_rows()
-int fp8_tile_rows(int64_t rows_per_expert, int64_t M, int64_t out, bool exact);
+int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact);
 hipError_t launch_fp8_tile(const Fp8Launch& a, int tile, hipStream_t s);
 
 hipError_t launch_dequant(const DequantLaunch& a, bool floor_variant, hipStream_t s);

@@ -90,9 +90,6 @@ size_t quantized_bytes(int64_t rows, int64_t n) {
 // Rows of x up to which the dense product passes over the weights once
 // without tiles.
 constexpr int64_t kRowsPass = 64;
-// Rows per expert up to which the routed product does.
-constexpr double kGroupedRows = 48;
-
 // Whether the routed product takes each pair by itself: no grouping, one
 // launch, an expert's weights read once for each of its pairs.
 bool pair_by_pair(int64_t P, int64_t E, int64_t n) {
@@ -191,7 +188,7 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
         if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace, s)) != hipSuccess)
             return hip_fail(e, "quantize launch");
         e = M <= kRowsPass ? iqk::launch_fp8_rows(L, (int)((M + 15) / 16), s)
-                           : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows(M, M, w->out, y_dtype == IQK_F32), s);
+                           : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows((double)M, M, w->out, false, y_dtype == IQK_F32), s);
     }
     if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
     return ok();
@@ -241,8 +238,7 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
         return at;
     };
     const double per_expert = (double)P / (double)E;
-    const bool tiled = per_expert > kGroupedRows;
-    const int tile = iqk::fp8_tile_rows((int64_t)per_expert, P, w->out, y_dtype == IQK_F32);
+    const int tile = iqk::fp8_tile_rows(per_expert, P, w->out, true, y_dtype == IQK_F32);
     iqk::Fp8GroupLaunch G{};
     G.ids = ids;
     G.P = P;
@@ -268,13 +264,7 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
     L.offsets = G.offsets;
     L.perm = G.perm;
     L.tiles = G.tiles;
-    if (tiled) {
-        e = iqk::launch_fp8_tile(L, tile, s);
-    } else {
-        // rows a pass holds: what most experts have (their counts spread like a square root)
-        const int passes = (int)std::ceil((per_expert + 2.0 * std::sqrt(per_expert)) / 16.0);
-        e = iqk::launch_fp8_rows(L, passes, s);
-    }
+    e = iqk::launch_fp8_tile(L, tile, s);
     if (e != hipSuccess) return hip_fail(e, "8-bit grouped product launch");
     return ok();
 }
