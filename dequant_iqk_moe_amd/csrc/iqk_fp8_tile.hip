@@ -34,6 +34,7 @@ struct TileParams {
     const float* sx;
     int64_t M;
     int out, n, k, x_slots, E;
+    int run;  // weight tiles a workgroup takes one after the other
     const int32_t *offsets, *perm, *tiles;  // grouped: tiles[e] = TM-row tiles of x before expert e
     void* y;
 };
@@ -73,19 +74,19 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & 15, g = lane >> 4;
     const int nb = (p.n + kBlock - 1) / kBlock, nob = (p.out + kBlock - 1) / kBlock;
-    const int ntn = (p.out + TN - 1) / TN;
+    const int ntn = (p.out + TN - 1) / TN, runs = (ntn + p.run - 1) / p.run;
 
-    // which tile: the tiles of one XCD (workgroups b with equal b % 8) are neighbours
+    // which tile of x and run of weight tiles: those of one XCD (workgroups b with equal b % 8) are neighbours
     int e = 0, n0;
     int64_t m0, count = p.M, begin = 0;
     {
         const int64_t tiles_m = GROUPED ? p.tiles[p.E] : (p.M + TM - 1) / TM;
-        const int64_t total = tiles_m * ntn, per = (total + 7) / 8;
+        const int64_t total = tiles_m * runs, per = (total + 7) / 8;
         const int64_t id = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
         if ((int64_t)(blockIdx.x >> 3) >= per || id >= total) return;
         if constexpr (GROUPED) {
-            const int t = (int)(id / ntn);
-            n0 = (int)(id - (int64_t)t * ntn) * TN;
+            const int t = (int)(id / runs);
+            n0 = (int)(id - (int64_t)t * runs) * p.run * TN;
             // the expert of tile t: the last e with tiles[e] <= t, 64 candidates at a time
             int lo = 0, span = p.E;
             while (span > 1) {
@@ -101,11 +102,11 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
             count = p.offsets[e + 1] - begin;
             m0 = (int64_t)(t - p.tiles[e]) * TM;
         } else {
-            // bands of 8 tiles of x by all of the weights' tiles
-            const int64_t band = id / (8 * ntn), in = id - band * 8 * ntn;
+            // bands of 8 tiles of x by all of the weights' runs
+            const int64_t band = id / (8 * runs), in = id - band * 8 * runs;
             const int64_t rows = min((int64_t)8, tiles_m - band * 8);
             m0 = (band * 8 + in % rows) * TM;
-            n0 = (int)(in / rows) * TN;
+            n0 = (int)(in / rows) * p.run * TN;
         }
     }
 
@@ -121,12 +122,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     const int crow = wave * 8 + (lane >> 3);
     static_assert(Sh::kRowsPerCopy % 32 == 0, "a lane's chunk is the same in all of its copies");
     const int wch = 16 * ((lane & 7) ^ wkey<kG>(crow)), xch = 16 * ((lane & 7) ^ xkey(crow));
-    const uint8_t* wbase = p.W + ((int64_t)e * p.out + n0) * p.n;
     const uint8_t* xbase = GROUPED ? p.x : p.x + m0 * p.n;  // (dense: offsets inside the tile fit 32 bits)
     uint32_t woff[Sh::kCW], xoff[Sh::kCX];                  // (grouped: xoff is the row of x, multiplied out at each copy)
-#pragma unroll
-    for (int c = 0; c < Sh::kCW; ++c)
-        woff[c] = (uint32_t)(min(c * Sh::kRowsPerCopy + crow, p.out - 1 - n0) * p.n + wch);
 #pragma unroll
     for (int c = 0; c < Sh::kCX; ++c) {
         const int64_t row = row_of(min(c * Sh::kRowsPerCopy + crow, TM - 1));
@@ -137,15 +134,23 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         else return xbase + k0 + xoff[c];
     };
     // scales: of row u of x in lane u < TM of the workgroup, then of the tile's blocks of 128 weight rows
-    const float* sptr;
-    {
-        const int u = wave * 64 + lane;
-        if (u < TM) sptr = p.sx + row_of(u) * nb;
-        else sptr = p.sw + ((int64_t)e * nob + min(n0 / kBlock + min(u - TM, (TN + 127) / 128 - 1), nob - 1)) * nb;
-    }
+    const int su = wave * 64 + lane;
+    const float* sptr = p.sx + row_of(min(su, TM - 1)) * nb;
+    // the next block to copy: block cb of the weight tile at row cn
+    int cb = 0, cn = n0;
+    const uint8_t* wbase;
+    auto weight_tile = [&]() {
+        wbase = p.W + ((int64_t)e * p.out + cn) * p.n;
+#pragma unroll
+        for (int c = 0; c < Sh::kCW; ++c)
+            woff[c] = (uint32_t)(min(c * Sh::kRowsPerCopy + crow, p.out - 1 - cn) * p.n + wch);
+        if (su >= TM)
+            sptr = p.sw + ((int64_t)e * nob + min(cn / kBlock + min(su - TM, (TN + 127) / 128 - 1), nob - 1)) * nb;
+    };
+    weight_tile();
     const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)sh;
-    auto copy_block = [&](int b, int slot) {
-        const int k0 = b * kBlock;
+    auto copy_next = [&](int slot) {
+        const int k0 = cb * kBlock;
         const uint32_t at = sh0 + slot * Sh::kStage + wave * 1024;
         if (k0 + kBlock <= p.n) {
 #pragma unroll
@@ -165,7 +170,12 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
                 lds_copy16(k0 + xch < p.n ? xsrc(c, k0) : (const uint8_t*)&g_zero,
                            at + Sh::kX + c * Sh::kRowsPerCopy * 128);
         }
-        lds_copy4(sptr + b, sh0 + slot * Sh::kStage + Sh::kScales + wave * 256);
+        lds_copy4(sptr + cb, sh0 + slot * Sh::kStage + Sh::kScales + wave * 256);
+        if (++cb == nb) {
+            cb = 0;
+            cn += TN;
+            if (cn < p.out) weight_tile();
+        }
     };
 
     const int wn = (wave % (TN / WN)) * WN, wm = (wave / (TN / WN)) * WM;  // this wave's part of the tile
@@ -187,6 +197,30 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
     };
 
+    // result lane (li, g) holds, of row 16 j + li of x, weight rows 64 h + 4 G g + 4 i + q of its wave's
+    const bool whole = (p.out & 7) == 0 && ((uintptr_t)p.y & 15) == 0;
+    auto store_tile = [&]() {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int i = wm + 16 * j + li;
+            if (m0 + i >= count) continue;
+            int64_t yrow = m0 + i;
+            if constexpr (GROUPED) yrow = pair_of(i);
+#pragma unroll
+            for (int h = 0; h < kI / kG; ++h) {
+#pragma unroll
+                for (int u = 0; u < kG / 2; ++u) {
+                    const int o = n0 + wn + 64 * h + 4 * kG * g + 8 * u;
+                    if (o >= p.out) continue;
+                    float v[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = acc[4 * h + 2 * u + (q >> 2)][j][q & 3];
+                    store8<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
+                }
+            }
+        }
+    };
+
     // Instruction t = i kJ + j of a block multiplies tile row i by x tile j.  Its product is added to the sums two
     // instructions later (kLag: it is done by then), and a tile row is read kAhead rows before its first use.
     constexpr int kAhead = kI < 4 ? 1 : (GROUPED && TM * TN > 128 * 128 ? 1 : 2);  // (two would spill there)
@@ -205,15 +239,16 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     };
 
     constexpr int kBehind = (S - 2) * Sh::kCopies;  // copies that may still be on their way when a block is published
+    const int steps = nb * min(p.run, (p.out - n0 + TN - 1) / TN);
 #pragma unroll
     for (int b = 0; b < S - 1; ++b)
-        if (b < nb) copy_block(b, b);
-    if (nb >= S - 1) publish<kBehind>();
+        if (b < steps) copy_next(b);
+    if (steps >= S - 1) publish<kBehind>();
     else publish<0>();
-    int slot = 0;
-    for (int b = 0; b < nb; ++b) {
+    int slot = 0, b = 0;  // b: block of the tile that is being multiplied
+    for (int step = 0; step < steps; ++step) {
         const uint8_t* cur = sh + slot * Sh::kStage;
-        if (b + S - 1 < nb) copy_block(b + S - 1, slot == 0 ? S - 1 : slot - 1);
+        if (step + S - 1 < steps) copy_next(slot == 0 ? S - 1 : slot - 1);
         if (busy) {
             // (tiles i and i + 4 are 64 rows apart, i and i + 1 four rows, which no bit of the key looks at)
             auto afrag = [&](int i) { return frag(cur, aoff + (i >> 2) * 8192 + (i & 3) * 512); };
@@ -277,47 +312,45 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
                 for (int j = 0; j < kJ; ++j) fp[j] = f[j];
             }
         }
-        if (b + S - 1 < nb) publish<kBehind>();
+        if (step + S - 1 < steps) publish<kBehind>();
         else publish<0>();
         slot = slot == S - 1 ? 0 : slot + 1;
-    }
-    if constexpr (!EXACT) {
+        if (++b == nb) {  // (after the wait, so that the stores are on their way while the next block is multiplied)
+            if constexpr (!EXACT) {
 #pragma unroll
-        for (int t = kT - kLag; t < kT; ++t) add(t, fp);
-    }
-
-    // result lane (li, g) holds, of row 16 j + li of x, weight rows 64 h + 4 G g + 4 i + q of its wave's
-    const bool whole = (p.out & 7) == 0 && ((uintptr_t)p.y & 15) == 0;
+                for (int t = kT - kLag; t < kT; ++t) add(t, fp);
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int i = wm + 16 * j + li;
-        if (m0 + i >= count) continue;
-        int64_t yrow = m0 + i;
-        if constexpr (GROUPED) yrow = pair_of(i);
-#pragma unroll
-        for (int h = 0; h < kI / kG; ++h) {
-#pragma unroll
-            for (int u = 0; u < kG / 2; ++u) {
-                const int o = n0 + wn + 64 * h + 4 * kG * g + 8 * u;
-                if (o >= p.out) continue;
-                float v[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = acc[4 * h + 2 * u + (q >> 2)][j][q & 3];
-                store8<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
+                for (int t = 0; t < kRing; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
+            store_tile();
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            b = 0;
+            n0 += TN;
         }
     }
 }
+
+constexpr int64_t kMaxRun = 2;
 
 // TM x TN tiles by waves of WM x WN, S stages
 template <int TM, int TN, int WM, int WN, int S, bool EXACT, int YT, bool GROUPED>
 hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     using Sh = TileShape<TM, TN, WM, WN, S>;
+    const int64_t ntn = (a.out + TN - 1) / TN;
+    const int64_t tiles = (a.M + TM - 1) / TM + (GROUPED ? std::min<int64_t>(a.E, a.M) : 0);  // (partial last tiles)
+    // A workgroup's first blocks arrive a memory latency after it starts and its results leave while nothing else
+    // of it runs, so it takes two weight tiles in a run where the runs fill the card as evenly as tiles do (four and eight
+    // measured no faster: their last turn is emptier).
+    constexpr int64_t kResident = 256 * std::min(2, 160 * 1024 / (S * Sh::kStage));
+    auto turns = [&](int64_t run) { return (tiles * ((ntn + run - 1) / run) + kResident - 1) / kResident * run; };
+    int64_t run = 1;
+    while (run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
-                       (int)a.E, a.offsets, a.perm, a.tiles, a.y};
-    // (grouped: each expert's last tile may be partial)
-    const int64_t tiles = (a.M + TM - 1) / TM + (GROUPED ? std::min<int64_t>(a.E, a.M) : 0);
-    const int64_t total = tiles * ((a.out + TN - 1) / TN);
+                       (int)a.E, (int)run, a.offsets, a.perm, a.tiles, a.y};
+    const int64_t total = tiles * ((ntn + run - 1) / run);
     hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT>), dim3((unsigned)((total + 7) / 8 * 8)),
                        dim3(64 * Sh::kWaves), 0, s, p);
     return hipGetLastError();
@@ -329,7 +362,7 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
     if constexpr (GROUPED) {
         // few rows per expert: the weights stream through, exact sums cost nothing there
         if (tile == 16) return tile_launch<16, 128, 16, 32, 4, true, YT, true>(a, s);
-        if (tile == 32) return tile_launch<32, 128, 32, 32, 4, true, YT, true>(a, s);
+        if (tile == 32) return tile_launch<32, 128, 32, 32, 3, true, YT, true>(a, s);
         if (tile == 64) return tile_launch<64, 128, 32, 64, 2, true, YT, true>(a, s);
     } else {
         if (tile == 64) return tile_launch<64, 64, 32, 32, 4, F32, YT, false>(a, s);
