@@ -99,6 +99,7 @@ struct RouterLaunch {
     float scale;
     int32_t* ids;    // [T, k]
     float* weights;  // [T, k]
+    bool wide = false, lane_groups = false;  // set by the launch
 };
 
 struct RouterGradLaunch {

@@ -162,7 +162,7 @@ int iqk_fp8_linear_workspace(const iqk_fp8_weights* w, int64_t M, size_t* bytes)
     int rc = check_fp8_shape(w);
     if (rc) return rc;
     if (M < 0 || M > kMaxRows) return fail(IQK_E_ARG, "M = %lld outside [0, 2^24]", (long long)M);
-    *bytes = quantized_bytes(M, w->in);
+    *bytes = iqk::fp8_few_fits(M, w->in) ? 0 : quantized_bytes(M, w->in);
     return ok();
 }
 
@@ -176,13 +176,14 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
     rc = check_fp8_io(x, x_dtype, x_scales, y, y_dtype);
     if (rc) return rc;
     const bool quantize = x_dtype != IQK_E4M3;
-    rc = check_workspace(workspace, ws_bytes, quantize ? quantized_bytes(M, w->in) : 0);
+    const bool few = iqk::fp8_few_fits(M, w->in);
+    rc = check_workspace(workspace, ws_bytes, quantize && !few ? quantized_bytes(M, w->in) : 0);
     if (rc) return rc;
     hipStream_t s = (hipStream_t)stream;
     iqk::Fp8Launch L{1, w->out, w->in, (const uint8_t*)w->codes, w->scales, x, x_dtype, x_scales, M, 1, 1,
                      nullptr, nullptr, nullptr, nullptr, y, y_dtype};
     hipError_t e;
-    if (iqk::fp8_few_fits(M, w->in)) {
+    if (few) {
         e = iqk::launch_fp8_few(L, s);
     } else {
         if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace, s)) != hipSuccess)
@@ -201,6 +202,10 @@ int iqk_moe_fp8_workspace(const iqk_fp8_weights* w, int64_t T, int k, int x_slot
     if (T < 0 || k <= 0 || T > kMaxRows / k) return fail(IQK_E_ARG, "T * k must lie in [0, 2^24]");
     if (x_slots != 1 && x_slots != k) return fail(IQK_E_ARG, "x_slots must be 1 or k");
     const size_t E = (size_t)w->experts, P = (size_t)std::max<int64_t>(T * k, 1);
+    if (pair_by_pair(T * k, w->experts, w->in)) {
+        *bytes = 0;
+        return ok();
+    }
     *bytes = round256(E * 4) + 2 * round256((E + 1) * 4) + round256(P * 4) +
              round256((size_t)iqk::fp8_group_slices(P) * E * 4) + quantized_bytes(T * x_slots, w->in);
     return ok();

@@ -14,49 +14,77 @@
 //   ids = the k largest c of the groups that stay, equal c in favour of the
 //         lowest id; w_j = scale * s_j / D, D = the sum of the chosen s or 1
 //
-// One wave owns one token: expert v * 64 + lane is register v of a lane, so
-// the row is loaded and the gradient stored 64 consecutive values at a time,
-// and a selection step is one wave-wide maximum (DPP) and one ballot per
-// register, whose first set bit is the lowest id.  No LDS, no barrier.  All
-// arithmetic is float32.
+// A row of L lanes owns one token, L = 64 (few tokens: the shortest chain) or 16
+// (many: four tokens per wave, whose instructions then do four tokens' work).
+// Lane i of it holds the V consecutive experts from i V, so its loads are wide,
+// the lowest id among equals is the lowest lane's, and a group is a number of
+// whole lanes.  Each lane keeps its own best; a selection step is a maximum
+// over the row (DPP), one ballot, and a new best in the lane that won.  Scores
+// are computed only for the experts whose score something needs: a choice by
+// logits with weights divided by their sum needs those of the chosen alone.
+// No LDS, no barrier; all arithmetic is float32.  Bound: vector instructions
+// (about 45 per token and slot with L = 16, V = 16), not bytes.
 #include "iqk_internal.h"
 
 namespace iqk {
 namespace {
 
-constexpr int kRouterWaves = 4;  // waves (tokens) per workgroup
+constexpr int kRouterWaves = 4;          // waves per workgroup
+constexpr int64_t kManyTokens = 8192;    // tokens from which rows of 16 lanes are taken
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Maximum and sum over the 64 lanes of a wave, the result in every lane.  The
-// first four steps rotate within rows of 16 lanes, the last two broadcast a
-// row's last lane to the rows after it; lane 63 then holds the result.
+// Maximum and sum over a row of L = 16 or 64 lanes, the result in every lane.
+// Four rotations within rows of 16 lanes; for 64, two broadcasts of a row's
+// last lane to the rows after it, after which lane 63 holds the result.
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ float dpp_or(float v, float otherwise) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(__float_as_uint(otherwise), __float_as_uint(v), CTRL, ROW_MASK,
                                                        0xF, false));
 }
-__device__ __forceinline__ float wave_max(float v) {
-    v = fmaxf(v, dpp_or<0x128, 0xF>(v, v));  // row_ror:8
-    v = fmaxf(v, dpp_or<0x124, 0xF>(v, v));  // row_ror:4
-    v = fmaxf(v, dpp_or<0x122, 0xF>(v, v));  // row_ror:2
-    v = fmaxf(v, dpp_or<0x121, 0xF>(v, v));  // row_ror:1
-    v = fmaxf(v, dpp_or<0x142, 0xA>(v, v));  // row_bcast:15 into rows 1 and 3
-    v = fmaxf(v, dpp_or<0x143, 0xC>(v, v));  // row_bcast:31 into rows 2 and 3
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return dpp_or<CTRL, 0xF>(v, v);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    v += dpp_or<0x128, 0xF>(v, 0.f);
-    v += dpp_or<0x124, 0xF>(v, 0.f);
-    v += dpp_or<0x122, 0xF>(v, 0.f);
-    v += dpp_or<0x121, 0xF>(v, 0.f);
-    v += dpp_or<0x142, 0xA>(v, 0.f);
-    v += dpp_or<0x143, 0xC>(v, 0.f);
-    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
-}
+constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128, kBcast15 = 0x142, kBcast31 = 0x143;
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;  // quad permutes, mirrors of 8 and 16
 __device__ __forceinline__ float lane_value(float v, int lane) {
     return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
 }
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, dpp<kRor8>(v));
+    v = fmaxf(v, dpp<kRor4>(v));
+    v = fmaxf(v, dpp<kRor2>(v));
+    v = fmaxf(v, dpp<kRor1>(v));
+    if constexpr (L == 64) {
+        v = fmaxf(v, dpp_or<kBcast15, 0xA>(v, v));
+        v = fmaxf(v, dpp_or<kBcast31, 0xC>(v, v));
+        v = lane_value(v, 63);
+    }
+    return v;
+}
+template <int L>
+__device__ __forceinline__ float row_sum(float v) {
+    v += dpp<kRor8>(v);
+    v += dpp<kRor4>(v);
+    v += dpp<kRor2>(v);
+    v += dpp<kRor1>(v);
+    if constexpr (L == 64) {
+        v += dpp_or<kBcast15, 0xA>(v, 0.f);
+        v += dpp_or<kBcast31, 0xC>(v, 0.f);
+        v = lane_value(v, 63);
+    }
+    return v;
+}
+// The ballot bits of this lane's row, from bit 0.
+template <int L>
+__device__ __forceinline__ uint64_t row_bits(uint64_t ballot, int lane) {
+    if constexpr (L == 64) return ballot;
+    else return (uint32_t)(ballot >> (lane & 48)) & 0xFFFFu;
+}
+__device__ __forceinline__ float wave_max(float v) { return row_max<64>(v); }
+__device__ __forceinline__ float wave_sum(float v) { return row_sum<64>(v); }
 
 template <int DT>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
@@ -76,149 +104,221 @@ __device__ __forceinline__ void store_logit(void* p, int64_t i, float v) {
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Largest of the V registers of all lanes and where it first stands.  `m` is
-// -inf when nothing is left.
-template <int V>
-__device__ __forceinline__ float wave_best(const float (&c)[V], int* reg, int* lane) {
-    float m = c[0];
+// V consecutive logits from element i, of which `left` are inside the row;
+// the others read -inf.  `wide`: rows are multiples of 16 bytes, so aligned
+// words of at most 16 bytes are all inside or all outside.
+template <int V, int DT>
+__device__ __forceinline__ void load_logits(const void* p, int64_t i, int left, bool wide, float (&l)[V]) {
+    constexpr int kSize = DT == IQK_F32 ? 4 : 2;
+    constexpr int kWord = V * kSize < 16 ? V * kSize : 16, kPer = kWord / kSize;
 #pragma unroll
-    for (int v = 1; v < V; ++v) m = fmaxf(m, c[v]);
-    m = wave_max(m);
-    *reg = V;
-    *lane = 0;
+    for (int v = 0; v < V; ++v) l[v] = neg_inf();
+    if constexpr (kWord >= 4) {
+        if (wide) {
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) {
-        const uint64_t b = __ballot(c[v] == m);
-        if (b) {
-            *reg = v;
-            *lane = __builtin_ctzll(b);
+            for (int c = 0; c < V; c += kPer) {
+                if (c >= left) continue;
+                uint32_t w[kWord / 4];
+                __builtin_memcpy(w, __builtin_assume_aligned((const char*)p + (i + c) * kSize, kWord), kWord);
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    if constexpr (DT == IQK_F32) l[c + u] = __uint_as_float(w[u]);
+                    if constexpr (DT == IQK_BF16) l[c + u] = __uint_as_float(u & 1 ? w[u / 2] & 0xFFFF0000u : w[u / 2] << 16);
+                    if constexpr (DT == IQK_F16) l[c + u] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[u / 2] >> (16 * (u & 1))));
+                }
+            }
+            return;
         }
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (v < left) l[v] = load_logit<DT>(p, i + v);
+}
+
+// The lane's best value and where it first stands.
+template <int V>
+__device__ __forceinline__ float lane_best(const float (&c)[V], int* at) {
+    float m = c[0];
+    int i = 0;
+#pragma unroll
+    for (int v = 1; v < V; ++v) {
+        const bool more = c[v] > m;
+        m = more ? c[v] : m;
+        i = more ? v : i;
+    }
+    *at = i;
     return m;
 }
 
-template <int V, int DT>
+template <int L, int V, int DT>
 __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterLaunch p) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * kRouterWaves + (threadIdx.x >> 6);
-    if (t >= p.T) return;
-    const int E = p.E;
+    const int lane = threadIdx.x & 63, sub = lane & (L - 1);
+    const int64_t row = ((int64_t)blockIdx.x * (64 * kRouterWaves) + threadIdx.x) / L;
+    const bool there = row < p.T;  // (a wave's rows past the last work on a copy of it and write nothing)
+    const int64_t t = there ? row : p.T - 1;
+    const int E = p.E, e0 = sub * V, left = E - e0;
+    const bool softmax = p.scoring == IQK_SOFTMAX;
     float l[V], s[V], c[V];
+    load_logits<V, DT>(p.logits, t * E + e0, left, p.wide, l);
     bool bad = false;  // a NaN, or an infinite logit under softmax
     float top = neg_inf();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = v * 64 + lane;
-        l[v] = e < E ? load_logit<DT>(p.logits, t * E + e) : neg_inf();
-        c[v] = p.bias && e < E ? p.bias[e] : 0.f;
-        bad |= l[v] != l[v] || c[v] != c[v] || (p.scoring == IQK_SOFTMAX && l[v] == __builtin_inff());
+        bad |= l[v] != l[v] || (softmax && l[v] == __builtin_inff());
         top = fmaxf(top, l[v]);
+        c[v] = l[v];
     }
-    if (__ballot(bad)) {
-        if (lane < p.k) {
-            p.ids[t * p.k + lane] = -1;
-            p.weights[t * p.k + lane] = __builtin_nanf("");
-        }
-        return;
-    }
+    // scores of all experts, where the choice or the weights need them
+    const bool two = p.n_group > 1 && p.group_top == 2;
     float total = 1.f;
-    if (p.scoring == IQK_SOFTMAX) {
-        top = wave_max(top);
-        float sum = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            s[v] = l[v] == neg_inf() ? 0.f : expf(l[v] - top);
-            sum += s[v];
-        }
-        total = wave_sum(sum);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = sigmoid(l[v]);
-    }
-    // what the choice goes by; an expert whose logit or bias is -inf is out (c = -inf)
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float sv = p.scoring == IQK_SOFTMAX ? s[v] / total : s[v];
-        c[v] = p.bias && l[v] != neg_inf() ? sv + c[v] : l[v];
-    }
-    if (p.n_group > 1) {
-        // a group's worth in lane g, -inf where none of its experts is in
-        const int per = E / p.n_group;
-        float worth = neg_inf();
-        for (int g = 0; g < p.n_group; ++g) {
-            float a[V];
+    if (p.bias || two || (softmax && !p.renorm)) {
+        if (softmax) {
+            top = row_max<L>(top);
+            float sum = 0.f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int e = v * 64 + lane;
-                const bool in = e >= g * per && e < (g + 1) * per && c[v] != neg_inf();
-                a[v] = !in ? neg_inf() : (p.group_top == 2 && !p.bias ? s[v] : c[v]);
+                s[v] = l[v] == neg_inf() ? 0.f : expf(l[v] - top);
+                sum += s[v];
             }
-            int reg, ln;
-            float w = wave_best<V>(a, &reg, &ln);
-            if (p.group_top == 2) {
+            total = row_sum<L>(sum);
+        } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v == reg && lane == ln) a[v] = neg_inf();
-                const float second = wave_best<V>(a, &reg, &ln);
-                if (second != neg_inf()) w += second;
-            }
-            if (lane == g) worth = w;
-        }
-        // the groups that stay, as a mask of group numbers
-        uint64_t stay = 0;
-        for (int i = 0; i < p.topk_group; ++i) {
-            const float m = wave_max(worth);
-            if (m == neg_inf()) break;
-            const int g = __builtin_ctzll(__ballot(worth == m));
-            stay |= 1ull << g;
-            if (lane == g) worth = neg_inf();
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = v * 64 + lane;
-            if (e >= E || !((stay >> (e / per)) & 1)) c[v] = neg_inf();
+            for (int v = 0; v < V; ++v) s[v] = sigmoid(l[v]);
         }
     }
-    // the k best; slot j's id, score and logit in lane j
-    int id = -1;
-    float score = 0.f, logit = neg_inf();
+    // what the choice goes by; an expert whose logit or bias is -inf is out (c = -inf)
+    if (p.bias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float b = v < left ? p.bias[e0 + v] : 0.f;
+            bad |= b != b;
+            c[v] = l[v] != neg_inf() ? (softmax ? s[v] / total : s[v]) + b : l[v];
+        }
+    }
+    if (p.n_group > 1) {
+        const int per = E / p.n_group;
+        if (p.lane_groups) {  // a group is 1, 2, 4, 8 or 16 whole lanes
+            const int lanes = per / V;
+            float a = neg_inf(), b = neg_inf();  // the lane's best two
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float w = two && !p.bias && c[v] != neg_inf() ? s[v] : c[v];
+                b = fmaxf(b, fminf(a, w));
+                a = fmaxf(a, w);
+            }
+            auto merge = [&](float oa, float ob) {
+                b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+                a = fmaxf(a, oa);
+            };
+            if (lanes > 1) merge(dpp<kXor1>(a), dpp<kXor1>(b));
+            if (lanes > 2) merge(dpp<kXor2>(a), dpp<kXor2>(b));
+            if (lanes > 4) merge(dpp<kHalfMirror>(a), dpp<kHalfMirror>(b));
+            if (lanes > 8) merge(dpp<kMirror>(a), dpp<kMirror>(b));
+            float worth = two && b != neg_inf() ? a + b : a;
+            if (left <= 0) worth = neg_inf();
+            bool stays = false;
+            for (int i = 0; i < p.topk_group; ++i) {
+                const float m = row_max<L>(worth);
+                const uint64_t best = row_bits<L>(__ballot(worth == m), lane);
+                const int first = __builtin_ctzll(best | (1ull << 63));
+                if (m != neg_inf() && sub / lanes == first / lanes) {
+                    stays = true;
+                    worth = neg_inf();
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] = stays ? c[v] : neg_inf();
+        } else if constexpr (L == 64) {
+            // a group's worth in lane g, -inf where none of its experts is in
+            float worth = neg_inf();
+            for (int g = 0; g < p.n_group; ++g) {
+                float a[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const bool in = e0 + v >= g * per && e0 + v < (g + 1) * per && c[v] != neg_inf();
+                    a[v] = !in ? neg_inf() : (two && !p.bias ? s[v] : c[v]);
+                }
+                int at;
+                float best = lane_best<V>(a, &at);
+                float w = row_max<64>(best);
+                if (two) {
+                    const int first = __builtin_ctzll(__ballot(best == w));
+                    if (lane == first) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) a[v] = v == at ? neg_inf() : a[v];
+                        best = lane_best<V>(a, &at);
+                    }
+                    const float second = row_max<64>(best);
+                    if (second != neg_inf()) w += second;
+                }
+                if (lane == g) worth = w;
+            }
+            uint64_t stay = 0;  // the groups that stay, as a mask of group numbers
+            for (int i = 0; i < p.topk_group; ++i) {
+                const float m = row_max<64>(worth);
+                if (m == neg_inf()) break;
+                const int g = __builtin_ctzll(__ballot(worth == m));
+                stay |= 1ull << g;
+                if (lane == g) worth = neg_inf();
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v >= left || !((stay >> ((e0 + v) / per)) & 1)) c[v] = neg_inf();
+        }
+    }
+    // the k best: slot j's id goes out from the lane that holds the expert, its score (or logit) to lane j
+    const bool whole_row_bad = row_bits<L>(__ballot(bad), lane) != 0;
+    int at;
+    float best = lane_best<V>(c, &at);
+    float value = 0.f, first_id = -1.f;
     int found = 0;
-    for (; found < p.k; ++found) {
-        int reg, ln;
-        if (wave_best<V>(c, &reg, &ln) == neg_inf()) break;
-        float sv = 0.f, lv = 0.f;
+    int32_t* ids = p.ids + t * p.k;
+    for (int j = 0; j < p.k; ++j) {
+        const float m = row_max<L>(best);
+        const bool any = m != neg_inf();
+        if (!__ballot(any)) break;
+        const uint64_t bits = row_bits<L>(__ballot(any && best == m), lane);
+        const bool won = any && sub == __builtin_ctzll(bits | (1ull << 63));
+        float got = m;  // the choice went by logits: the winner's logit
+        if (p.bias) {
+            float mine = neg_inf();  // its score
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (v == reg) {
-                sv = lane_value(s[v], ln);
-                lv = lane_value(l[v], ln);
-                if (lane == ln) c[v] = neg_inf();
-            }
+            for (int v = 0; v < V; ++v) mine = won && v == at ? s[v] : mine;
+            got = row_max<L>(mine);
         }
-        if (lane == found) {
-            id = reg * 64 + ln;
-            score = sv;
-            logit = lv;
+        if (j == 0) first_id = row_max<L>(won ? (float)(e0 + at) : -1.f);
+        if (won) {
+            if (there && !whole_row_bad) ids[j] = e0 + at;
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] = v == at ? neg_inf() : c[v];
+            best = lane_best<V>(c, &at);
         }
+        found += any;
+        value = any && sub == j ? got : value;
     }
-    const bool filled = lane < found;
+    const bool filled = sub < found;
     float w = 0.f;
-    if (p.scoring == IQK_SOFTMAX && p.renorm) {
-        // exp(l - the largest chosen logit): the row's other experts cancel
-        const float best = wave_max(logit);
-        const float e = filled ? expf(logit - best) : 0.f;
-        w = e / wave_sum(e);
-    } else if (p.renorm) {
-        const float d = wave_sum(filled ? score : 0.f);
-        w = d > 0.f ? score / d : 0.f;
+    if (p.bias) {  // value is a score (softmax: before its division by the total)
+        const float d = p.renorm ? row_sum<L>(filled ? value : 0.f) : total;
+        w = d > 0.f ? value / d : 0.f;
+    } else if (softmax) {  // value is a logit; renorm: the row's other experts cancel
+        const float most = p.renorm ? row_max<L>(filled ? value : neg_inf()) : top;
+        const float x = filled ? expf(value - most) : 0.f;
+        w = x / (p.renorm ? row_sum<L>(x) : total);
     } else {
-        w = score / total;
+        const float x = filled ? sigmoid(value) : 0.f;
+        const float d = p.renorm ? row_sum<L>(x) : 1.f;
+        w = d > 0.f ? x / d : 0.f;
     }
     // slots that no expert is left for repeat the first one at weight zero
-    const int first = __builtin_amdgcn_readlane(id, 0);
-    if (lane < p.k) {
-        p.ids[t * p.k + lane] = filled ? id : first;
-        p.weights[t * p.k + lane] = filled ? w * p.scale : 0.f;
+    for (int j = sub; j < p.k && there; j += L) {
+        if (whole_row_bad) {
+            ids[j] = -1;
+            p.weights[t * p.k + j] = __builtin_nanf("");
+        } else {
+            if (j >= found) ids[j] = (int)first_id;
+            p.weights[t * p.k + j] = j < found ? w * p.scale : 0.f;
+        }
     }
 }
 
@@ -305,7 +405,6 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(RouterGr
     }
 }
 
-// Registers per lane for E experts: 1, 2, 4, 8 or 16 (E <= 1024).
 template <class F>
 void by_width(int E, F f) {
     if (E <= 64) f(std::integral_constant<int, 1>{});
@@ -324,11 +423,27 @@ void by_dtype(int dt, F f) {
 }  // namespace
 
 hipError_t launch_router(const RouterLaunch& a, hipStream_t s) {
-    const unsigned blocks = (unsigned)((a.T + kRouterWaves - 1) / kRouterWaves);
-    by_width(a.E, [&](auto v) {
+    RouterLaunch p = a;
+    const int size = a.dtype == IQK_F32 ? 4 : 2;
+    p.wide = (int64_t)a.E * size % 16 == 0 && (uintptr_t)a.logits % 16 == 0;
+    const int per = a.E / a.n_group;
+    by_width(a.E, [&](auto v64) {
+        constexpr int V64 = decltype(v64)::value, V16 = 4 * V64;  // experts per lane of 64 and of 16
+        // whether a group is 2^i <= 16 whole lanes
+        auto whole = [&](int V) { return per % V == 0 && per / V <= 16 && (per / V & (per / V - 1)) == 0; };
+        // Rows of 16 lanes: four tokens for little more than one's instructions, in a chain a few times as long, so
+        // they win where tokens far outnumber the card's 8192 resident waves (256 experts, softmax, k = 6: 4096
+        // tokens 6.9 us against 5.3 with rows of 64, 16384 tokens 8.8 against 12.5; 512 experts gain nothing).
+        const bool many = a.T >= kManyTokens && V16 <= 16 && a.k <= 16 && (a.n_group == 1 || whole(V16));
+        p.lane_groups = a.n_group > 1 && whole(many ? V16 : V64);
         by_dtype(a.dtype, [&](auto dt) {
-            hipLaunchKernelGGL((router_kernel<decltype(v)::value, decltype(dt)::value>), dim3(blocks),
-                               dim3(64 * kRouterWaves), 0, s, a);
+            constexpr int DT = decltype(dt)::value;
+            const int64_t lanes = a.T * (many ? 16 : 64);
+            const dim3 grid((unsigned)((lanes + 64 * kRouterWaves - 1) / (64 * kRouterWaves))), block(64 * kRouterWaves);
+            if constexpr (V16 <= 16) {
+                if (many) hipLaunchKernelGGL((router_kernel<16, V16, DT>), grid, block, 0, s, p);
+            }
+            if (!many) hipLaunchKernelGGL((router_kernel<64, V64, DT>), grid, block, 0, s, p);
         });
     });
     return hipGetLastError();

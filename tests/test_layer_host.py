@@ -64,7 +64,7 @@ BAD_WEIGHTS = [(dict(experts=0), E_ARG), (dict(out=0), E_ARG), (dict(in_=0), E_A
 
 
 def _linear(w, **change):
-    a = dict(x=P, dtype=BF16, xs=None, M=4, ws=P, nbytes=1 << 20, y=P, ydt=F32, stream=None)
+    a = dict(x=P, dtype=BF16, xs=None, M=100, ws=P, nbytes=1 << 20, y=P, ydt=F32, stream=None)
     a.update(change)
     return q._lib.iqk_fp8_linear(ctypes.byref(w), *a.values())
 
