@@ -66,12 +66,12 @@ struct TileShape {
     static_assert(S * kStage <= 160 * 1024, "LDS");
 };
 
-template <int TM, int TN, int WM, int WN, int S, int YT, bool GROUPED, bool EXACT>
+template <int TM, int TN, int WM, int WN, int S, int YT, bool GROUPED, bool EXACT, bool PART>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(TileParams p) {
     using Sh = TileShape<TM, TN, WM, WN, S>;
     constexpr int kI = Sh::kI, kJ = Sh::kJ, kG = Sh::kG;
     __shared__ __align__(16) uint8_t sh[S * Sh::kStage];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int li = lane & 15, g = lane >> 4;
     const int nb = (p.n + kBlock - 1) / kBlock, nob = (p.out + kBlock - 1) / kBlock;
     const int ntn = (p.out + TN - 1) / TN, runs = (ntn + p.run - 1) / p.run;
@@ -137,6 +137,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     const int su = wave * 64 + lane;
     const float* sptr = p.sx + row_of(min(su, TM - 1)) * nb;
     // the next block to copy: block cb of the weight tile at row cn
+    const int nend = min(n0 + p.run * TN, p.out);
     int cb = 0, cn = n0;
     const uint8_t* wbase;
     auto weight_tile = [&]() {
@@ -149,34 +150,38 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     };
     weight_tile();
     const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)sh;
-    auto copy_next = [&](int slot) {
+    // Copy c of the kCopies that bring the next block into a stage: weight rows, rows of x, scales.  PART: the depth's
+    // last block is partial, and chunks past the depth are zero.  (Once the last block is on its way the last tile's
+    // first one is copied again, which nothing reads: every step takes as many instructions, and the waits count them.)
+    auto copy = [&](int c, int slot) {
         const int k0 = cb * kBlock;
         const uint32_t at = sh0 + slot * Sh::kStage + wave * 1024;
-        if (k0 + kBlock <= p.n) {
-#pragma unroll
-            for (int c = 0; c < Sh::kCW; ++c) lds_copy16(wbase + k0, woff[c], at + c * Sh::kRowsPerCopy * 128);
-#pragma unroll
-            for (int c = 0; c < Sh::kCX; ++c) {
-                const uint32_t d = at + Sh::kX + c * Sh::kRowsPerCopy * 128;
-                if constexpr (GROUPED) lds_copy16(xsrc(c, k0), d);
-                else lds_copy16(xbase + k0, xoff[c], d);
-            }
-        } else {  // the partial last block (as many instructions as any other: the waits count them)
-#pragma unroll
-            for (int c = 0; c < Sh::kCW; ++c)
-                lds_copy16(k0 + wch < p.n ? wbase + k0 + woff[c] : (const uint8_t*)&g_zero, at + c * Sh::kRowsPerCopy * 128);
-#pragma unroll
-            for (int c = 0; c < Sh::kCX; ++c)
-                lds_copy16(k0 + xch < p.n ? xsrc(c, k0) : (const uint8_t*)&g_zero,
-                           at + Sh::kX + c * Sh::kRowsPerCopy * 128);
-        }
-        lds_copy4(sptr + cb, sh0 + slot * Sh::kStage + Sh::kScales + wave * 256);
-        if (++cb == nb) {
-            cb = 0;
-            cn += TN;
-            if (cn < p.out) weight_tile();
+        if (c < Sh::kCW) {
+            const uint32_t d = at + c * Sh::kRowsPerCopy * 128;
+            if constexpr (PART) lds_copy16(k0 + wch < p.n ? wbase + k0 + woff[c] : (const uint8_t*)&g_zero, d);
+            else lds_copy16(wbase + k0, woff[c], d);
+        } else if (c < Sh::kCW + Sh::kCX) {
+            const int i = c - Sh::kCW;
+            const uint32_t d = at + Sh::kX + i * Sh::kRowsPerCopy * 128;
+            if constexpr (PART) lds_copy16(k0 + xch < p.n ? xsrc(i, k0) : (const uint8_t*)&g_zero, d);
+            else if constexpr (GROUPED) lds_copy16(xsrc(i, k0), d);
+            else lds_copy16(xbase + k0, xoff[i], d);
+        } else {
+            lds_copy4(sptr + cb, sh0 + slot * Sh::kStage + Sh::kScales + wave * 256);
         }
     };
+    auto advance = [&]() {
+        if (++cb < nb) return;
+        cb = 0;
+        if (cn + TN < nend) {
+            cn += TN;
+            weight_tile();
+        }
+    };
+    // A wave that has copies to issue waits until the memory pipeline takes them, which is slower than it issues them
+    // (all at the head of a block: half of the waves 2800 cycles of a block's 4800), so they go out between the
+    // tile rows' products: kPer at each of the first rows.
+    constexpr int kPer = (4 * Sh::kCopies + 3 * kI - 1) / (3 * kI);
 
     const int wn = (wave % (TN / WN)) * WN, wm = (wave / (TN / WN)) * WM;  // this wave's part of the tile
     const bool busy = m0 + wm < count;                                     // whether any of its rows of x is there
@@ -223,7 +228,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
 
     // Instruction t = i kJ + j of a block multiplies tile row i by x tile j.  Its product is added to the sums two
     // instructions later (kLag: it is done by then), and a tile row is read kAhead rows before its first use.
-    constexpr int kAhead = kI < 4 ? 1 : (GROUPED && TM * TN > 128 * 128 ? 1 : 2);  // (two would spill there)
+    constexpr int kAhead = kI < 4 ? 1 : ((GROUPED || PART) && TM * TN > 128 * 128 ? 1 : 2);  // (two would spill there)
     constexpr int kLag = 2, kRing = 4, kT = kI * kJ;
     static_assert(EXACT || kT % kRing == 0, "a block's first products follow the last block's in the ring");
     float f[kJ], fp[kJ];
@@ -239,16 +244,23 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     };
 
     constexpr int kBehind = (S - 2) * Sh::kCopies;  // copies that may still be on their way when a block is published
-    const int steps = nb * min(p.run, (p.out - n0 + TN - 1) / TN);
+    const int steps = nb * ((nend - n0 + TN - 1) / TN);
 #pragma unroll
-    for (int b = 0; b < S - 1; ++b)
-        if (b < steps) copy_next(b);
-    if (steps >= S - 1) publish<kBehind>();
-    else publish<0>();
+    for (int b = 0; b < S - 1; ++b) {
+#pragma unroll
+        for (int c = 0; c < Sh::kCopies; ++c) copy(c, b);
+        advance();
+    }
+    publish<kBehind>();
     int slot = 0, b = 0;  // b: block of the tile that is being multiplied
     for (int step = 0; step < steps; ++step) {
         const uint8_t* cur = sh + slot * Sh::kStage;
-        if (step + S - 1 < steps) copy_next(slot == 0 ? S - 1 : slot - 1);
+        const int into = slot == 0 ? S - 1 : slot - 1;
+        auto copy_some = [&](int i) {
+#pragma unroll
+            for (int c = i * kPer; c < (i + 1) * kPer; ++c)
+                if (c < Sh::kCopies) copy(c, into);
+        };
         if (busy) {
             // (tiles i and i + 4 are 64 rows apart, i and i + 1 four rows, which no bit of the key looks at)
             auto afrag = [&](int i) { return frag(cur, aoff + (i >> 2) * 8192 + (i & 3) * 512); };
@@ -277,6 +289,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
 #pragma unroll
                 for (int i = 0; i < kI; ++i) {
                     if (i + kAhead < kI) af[(i + kAhead) % (kAhead + 1)] = afrag(i + kAhead);
+                    copy_some(i);
                     f16x8 ww[4];
 #pragma unroll
                     for (int h = 0; h < 4; ++h) ww[h] = widen(af[i % (kAhead + 1)][2 * h], af[i % (kAhead + 1)][2 * h + 1]);
@@ -302,6 +315,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
                         const f32x4 r = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                             af[i % (kAhead + 1)], bf[j], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
                         __builtin_amdgcn_sched_barrier(0);
+                        if (j == 0) copy_some(i);
                         if (t >= kLag) add(t - kLag, f);
                         else add(kT - kLag + t, fp);
                         d[t % kRing] = r;
@@ -311,9 +325,12 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
 #pragma unroll
                 for (int j = 0; j < kJ; ++j) fp[j] = f[j];
             }
+        } else {
+#pragma unroll
+            for (int c = 0; c < Sh::kCopies; ++c) copy(c, into);
         }
-        if (step + S - 1 < steps) publish<kBehind>();
-        else publish<0>();
+        advance();
+        publish<kBehind>();
         slot = slot == S - 1 ? 0 : slot + 1;
         if (++b == nb) {  // (after the wait, so that the stores are on their way while the next block is multiplied)
             if constexpr (!EXACT) {
@@ -331,6 +348,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
             n0 += TN;
         }
     }
+    // no copy may land in the LDS of the workgroup that gets it next
+    __builtin_amdgcn_s_waitcnt(0x0070);
 }
 
 constexpr int64_t kMaxRun = 2;
@@ -351,8 +370,9 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
                        (int)a.E, (int)run, a.offsets, a.perm, a.tiles, a.y};
     const int64_t total = tiles * ((ntn + run - 1) / run);
-    hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT>), dim3((unsigned)((total + 7) / 8 * 8)),
-                       dim3(64 * Sh::kWaves), 0, s, p);
+    const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * Sh::kWaves);
+    if (a.n % kBlock) hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, false>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
