@@ -366,7 +366,7 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     constexpr int64_t kResident = 256 * std::min(2, 160 * 1024 / (S * Sh::kStage));
     auto turns = [&](int64_t run) { return (tiles * ((ntn + run - 1) / run) + kResident - 1) / kResident * run; };
     int64_t run = 1;
-    while (run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
+    while (TM <= 64 && run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
                        (int)a.E, (int)run, a.offsets, a.perm, a.tiles, a.y};
     const int64_t total = tiles * ((ntn + run - 1) / run);
@@ -390,7 +390,8 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
     if constexpr (!F32) {
         if (tile == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, GROUPED>(a, s);
     }
-    return tile_launch<128, 128, 64, 64, 2, F32, YT, GROUPED>(a, s);
+    if constexpr (GROUPED) return tile_launch<128, 256, 64, 64, 3, F32, YT, true>(a, s);
+    else return tile_launch<128, 128, 64, 64, 2, F32, YT, false>(a, s);
 }
 
 }  // namespace
@@ -403,6 +404,7 @@ int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, 
         if (most <= 16) return 16;
         if (most <= 32) return 32;
         if (most <= 64) return 64;
+        // 64 experts of 2048 x 4096, 384 rows each: 256-row tiles 333 us, 128-row ones 380; 96 rows each: 294 and 271
         return !exact && rows_per_expert >= 192 && count(256) >= 160 ? 256 : 128;
     }
     // 256 x 256 tiles move half the bytes per product that 128 x 128 ones do, and those half of what 64 x 64 do;
