@@ -197,7 +197,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(RowsParams p) {
 constexpr int kRowsWaves = 4;
 
 template <int NT, int YT>
-__global__ __launch_bounds__(64 * kRowsWaves, NT >= 4 ? 3 : 4) void fp8_rows_kernel(RowsParams p) {
+__global__ __launch_bounds__(64 * kRowsWaves, 4) void fp8_rows_kernel(RowsParams p) {
     __shared__ float4 red[kRowsWaves][NT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int li = lane & 15, g = lane >> 4;
@@ -314,8 +314,7 @@ hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s) {
     by_float(a.y_dtype, [&](auto yt) {
         constexpr int YT = decltype(yt)::value;
         if (passes16 <= 1) rows_launch<1, YT>(p, s);
-        else if (passes16 <= 2) rows_launch<2, YT>(p, s);
-        else rows_launch<4, YT>(p, s);
+        else rows_launch<2, YT>(p, s);
     });
     return hipGetLastError();
 }

@@ -162,7 +162,7 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
 bool fp8_few_fits(int64_t rows, int64_t n);
 // few rows (or one pair per workgroup row), x of any type
 hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s);
-// e4m3 x: 16 * min(passes16, 4) rows in a pass over the weights
+// e4m3 x: 16 * min(passes16, 2) rows in a pass over the weights
 hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s);
 // e4m3 x, many rows; tile = fp8_tile_rows()
 int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact);

@@ -89,7 +89,7 @@ size_t quantized_bytes(int64_t rows, int64_t n) {
 
 // Rows of x up to which the dense product passes over the weights once
 // without tiles.
-constexpr int64_t kRowsPass = 64;
+constexpr int64_t kRowsPass = 32;
 // Whether the routed product takes each pair by itself: no grouping, one
 // launch, an expert's weights read once for each of its pairs.
 bool pair_by_pair(int64_t P, int64_t E, int64_t n) {
