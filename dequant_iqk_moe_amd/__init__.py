@@ -537,6 +537,17 @@ def moe_prefill_fused(w: Weights, x: torch.Tensor, ids: torch.Tensor, values=Non
     return y
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor of the stream the call runs on (the caching allocator may
+    give a tensor's memory away while another stream still writes it)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 # ---------------------------------------------------------------------------
 # expert selection
 # ---------------------------------------------------------------------------
@@ -567,9 +578,9 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
     lp, dt = _logits(logits)
     T, E = logits.shape
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        ids = _empty((T, k), torch.int32, logits.device, stream)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        weights = _empty((T, k), torch.float32, logits.device, stream)
     _check(_lib.iqk_router_topk(lp, dt, T, E, k, _scoring(scoring), _dev(bias, "bias", torch.float32, E), n_group,
                                 topk_group, group_top, int(bool(renorm)), scale,
                                 _dev(ids, "ids", torch.int32, T * k), _dev(weights, "weights", torch.float32, T * k),
@@ -589,7 +600,7 @@ def router_topk_grad(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.T
         raise IqkValueError(_E_SIZE, f"ids has {ids.shape[0]} rows, logits {T}")
     k = ids.shape[1]
     if d_logits is None:
-        d_logits = torch.empty_like(logits)
+        d_logits = _empty(logits.shape, logits.dtype, logits.device, stream)
     _check(_lib.iqk_router_topk_grad(lp, dt, ip, _dev(d_weights, "d_weights", torch.float32, T * k), T, E, k,
                                      _scoring(scoring), int(bool(renorm)), scale,
                                      _dev(d_logits, "d_logits", logits.dtype, T * E), _stream(stream)))
@@ -639,9 +650,9 @@ def fp8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: tor
     n = x.shape[-1]
     rows = x.numel() // n
     if codes is None:
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        codes = _empty(x.shape, torch.float8_e4m3fn, x.device, stream)
     if scales is None:
-        scales = torch.empty((*x.shape[:-1], _blocks(n)), dtype=torch.float32, device=x.device)
+        scales = _empty((*x.shape[:-1], _blocks(n)), torch.float32, x.device, stream)
     _check(_lib.iqk_fp8_quantize(_dev(x, "x"), _DT[x.dtype], rows, n,
                                  _dev(codes, "codes", torch.float8_e4m3fn, rows * n),
                                  _dev(scales, "scales", torch.float32, rows * _blocks(n)), _stream(stream)))
@@ -667,12 +678,12 @@ def fp8_linear_workspace_bytes(w: Fp8Weights, M: int) -> int:
     return _fp8_linear_bytes(w.experts, w.out, w.in_features, M)
 
 
-def _workspace(workspace: torch.Tensor | None, nbytes: int, device):
-    """(pointer, size) of the caller's workspace, or of a new one where the call needs any."""
+def _workspace(workspace: torch.Tensor | None, nbytes: int, device, stream):
+    """(workspace, pointer, size): the caller's, or a new one where the call needs any."""
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = _empty(nbytes, torch.uint8, device, stream)
     return workspace, _dev(workspace, "workspace", torch.uint8), workspace.numel()
 
 
@@ -687,10 +698,11 @@ def fp8_linear(w: Fp8Weights, x: torch.Tensor, x_scales: torch.Tensor | None = N
     M = x.numel() // n
     xp, xdt, sp = _fp8_x(x, x_scales, M, n)
     if y is None:
-        y = torch.empty((*x.shape[:-1], w.out), dtype=out_dtype, device=x.device)
+        y = _empty((*x.shape[:-1], w.out), out_dtype, x.device, stream)
     if y.dtype not in _DT:
         raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
-    ws, wp, nbytes = _workspace(workspace, 0 if xdt == _E4M3 else fp8_linear_workspace_bytes(w, M), x.device)
+    ws, wp, nbytes = _workspace(workspace, 0 if xdt == _E4M3 else fp8_linear_workspace_bytes(w, M), x.device,
+                               stream)
     cw = w._c()
     _check(_lib.iqk_fp8_linear(ctypes.byref(cw), xp, xdt, sp, M, wp, nbytes, _dev(y, "y", None, M * w.out),
                                _DT[y.dtype], _stream(stream)))
@@ -718,10 +730,10 @@ def moe_fp8(w: Fp8Weights, x: torch.Tensor, ids: torch.Tensor, x_slots: int = 1,
     T, k = ids.shape
     xp, xdt, sp = _fp8_x(x, x_scales, T * x_slots, w.in_features)
     if y is None:
-        y = torch.empty((T, k, w.out), dtype=out_dtype, device=x.device)
+        y = _empty((T, k, w.out), out_dtype, x.device, stream)
     if y.dtype not in _DT:
         raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
-    ws, wp, nbytes = _workspace(workspace, moe_fp8_workspace_bytes(w, T, k, x_slots), x.device)
+    ws, wp, nbytes = _workspace(workspace, moe_fp8_workspace_bytes(w, T, k, x_slots), x.device, stream)
     cw = w._c()
     _check(_lib.iqk_moe_fp8(ctypes.byref(cw), xp, xdt, sp, x_slots, ip, T, k, int(bool(sorted)), wp, nbytes,
                             _dev(y, "y", None, T * k * w.out), _DT[y.dtype], _stream(stream)))

@@ -405,7 +405,8 @@ typedef struct iqk_fp8_weights {
  * e4m3(x * (448 / a)), the quotients and the product rounded to float32, the
  * code to nearest even.  A NaN in x gives a NaN code; an infinity gives a NaN
  * code and an infinite scale.  n % 16 == 0 (IQK_E_SHAPE), n <= 2^20, rows <=
- * 2^24; x and codes 16-byte aligned. */
+ * 2^24, rows * n <= 2^40 (IQK_E_ARG, also in the products below); x and
+ * codes 16-byte aligned. */
 int iqk_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, uint8_t* codes, float* scales,
                      void* stream);
 

@@ -109,6 +109,21 @@ def test_linear(M, N, K):
         assert torch.equal(again, y)
 
 
+@pytest.mark.parametrize("M,N,K", [(34, 66, 256), (200, 1000, 656), (1300, 2000, 272), (1290, 1990, 384), (4000, 2600, 272),
+                                   (3990, 2570, 256)])
+def test_linear_tiles(M, N, K):
+    """Enough tiles for each tile size, in whole and in partial blocks of the depth."""
+    announce(f"linear tiles M={M} N={N} K={K}")
+    rng = np.random.default_rng(M + N + K)
+    w, s = _weights(rng, 1, N, K)
+    W = _device_weights(w, s)
+    t, x = _activations(rng, M, K, "bf16")
+    rc, rs = layer.quantize(x)
+    ref = layer.linear(w[0], s[0], rc, rs)
+    for yt in ("f32", "bf16", "f16"):
+        assert _off(q.fp8_linear(W, t, out_dtype=DT[yt]), ref) <= BAR[yt], yt
+
+
 def test_linear_is_the_transposed_products_gradient():
     """sum(y * dy) differentiated by x is the product of dy with the
     transposed codes and scales (square blocks transpose): checked against
@@ -227,12 +242,44 @@ def test_moe(T, k, E, N, K):
         _moe_check(w, s, ids, slots, xt, yt, rng)
 
 
+@pytest.mark.parametrize("T,k,E,N,K", [(128, 4, 64, 512, 528),      # about 8 rows per expert
+                                       (160, 2, 16, 512, 512),      # 20
+                                       (180, 2, 8, 300, 656),       # 45
+                                       (400, 2, 8, 520, 384),       # 100
+                                       (2048, 2, 8, 2570, 272),     # 512
+                                       (2050, 2, 8, 2560, 256),
+                                       (600, 4, 1100, 256, 256),    # more experts than one workgroup counts
+                                       (5000, 2, 5, 130, 144)])     # more pairs than one workgroup places
+def test_moe_grouped(T, k, E, N, K):
+    """Each size of group, and of the grouping before it."""
+    announce(f"moe grouped T={T} k={k} E={E} N={N} K={K}")
+    rng = np.random.default_rng(T + E + N)
+    w, s = _weights(rng, E, N, K)
+    ids = np.argsort(rng.random((T, E)), 1)[:, :k].astype(np.int32)
+    ids[1, 0], ids[T - 1, 1] = E, -5
+    for slots, xt, yt in ((1, "bf16", "f32"), (k, "f32", "bf16"), (1, "f16", "f16")):
+        _moe_check(w, s, ids, slots, xt, yt, rng)
+
+
+@pytest.mark.parametrize("counts", [[16, 17, 0, 1, 15, 33, 32, 64], [0, 0, 500, 0, 0, 0, 0, 1], [63, 65, 48, 49, 31, 47, 50, 40],
+                                    [255, 257, 1, 128, 129, 0, 300, 127], [700, 200, 192, 256, 64, 320, 449, 512]])
+def test_moe_group_sizes(counts):
+    """Groups at and around the edges of the tiles; some empty."""
+    announce(f"moe group sizes {counts}")
+    rng = np.random.default_rng(sum(counts))
+    E, N, K = len(counts), 2580 if sum(counts) > 2000 else 530, 272
+    w, s = _weights(rng, E, N, K)
+    ids = rng.permutation(np.repeat(np.arange(E), counts)).astype(np.int32)[:, None]
+    for yt in ("f32", "bf16"):
+        _moe_check(w, s, ids, 1, "bf16", yt, rng)
+
+
 @pytest.mark.parametrize("T", [1, 9, 200])
 def test_moe_ids(T):
     """Invalid, repeated, one-sided and sorted ids."""
     announce(f"moe ids T={T}")
     rng = np.random.default_rng(T)
-    E, k, N, K = 6, 4, 72, 160
+    E, k, N, K = 6, 4, 472, 1040
     w, s = _weights(rng, E, N, K)
     ids = rng.integers(0, E, (T, k)).astype(np.int32)
     for yt in ("f32", "bf16"):
@@ -278,6 +325,31 @@ def test_same_result_every_time_and_on_another_stream():
     q.moe_fp8(W, t, ids, workspace=ws, y=y, stream=st)
     st.synchronize()
     assert torch.equal(first, y)
+
+
+def test_new_results_belong_to_the_calls_stream():
+    """Results and workspaces made by a call on another stream come from that
+    stream's memory: freed, they are not given to the current stream's next
+    tensors while the call still runs."""
+    rng = np.random.default_rng(12)
+    E, k, N, K, T = 8, 2, 512, 1024, 300
+    W = _device_weights(*_weights(rng, E, N, K))
+    S = _device_weights(*_weights(rng, 1, N, K))
+    t, _ = _activations(rng, T, K, "bf16")
+    logits = torch.randn(T, E, device="cuda")
+    ids, wt = q.router_topk(logits, k)
+    want = (q.moe_fp8(W, t, ids), q.fp8_linear(S, t), *q.fp8_quantize(t), wt)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    for stream in (st, st.cuda_stream):
+        for _ in range(20):
+            i2, w2 = q.router_topk(logits, k, stream=stream)
+            got = (q.moe_fp8(W, t, i2, stream=stream), q.fp8_linear(S, t, stream=stream), *q.fp8_quantize(t, stream=stream), w2)
+            junk = [torch.full((T * N,), float("nan"), device="cuda") for _ in range(3)]
+            del junk
+        st.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a.float(), b.float())
 
 
 def test_graph_replays():

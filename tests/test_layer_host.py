@@ -92,7 +92,7 @@ def test_linear_takes_one_expert_and_no_rows():
     (dict(T=-1), E_ARG), (dict(T=1 << 24), E_ARG), (dict(sorted=2), E_ARG), (dict(nbytes=64), E_SIZE),
     (dict(ws=None), E_SIZE), (dict(xs=P), E_ARG)])
 def test_moe_refuses(change, code):
-    a = dict(x=P, dtype=BF16, xs=None, x_slots=1, ids=P, T=3, k=4, sorted=0, ws=P, nbytes=1 << 20, y=P, ydt=F32,
+    a = dict(x=P, dtype=BF16, xs=None, x_slots=1, ids=P, T=300, k=4, sorted=0, ws=P, nbytes=1 << 20, y=P, ydt=F32,
              stream=None)
     a.update(change)
     w = _w(experts=8)
