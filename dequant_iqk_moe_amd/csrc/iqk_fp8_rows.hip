@@ -10,9 +10,11 @@
 // together they read consecutive bytes of each weight row, and add their sums
 // through LDS in wave order: the same result every time.
 //
-// Bound: bytes of the weights.  A widened weight costs half a vector
-// instruction and an eighth of a matrix instruction's lane slot, well below
-// what memory delivers.
+// Bound: bytes of the weights, and a launch's start.  A widened weight costs
+// half a vector instruction and an eighth of a matrix instruction's lane slot,
+// well below what memory delivers.  One row of x by 4096 x 4096 weights: 6.0
+// us (2.8 TB/s of 16.8 MB); one token at six experts of that size: 22 us (4.5
+// TB/s; a plain read of as many bytes 17.7 us).
 #include "iqk_fp8_device.h"
 
 namespace iqk {

@@ -1,22 +1,33 @@
 // iqk_fp8_tile.hip -- the 8-bit product tile by tile.
 //
 // A workgroup owns TM rows of x by TN weight rows.  Each block of 128 of the
-// depth goes from memory straight into LDS, kStages - 1 blocks ahead, as 128
-// bytes per row with their 16-byte chunks permuted (xkey, wkey) so that a
-// fragment's reads meet no bank twice; the block's scales go along.  Every
-// block's products start at zero and are added to the float32 sums with the
-// product of the two scales.
+// depth goes from memory straight into LDS, S - 1 blocks ahead, as 128 bytes
+// per row with their 16-byte chunks permuted (xkey, wkey) so that a fragment's
+// reads meet no bank twice (no conflicts by the counters); the block's scales
+// go along.  Every block's products start at zero and are added to the float32
+// sums with the product of the two scales, so a matrix instruction's
+// accumulator is never carried from one block to the next.
 //
 // EXACT widens the fragments to float16 in registers and uses
 // v_mfma_f32_16x16x32_f16; otherwise one v_mfma_scale_f32_16x16x128_f8f6f4
 // (both scales 2^0) takes a whole block.
 //
-// What bounds it.  256 x 256 tiles of 16-bit results: the LDS, which every wave
-// reads 24 KiB of per block for 32 matrix instructions.  Small TM: the bytes of
-// the weights; the copies need no registers, so as many are in flight as the
-// LDS holds, and each is whole 128-byte lines, where fragments loaded by their
-// lanes would ask for halves of 16 lines at a time (512-token case of 256
-// experts: 445 us that way, 64 lines of x staged in LDS).
+// Measured, with 16-bit results: 8192 x 4096 x 4096 in 133 us = 2.06 PFLOP/s,
+// matrix pipes 41 % busy, where the same instructions with the four
+// multiply-adds each needs, and nothing else, run at 3.1 to 3.9 PFLOP/s.  A
+// block of 256 x 256 tiles takes 3540 cycles of a CU for 2048 of its matrix
+// pipes: about 450 until a block's first fragments are there, 250 at its
+// barrier, and two waves per SIMD that share its pipe at 40 cycles per
+// instruction of 32.  More stages do not fit its LDS, and smaller tiles, which
+// would leave room for them, move more bytes per product (128 x 256 in three
+// stages 166 us).  float32 results: 290 us = 0.95 PFLOP/s.
+//
+// Few rows per expert: bytes of the weights.  The copies need no registers, so
+// as many are in flight as the LDS holds, and each is whole 128-byte lines,
+// where fragments loaded by their lanes ask for halves of 16 lines at a time
+// (256 experts of 4096 x 2048, 12 rows each: 410 us = 5.3 TB/s of weights;
+// with fragments loaded by their lanes 430 to 460).  What is left to the 6.4
+// TB/s of a plain read is the start of each workgroup and the results' stores.
 #include <algorithm>
 #include <cmath>
 
@@ -42,20 +53,16 @@ struct TileParams {
 // What copies past the depth read.
 __device__ const uint4 g_zero = {0, 0, 0, 0};
 
-// Key of a tile's weight rows: a fragment's 16 lanes read rows
-// 4 G (l / 4) + l % 4 + const for groups of G = min(kI, 4) tiles, so bits 0, 1
-// and log2(4 G) of the row tell eight neighbouring lanes apart.
-template <int G>
-__device__ __forceinline__ int wkey(int r) {
-    constexpr int kBit = G == 1 ? 2 : (G == 2 ? 3 : 4);
-    return (r & 3) | (((r >> kBit) & 1) << 2);
-}
+// Key of a tile's weight rows: a fragment's 16 lanes read rows 8 (l / 4) + l % 4
+// + const, so bits 0, 1 and 3 of the row tell eight neighbouring lanes apart.
+__device__ __forceinline__ int wkey(int r) { return (r & 3) | ((r >> 1) & 4); }
 
 template <int TM, int TN, int WM, int WN, int S>
 struct TileShape {
     static constexpr int kWaves = (TM / WM) * (TN / WN);
     static constexpr int kI = WN / 16, kJ = WM / 16;     // a wave's tiles of weight rows and of rows of x
-    static constexpr int kG = kI < 4 ? kI : 4;           // tiles whose rows are dealt out four at a time
+    static constexpr int kG = 2;                         // tiles whose rows are dealt out four at a time
+    static_assert(kI % kG == 0, "whole groups of tiles");
     static constexpr int kRowsPerCopy = 8 * kWaves;      // rows one copy instruction of all waves covers
     static constexpr int kCW = TN / kRowsPerCopy;
     static constexpr int kCX = (TM + kRowsPerCopy - 1) / kRowsPerCopy;
@@ -121,7 +128,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     // copies: lane l of a copy moves slot l & 7 of row l >> 3 of its wave's eight rows
     const int crow = wave * 8 + (lane >> 3);
     static_assert(Sh::kRowsPerCopy % 32 == 0, "a lane's chunk is the same in all of its copies");
-    const int wch = 16 * ((lane & 7) ^ wkey<kG>(crow)), xch = 16 * ((lane & 7) ^ xkey(crow));
+    const int wch = 16 * ((lane & 7) ^ wkey(crow)), xch = 16 * ((lane & 7) ^ xkey(crow));
     const uint8_t* xbase = GROUPED ? p.x : p.x + m0 * p.n;  // (dense: offsets inside the tile fit 32 bits)
     uint32_t woff[Sh::kCW], xoff[Sh::kCX];                  // (grouped: xoff is the row of x, multiplied out at each copy)
 #pragma unroll
@@ -193,10 +200,11 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
 #pragma unroll
         for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // lane li of tile i reads weight row 64 (i / 4) + 4 G (li / 4) + 4 (i % 4) + li % 4, so that a result lane's
-    // four rows of G neighbouring tiles are 4 G consecutive rows
+    // lane li of tile i reads weight row 32 (i / 2) + 8 (li / 4) + 4 (i % 2) + li % 4, so that a result lane's four
+    // rows of two neighbouring tiles are eight consecutive rows, and the four lanes of a row of x store 32 at a time
+    // (whole 64-byte pieces of 16-bit results)
     const int afirst = 4 * kG * (li >> 2) + (li & 3);
-    const int aoff = (wn + afirst) * 128 + 16 * (g ^ wkey<kG>(afirst));
+    const int aoff = (wn + afirst) * 128 + 16 * (g ^ wkey(afirst));
     const int boff = Sh::kX + (wm + li) * 128 + 16 * (g ^ xkey(li));
     const int soff = Sh::kScales + 4 * (wm + li), swoff = Sh::kScales + 4 * (TM + wn / kBlock);
     auto frag = [&](const uint8_t* s, int off) {
@@ -204,7 +212,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
     };
 
-    // result lane (li, g) holds, of row 16 j + li of x, weight rows 64 h + 4 G g + 4 i + q of its wave's
+    // result lane (li, g) holds, of row 16 j + li of x, weight rows 32 h + 8 g + 4 i + q of its wave's
     const bool whole = (p.out & 7) == 0 && ((uintptr_t)p.y & 15) == 0;
     auto store_tile = [&]() {
 #pragma unroll
@@ -215,15 +223,12 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
             if constexpr (GROUPED) yrow = pair_of(i);
 #pragma unroll
             for (int h = 0; h < kI / kG; ++h) {
+                const int o = n0 + wn + 32 * h + 8 * g;
+                if (o >= p.out) continue;
+                float v[8];
 #pragma unroll
-                for (int u = 0; u < kG / 2; ++u) {
-                    const int o = n0 + wn + 64 * h + 4 * kG * g + 8 * u;
-                    if (o >= p.out) continue;
-                    float v[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = acc[4 * h + 2 * u + (q >> 2)][j][q & 3];
-                    store8<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
-                }
+                for (int q = 0; q < 8; ++q) v[q] = acc[2 * h + (q >> 2)][j][q & 3];
+                store8<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
             }
         }
     };
@@ -268,8 +273,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
             for (int c = 0; c < Sh::kCopies; ++c) copy(c, into);
         }
         if (busy) {
-            // (tiles i and i + 4 are 64 rows apart, i and i + 1 four rows, which no bit of the key looks at)
-            auto afrag = [&](int i) { return frag(cur, aoff + (i >> 2) * 8192 + (i & 3) * 512); };
+            // (pairs of tiles are 32 rows apart, a pair's tiles four rows, which no bit of the key looks at)
+            auto afrag = [&](int i) { return frag(cur, aoff + (i >> 1) * 4096 + (i & 1) * 512); };
             i32x8 af[kAhead + 1], bf[kJ];
             af[0] = afrag(0);
             bf[0] = frag(cur, boff);
@@ -364,12 +369,13 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     const int64_t ntn = (a.out + TN - 1) / TN;
     const int64_t tiles = (a.M + TM - 1) / TM + (GROUPED ? std::min<int64_t>(a.E, a.M) : 0);  // (partial last tiles)
     // A workgroup's first blocks arrive a memory latency after it starts and its results leave while nothing else
-    // of it runs, so it takes two weight tiles in a run where the runs fill the card as evenly as tiles do (four and eight
-    // measured no faster: their last turn is emptier).
+    // of it runs, so it takes two weight tiles in a run where the runs fill the card as evenly as tiles do (8192 x
+    // 4096 x 4096: 133 us against 139; 256 experts of 4096 x 2048 with 12 rows each: 425 against 442; four and eight
+    // were no faster: their last turn is emptier).  Large groups differ too much in size for that: 350 against 337.
     constexpr int64_t kResident = 256 * std::min(2, 160 * 1024 / (S * Sh::kStage));
     auto turns = [&](int64_t run) { return (tiles * ((ntn + run - 1) / run) + kResident - 1) / kResident * run; };
     int64_t run = 1;
-    while (TM <= 64 && run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
+    while ((TM <= 64 || !GROUPED) && run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
                        (int)a.E, (int)run, a.offsets, a.perm, a.tiles, a.y};
     const int64_t total = tiles * ((ntn + run - 1) / run);
