@@ -63,8 +63,23 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* part) {
     return v + before;
 }
 
-// Counts of slice h's pairs per expert -> hist[h].  Rows of y for pairs with
-// an id outside [0, E) become NaN.
+// Rows of y for the pairs of this wave's 64 ids (from pair q0) that lie outside
+// [0, E) become NaN.
+__device__ __forceinline__ void nan_rows(const Fp8GroupLaunch& p, int64_t q0, bool in) {
+    const int lane = threadIdx.x & 63;
+    uint64_t bad = __ballot(!in);
+    while (bad) {
+        const int64_t row = (q0 + __builtin_ctzll(bad)) * p.out;
+        bad &= bad - 1;
+        if (p.y_half) {  // 0x7FFF is a quiet NaN in float16 and in bfloat16
+            for (int o = lane; o < p.out; o += 64) ((uint16_t*)p.y)[row + o] = 0x7FFFu;
+        } else {
+            for (int o = lane; o < p.out; o += 64) ((float*)p.y)[row + o] = __builtin_nanf("");
+        }
+    }
+}
+
+// Counts of a slice's pairs per expert, and the NaN rows of its other pairs.
 __device__ __forceinline__ void count_slice(const Fp8GroupLaunch& p, int64_t p0, int64_t p1, int32_t* cnt) {
     const int E = p.E;
     for (int e = threadIdx.x; e < E; e += kPrepThreads) cnt[e] = 0;
@@ -75,16 +90,7 @@ __device__ __forceinline__ void count_slice(const Fp8GroupLaunch& p, int64_t p0,
         const int e = q < p1 ? p.ids[q] : 0;
         const bool in = e >= 0 && e < E;
         if (q < p1 && in) atomicAdd(&cnt[e], 1);
-        uint64_t bad = __ballot(!in);
-        while (bad) {
-            const int64_t row = (q0 + __builtin_ctzll(bad)) * p.out;
-            bad &= bad - 1;
-            if (p.y_half) {  // 0x7FFF is a quiet NaN in float16 and in bfloat16
-                for (int o = lane; o < p.out; o += 64) ((uint16_t*)p.y)[row + o] = 0x7FFFu;
-            } else {
-                for (int o = lane; o < p.out; o += 64) ((float*)p.y)[row + o] = __builtin_nanf("");
-            }
-        }
+        nan_rows(p, q0, in);
     }
     __syncthreads();
 }
@@ -150,7 +156,14 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_place_kernel(Fp8GroupLaunch 
     place_slice(p, h, p0, p1, before, total, cur, part);
 }
 
-// Tile counts from iqk_route's offsets (more experts than one workgroup counts)
+// For more experts than one workgroup counts: the NaN rows that iqk_route's
+// grouping leaves out, and tile counts from its offsets.
+__global__ __launch_bounds__(kPrepThreads) void fp8_nan_kernel(Fp8GroupLaunch p) {
+    const int64_t q = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x;
+    const int e = q < p.P ? p.ids[q] : 0;
+    nan_rows(p, q - (threadIdx.x & 63), e >= 0 && e < p.E);
+}
+
 __global__ __launch_bounds__(kPrepThreads) void fp8_tiles_kernel(Fp8GroupLaunch p) {
     __shared__ uint64_t part[kPrepWaves];
     uint64_t base = 0;
@@ -189,12 +202,11 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
     const int64_t blocks128 = quantize ? q.rows * ((q.n + kBlock - 1) / kBlock) : 0;
     const int64_t qb = (blocks128 + kPrepBlocks - 1) / kPrepBlocks;
     if (g.E > kGroupE) {
-        RouteLaunch r{g.ids, g.P, g.E, 0, g.counts, g.offsets, g.perm};
-        r.ynan = (float*)g.y;
-        r.yout = g.out;
-        r.yhalf = g.y_half;
-        hipError_t e = launch_route(r, s);
+        hipError_t e = launch_route(RouteLaunch{g.ids, g.P, g.E, 0, g.counts, g.offsets, g.perm}, s);
         if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(fp8_nan_kernel, dim3((unsigned)((g.P + kPrepThreads - 1) / kPrepThreads)), dim3(kPrepThreads), 0,
+                           s, g);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL(fp8_tiles_kernel, dim3(1), dim3(kPrepThreads), 0, s, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         return quantize ? launch_fp8_quantize(q, s) : hipSuccess;

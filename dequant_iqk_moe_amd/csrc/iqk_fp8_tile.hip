@@ -213,7 +213,6 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     };
 
     // result lane (li, g) holds, of row 16 j + li of x, weight rows 32 h + 8 g + 4 i + q of its wave's
-    const bool whole = (p.out & 7) == 0 && ((uintptr_t)p.y & 15) == 0;
     auto store_tile = [&]() {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
@@ -228,7 +227,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
                 float v[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = acc[2 * h + (q >> 2)][j][q & 3];
-                store8<YT>(p.y, yrow * p.out + o, v, whole, p.out - o);
+                store8<YT>(p.y, yrow * p.out + o, v, p.out - o);
             }
         }
     };

@@ -5,7 +5,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "iqk_internal.h"
+#include "iqk_layer.h"
 #include "iqk_status.h"
 
 using iqk::fail;

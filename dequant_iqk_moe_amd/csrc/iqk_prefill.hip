@@ -44,7 +44,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const int32_t* __r
                                                               int32_t sorted, int32_t* __restrict__ counts,
                                                               int32_t* __restrict__ offsets,
                                                               int32_t* __restrict__ perm, float* __restrict__ ynan,
-                                                              int32_t yout, int32_t yhalf) {
+                                                              int32_t yout) {
     __shared__ int32_t cur[kRouteMaxE];
     __shared__ int32_t part[kRouteThreads];
     __shared__ int32_t stage[kRouteStage];
@@ -78,13 +78,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const int32_t* __r
             while (m) {
                 const int pp = p0 + __builtin_ctzll(m);
                 m &= m - 1;
-                if (yhalf) {  // 0x7FFF is a quiet NaN in float16 and in bfloat16
-                    uint16_t* row = (uint16_t*)ynan + (int64_t)pp * yout;
-                    for (int o = lane; o < yout; o += 64) row[o] = 0x7FFFu;
-                } else {
-                    float* row = ynan + (int64_t)pp * yout;
-                    for (int o = lane; o < yout; o += 64) row[o] = __builtin_nanf("");
-                }
+                float* row = ynan + (int64_t)pp * yout;
+                for (int o = lane; o < yout; o += 64) row[o] = __builtin_nanf("");
             }
         }
     }
@@ -352,8 +347,7 @@ hipError_t launch_stream_write(void* buf, size_t bytes, uint32_t value, int runs
 hipError_t launch_route(const RouteLaunch& a, hipStream_t s) {
     if (a.E > kRouteMaxE) return hipErrorInvalidValue;
     hipLaunchKernelGGL(route_kernel, dim3(1), dim3(kRouteThreads), 0, s, a.ids, (int32_t)a.P, (int32_t)a.E,
-                       (int32_t)a.sorted, a.counts, a.offsets, a.perm, a.ynan, (int32_t)a.yout,
-                       a.yhalf);
+                       (int32_t)a.sorted, a.counts, a.offsets, a.perm, a.ynan, (int32_t)a.yout);
     return hipGetLastError();
 }
 

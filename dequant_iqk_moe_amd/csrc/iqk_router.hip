@@ -24,7 +24,7 @@
 // logits with weights divided by their sum needs those of the chosen alone.
 // No LDS, no barrier; all arithmetic is float32.  Bound: vector instructions
 // (about 45 per token and slot with L = 16, V = 16), not bytes.
-#include "iqk_internal.h"
+#include "iqk_layer.h"
 
 namespace iqk {
 namespace {
