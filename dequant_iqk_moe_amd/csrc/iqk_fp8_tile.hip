@@ -226,7 +226,12 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
                 if (o >= p.out) continue;
                 float v[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = acc[2 * h + (q >> 2)][j][q & 3];
+                for (int q = 0; q < 8; ++q) {
+                    v[q] = acc[2 * h + (q >> 2)][j][q & 3];
+                    // (the tile's last products are added right before: fused with the conversion to f16 they would
+                    // round once, where the others round twice, and a row's bits would depend on its place)
+                    if constexpr (YT == IQK_F16) asm("" : "+v"(v[q]));
+                }
                 store8<YT>(p.y, yrow * p.out + o, v, p.out - o);
             }
         }

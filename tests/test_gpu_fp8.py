@@ -392,3 +392,22 @@ def test_no_rows():
     assert q.moe_fp8(W, torch.empty(0, 64, device="cuda"), torch.empty(0, 2, dtype=torch.int32, device="cuda")).shape == (0, 2, 32)
     codes, scales = q.fp8_quantize(torch.empty(0, 64, device="cuda"))
     assert codes.shape == (0, 64) and scales.shape == (0, 1)
+
+
+@pytest.mark.parametrize("yt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,K", [(1, 272), (70, 528), (300, 400), (1100, 528)])
+def test_a_rows_bits_do_not_depend_on_its_place(T, K, yt):
+    """Rows in another order, and the same rows again, give the same bits."""
+    rng = np.random.default_rng(T + K)
+    k, E, N = 3, 4, 384
+    w, s = _weights(rng, E, N, K)
+    W, one = _device_weights(w, s), _device_weights(w[:1], s[:1])
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).cuda().to(torch.bfloat16)
+    ids = _dev(rng.integers(0, E, (T, k)).astype(np.int32))
+    y, d = q.moe_fp8(W, x, ids, out_dtype=DT[yt]), q.fp8_linear(one, x, out_dtype=DT[yt])
+    for _ in range(8):
+        order = torch.from_numpy(rng.permutation(T)).cuda()
+        again = q.moe_fp8(W, x[order].contiguous(), ids[order].contiguous(), out_dtype=DT[yt])
+        assert torch.equal(again, y[order]), (T, K, yt)
+        again = q.fp8_linear(one, x[order].contiguous(), out_dtype=DT[yt])
+        assert torch.equal(again, d[order]), (T, K, yt)
