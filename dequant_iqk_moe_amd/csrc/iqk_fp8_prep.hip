@@ -20,6 +20,14 @@ constexpr int kPrepWaves = kPrepThreads / 64;
 constexpr int kPrepBlocks = kPrepThreads / 16;  // blocks of 128 values per workgroup
 constexpr int kGroupE = 1024;                   // experts one workgroup counts, one per thread
 
+// A launch's x extent holds fewer than 2^32 threads, so many workgroups take
+// rows of 2^20 of a plane.
+dim3 plane(int64_t groups) {
+    const int64_t x = std::min<int64_t>(groups, 1 << 20);
+    return dim3((unsigned)x, (unsigned)((groups + x - 1) / x));
+}
+__device__ __forceinline__ int64_t plane_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // 16 lanes own one block of 128, 8 consecutive values each (rows are multiples
 // of 16 values, so a lane's 8 are all inside a row or all past its end).  Bound
 // by bytes: 8192 x 4096 bfloat16 (102 MB read and written) in 18.5 us = 5.5
@@ -44,7 +52,7 @@ __device__ __forceinline__ void quantize_blocks(const Fp8QuantLaunch& p, int64_t
 
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(Fp8QuantLaunch p) {
-    quantize_blocks<DT>(p, blockIdx.x, 256);
+    quantize_blocks<DT>(p, plane_index(), 256);
 }
 
 // Inclusive sum over the workgroup of one value per thread.
@@ -125,8 +133,9 @@ template <int DT>
 __global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p, Fp8QuantLaunch q) {
     __shared__ int32_t cnt[kGroupE];
     __shared__ uint64_t part[kPrepWaves];
-    if ((int)blockIdx.x < p.slices) {
-        const int h = blockIdx.x;
+    const int64_t group = plane_index();
+    if (group < p.slices) {
+        const int h = (int)group;
         const int64_t p0 = h * p.slice, p1 = min(p0 + p.slice, p.P);
         count_slice(p, p0, p1, cnt);
         if (p.slices == 1) {
@@ -137,7 +146,7 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p
         }
         return;
     }
-    if constexpr (DT != IQK_E4M3) quantize_blocks<DT>(q, (int64_t)blockIdx.x - p.slices, kPrepThreads);
+    if constexpr (DT != IQK_E4M3) quantize_blocks<DT>(q, group - p.slices, kPrepThreads);
 }
 
 __global__ __launch_bounds__(kPrepThreads) void fp8_place_kernel(Fp8GroupLaunch p) {
@@ -186,8 +195,7 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_tiles_kernel(Fp8GroupLaunch 
 hipError_t launch_fp8_quantize(const Fp8QuantLaunch& a, hipStream_t s) {
     const int64_t blocks128 = a.rows * ((a.n + kBlock - 1) / kBlock);
     by_float(a.x_dtype, [&](auto dt) {
-        hipLaunchKernelGGL((fp8_quantize_kernel<decltype(dt)::value>), dim3((unsigned)((blocks128 + 15) / 16)), dim3(256),
-                           0, s, a);
+        hipLaunchKernelGGL((fp8_quantize_kernel<decltype(dt)::value>), plane((blocks128 + 15) / 16), dim3(256), 0, s, a);
     });
     return hipGetLastError();
 }
@@ -213,7 +221,7 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
     }
     g.slices = fp8_group_slices(g.P);
     g.slice = (g.P + g.slices - 1) / g.slices;
-    const dim3 grid((unsigned)(g.slices + qb));
+    const dim3 grid = plane(g.slices + qb);
     if (quantize) {
         by_float(q.x_dtype, [&](auto dt) {
             hipLaunchKernelGGL((fp8_prep_kernel<decltype(dt)::value>), grid, dim3(kPrepThreads), 0, s, g, q);

@@ -383,6 +383,7 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
                        (int)a.E, (int)run, a.offsets, a.perm, a.tiles, a.y};
     const int64_t total = tiles * ((ntn + run - 1) / run);
+    if (total >= (int64_t)(UINT32_MAX / (64 * Sh::kWaves))) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * Sh::kWaves);
     if (a.n % kBlock) hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, true>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, false>), grid, block, 0, s, p);

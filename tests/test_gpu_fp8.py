@@ -394,6 +394,23 @@ def test_no_rows():
     assert codes.shape == (0, 64) and scales.shape == (0, 1)
 
 
+def test_quantize_more_blocks_than_one_grid_row():
+    announce("quantize, 69 GB of values")
+    M, K = 1 << 24, 2064  # 2^24 rows of 17 blocks: 2^32 threads and more at 16 a block
+    if torch.cuda.mem_get_info()[0] < 120e9:
+        pytest.skip("needs 106 GB")
+    x = torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+    rows = torch.tensor([0, 1, M // 2, M - 1], device="cuda")
+    some = torch.randn(4, K, device="cuda", dtype=torch.float32).to(torch.bfloat16)
+    x[rows] = some
+    codes, scales = q.fp8_quantize(x)
+    few, few_scales = q.fp8_quantize(some)
+    assert torch.equal(codes[rows], few) and torch.equal(scales[rows], few_scales)
+    assert torch.equal(codes[M - 1000:M - 1], torch.zeros_like(codes[M - 1000:M - 1]))
+    del x, codes, scales
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("yt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("T,K", [(1, 272), (70, 528), (300, 400), (1100, 528)])
 def test_a_rows_bits_do_not_depend_on_its_place(T, K, yt):
