@@ -28,7 +28,7 @@ constexpr int64_t kMaxE = 16384;
 constexpr int64_t kMaxValues = 1LL << 40;  // activations of one call
 
 int check_router(const void* logits, int dtype, int64_t T, int64_t E, int k, int scoring, int renorm, float scale) {
-    if (T < 0 || T > (1LL << 30)) return fail(IQK_E_ARG, "T = %lld outside [0, 2^30]", (long long)T);
+    if (T < 0 || T > kMaxRows) return fail(IQK_E_ARG, "T = %lld outside [0, 2^24]", (long long)T);
     if (E <= 0 || E > 1024) return fail(IQK_E_ARG, "expert count %lld outside [1, 1024]", (long long)E);
     if (k <= 0 || k > 64 || k > E) return fail(IQK_E_ARG, "k = %d outside [1, min(64, E)]", k);
     if (!is_float(dtype)) return fail(IQK_E_ARG, "logits must be IQK_F32, IQK_F16 or IQK_BF16");

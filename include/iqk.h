@@ -365,7 +365,7 @@ int iqk_stream_write(void* buf, size_t bytes, uint32_t value, int runs, void* st
  * all gets ids -1 and weights zero.  A row with a NaN logit, and with +inf
  * under IQK_SOFTMAX, and every row under a NaN bias, gets ids -1 and weights
  * NaN (the routed calls make such rows NaN).
- * Limits: E <= 1024, k <= min(64, E), n_group <= 64, T <= 2^30 (IQK_E_ARG). */
+ * Limits: E <= 1024, k <= min(64, E), n_group <= 64, T <= 2^24 (IQK_E_ARG). */
 int iqk_router_topk(const void* logits, int dtype, int64_t T, int64_t E, int k, int scoring, const float* bias,
                     int n_group, int topk_group, int group_top, int renorm, float scale,
                     int32_t* ids, float* weights, void* stream);
