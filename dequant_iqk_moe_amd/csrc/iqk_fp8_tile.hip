@@ -350,6 +350,9 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
                 for (int t = kT - kLag; t < kT; ++t) add(t, fp);
 #pragma unroll
                 for (int t = 0; t < kRing; ++t) d[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+                // (the next tile's first sums add 0 * fp, which is not zero where a scale of this tile is infinite)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) fp[j] = 0.f;
             }
             store_tile();
 #pragma unroll

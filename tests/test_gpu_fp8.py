@@ -428,3 +428,19 @@ def test_a_rows_bits_do_not_depend_on_its_place(T, K, yt):
         assert torch.equal(again, y[order]), (T, K, yt)
         again = q.fp8_linear(one, x[order].contiguous(), out_dtype=DT[yt])
         assert torch.equal(again, d[order]), (T, K, yt)
+
+
+@pytest.mark.parametrize("yt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(3, 300, 272), (20, 300, 272), (40, 1000, 272), (300, 5000, 400), (4096, 8192, 256)])
+def test_a_weight_scale_reaches_its_rows_only(M, N, K, yt):
+    """A NaN and an infinite weight scale in the depth's last block, at the first weight rows."""
+    rng = np.random.default_rng(M)
+    w, s = _weights(rng, 1, N, K)
+    x = torch.from_numpy(rng.standard_normal((M, K)).astype(np.float32)).cuda().to(torch.bfloat16)
+    clean = q.fp8_linear(_device_weights(w, s), x, out_dtype=DT[yt])
+    for value in (np.nan, np.inf):
+        bad = s.copy()
+        bad[0, 0, -1] = value
+        y = q.fp8_linear(_device_weights(w, bad), x, out_dtype=DT[yt])
+        assert torch.equal(y[:, 128:], clean[:, 128:])
+        assert not torch.isfinite(y[:, :128]).any()
