@@ -407,8 +407,16 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
     if constexpr (!F32) {
         if (tile == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, GROUPED>(a, s);
     }
-    if constexpr (GROUPED) return tile_launch<128, 256, 64, 64, 3, F32, YT, true>(a, s);
-    else return tile_launch<128, 128, 64, 64, 2, F32, YT, false>(a, s);
+    if constexpr (GROUPED) {
+        // A CU holds one workgroup of 128 x 256 tiles or two of 128 x 128 ones, which take as long together.  The
+        // small ones are taken where each has a CU to itself, or where they fit at once and the others do not (16
+        // experts of 310 x 2960, 1000 rows each: 62 us against 81; float32 results of 312 x 1456, 433 rows: 34
+        // against 42; else 171 against 165 for 64 experts of 2048 x 4096, 96 rows each).
+        const int64_t rows = a.M / 128 + std::min(a.E, a.M) / 2;
+        const int64_t small = rows * ((a.out + 127) / 128), large = rows * ((a.out + 255) / 256);
+        if (small <= 256 || (large > 256 && small <= 512)) return tile_launch<128, 128, 64, 64, 2, F32, YT, true>(a, s);
+        return tile_launch<128, 256, 64, 64, 3, F32, YT, true>(a, s);
+    } else return tile_launch<128, 128, 64, 64, 2, F32, YT, false>(a, s);
 }
 
 }  // namespace

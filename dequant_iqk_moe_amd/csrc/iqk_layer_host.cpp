@@ -92,15 +92,18 @@ size_t quantized_bytes(int64_t rows, int64_t n) {
 // without tiles.
 constexpr int64_t kRowsPass = 32;
 // Whether the routed product takes each pair by itself: one launch without
-// grouping, an expert's weights read once for each of its pairs.  Measured, it
-// streams weights at about 4.0 TB/s, the grouped product at 5.2 TB/s over the
-// distinct experts after about 9 us for grouping (256 experts of 4096 x 4096,
-// top-6: 1 token 25 us against 26, 2 tokens 47 against 45; 8 experts, top-2: 4
-// tokens 28 against 35, 8 tokens 49 against 36).
+// grouping, an expert's weights read once for each of its pairs.  Measured,
+// each of its workgroups (16 weight rows) costs 3.3 ns of the card and its
+// weights stream at 5.8 TB/s beside that; the grouped product reads the
+// distinct experts at 5.2 TB/s after about 9 us for grouping (256 experts of
+// 4096 x 4096, top-6: 1 token 25 us against 26, 2 tokens 47 against 45; 8
+// experts, top-2: 4 tokens 28 against 35, 8 tokens 49 against 36; 256 experts
+// of 1589 x 256, top-4: 4 tokens 12 against 17, 16 tokens 28 against 18).
 bool pair_by_pair(int64_t P, int64_t E, int64_t out, int64_t n) {
     if (P > 4096 || !iqk::fp8_few_fits(1, n)) return false;
     const double us = 1e-6 * (double)(out * n);  // an expert's bytes at 1 TB/s
-    return (double)P * us / 4.0 <= (double)std::min(P, E) * us / 5.2 + 9.0;
+    const double pairs = (double)P * (3.3e-3 * (double)((out + 15) / 16) + us / 5.8);
+    return pairs <= (double)std::min(P, E) * us / 5.2 + 9.0;
 }
 
 // Quantizes the rows of a product's x into `ws` and points L at the result.
