@@ -678,6 +678,10 @@ def fp8_linear_workspace_bytes(w: Fp8Weights, M: int) -> int:
     return _fp8_linear_bytes(w.experts, w.out, w.in_features, M)
 
 
+def _round256(nbytes: int) -> int:
+    return -(-nbytes // 256) * 256
+
+
 def _workspace(workspace: torch.Tensor | None, nbytes: int, device, stream):
     """(workspace, pointer, size): the caller's, or a new one where the call needs any."""
     if workspace is None:
@@ -701,8 +705,10 @@ def fp8_linear(w: Fp8Weights, x: torch.Tensor, x_scales: torch.Tensor | None = N
         y = _empty((*x.shape[:-1], w.out), out_dtype, x.device, stream)
     if y.dtype not in _DT:
         raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
-    ws, wp, nbytes = _workspace(workspace, 0 if xdt == _E4M3 else fp8_linear_workspace_bytes(w, M), x.device,
-                               stream)
+    need = fp8_linear_workspace_bytes(w, M)
+    if xdt == _E4M3 and need:  # (codes are there already)
+        need -= _round256(M * n) + _round256(M * (-(-n // 128)) * 4)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
     cw = w._c()
     _check(_lib.iqk_fp8_linear(ctypes.byref(cw), xp, xdt, sp, M, wp, nbytes, _dev(y, "y", None, M * w.out),
                                _DT[y.dtype], _stream(stream)))

@@ -46,6 +46,7 @@ struct TileParams {
     int64_t M;
     int out, n, k, x_slots, E;
     int run;  // weight tiles a workgroup takes one after the other
+    int parts;  // SPLIT: of the depth, part i into the i-th array of sums at y
     const int32_t *offsets, *perm, *tiles;  // grouped: tiles[e] = TM-row tiles of x before expert e
     void* y;
 };
@@ -73,7 +74,7 @@ struct TileShape {
     static_assert(S * kStage <= 160 * 1024, "LDS");
 };
 
-template <int TM, int TN, int WM, int WN, int S, int YT, bool GROUPED, bool EXACT, bool PART>
+template <int TM, int TN, int WM, int WN, int S, int YT, bool GROUPED, bool EXACT, bool PART, bool SPLIT>
 __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(TileParams p) {
     using Sh = TileShape<TM, TN, WM, WN, S>;
     constexpr int kI = Sh::kI, kJ = Sh::kJ, kG = Sh::kG;
@@ -82,6 +83,9 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     const int li = lane & 15, g = lane >> 4;
     const int nb = (p.n + kBlock - 1) / kBlock, nob = (p.out + kBlock - 1) / kBlock;
     const int ntn = (p.out + TN - 1) / TN, runs = (ntn + p.run - 1) / p.run;
+
+    // the blocks of the depth this workgroup takes
+    const int b0 = SPLIT ? (int)blockIdx.y * nb / p.parts : 0, b1 = SPLIT ? ((int)blockIdx.y + 1) * nb / p.parts : nb;
 
     // which tile of x and run of weight tiles: those of one XCD (workgroups b with equal b % 8) are neighbours
     int e = 0, n0;
@@ -145,7 +149,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     const float* sptr = p.sx + row_of(min(su, TM - 1)) * nb;
     // the next block to copy: block cb of the weight tile at row cn
     const int nend = min(n0 + p.run * TN, p.out);
-    int cb = 0, cn = n0;
+    int cb = b0, cn = n0;
     const uint8_t* wbase;
     auto weight_tile = [&]() {
         wbase = p.W + ((int64_t)e * p.out + cn) * p.n;
@@ -178,8 +182,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         }
     };
     auto advance = [&]() {
-        if (++cb < nb) return;
-        cb = 0;
+        if (++cb < b1) return;
+        cb = b0;
         if (cn + TN < nend) {
             cn += TN;
             weight_tile();
@@ -219,6 +223,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
             const int i = wm + 16 * j + li;
             if (m0 + i >= count) continue;
             int64_t yrow = m0 + i;
+            if constexpr (SPLIT) yrow += blockIdx.y * p.M;
             if constexpr (GROUPED) yrow = pair_of(i);
 #pragma unroll
             for (int h = 0; h < kI / kG; ++h) {
@@ -255,7 +260,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
     };
 
     constexpr int kBehind = (S - 2) * Sh::kCopies;  // copies that may still be on their way when a block is published
-    const int steps = nb * ((nend - n0 + TN - 1) / TN);
+    const int steps = (b1 - b0) * ((nend - n0 + TN - 1) / TN);
 #pragma unroll
     for (int b = 0; b < S - 1; ++b) {
 #pragma unroll
@@ -344,7 +349,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
         advance();
         publish<kBehind>();
         slot = slot == S - 1 ? 0 : slot + 1;
-        if (++b == nb) {  // (after the wait, so that the stores are on their way while the next block is multiplied)
+        if (++b == b1 - b0) {  // (after the wait, so that the stores are on their way while the next block is multiplied)
             if constexpr (!EXACT) {
 #pragma unroll
                 for (int t = kT - kLag; t < kT; ++t) add(t, fp);
@@ -369,6 +374,36 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN)) void fp8_tile_kernel(Ti
 
 constexpr int64_t kMaxRun = 2;
 
+// Joins the parts' sums in their order: the same result every time.
+constexpr int kJoinThreads = 256;
+template <int YT>
+__global__ __launch_bounds__(kJoinThreads) void fp8_join_kernel(const float* sums, int parts, int64_t count, void* y) {
+    const int64_t i = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+    if (i >= count) return;
+    float v = sums[i];
+    for (int part = 1; part < parts; ++part) v += sums[part * count + i];
+    store_y<YT>(y, i, v);
+}
+
+template <int YT>
+hipError_t split_launch(const Fp8Launch& a, int parts, hipStream_t s) {
+    using Sh = TileShape<64, 64, 16, 32, 4>;
+    constexpr bool F32 = YT == IQK_F32;
+    const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
+                       (int)a.E, 1, parts, nullptr, nullptr, nullptr, a.sums};
+    const int64_t tiles = (a.M + 63) / 64 * ((a.out + 63) / 64), count = a.M * a.out;
+    const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)parts), block(64 * Sh::kWaves);
+    if (a.n % kBlock)
+        hipLaunchKernelGGL((fp8_tile_kernel<64, 64, 16, 32, 4, IQK_F32, false, F32, true, true>), grid, block, 0, s, p);
+    else
+        hipLaunchKernelGGL((fp8_tile_kernel<64, 64, 16, 32, 4, IQK_F32, false, F32, false, true>), grid, block, 0, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((fp8_join_kernel<YT>), dim3((unsigned)((count + kJoinThreads - 1) / kJoinThreads)),
+                       dim3(kJoinThreads), 0, s, a.sums, parts, count, a.y);
+    return hipGetLastError();
+}
+
 // TM x TN tiles by waves of WM x WN, S stages
 template <int TM, int TN, int WM, int WN, int S, bool EXACT, int YT, bool GROUPED>
 hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
@@ -384,12 +419,12 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     int64_t run = 1;
     while ((TM <= 64 || !GROUPED) && run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
-                       (int)a.E, (int)run, a.offsets, a.perm, a.tiles, a.y};
+                       (int)a.E, (int)run, 1, a.offsets, a.perm, a.tiles, a.y};
     const int64_t total = tiles * ((ntn + run - 1) / run);
     if (total >= (int64_t)(UINT32_MAX / (64 * Sh::kWaves))) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * Sh::kWaves);
-    if (a.n % kBlock) hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, false>), grid, block, 0, s, p);
+    if (a.n % kBlock) hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, true, false>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((fp8_tile_kernel<TM, TN, WM, WN, S, YT, GROUPED, EXACT, false, false>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
@@ -402,7 +437,10 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
         if (tile == 32) return tile_launch<32, 128, 32, 32, 3, true, YT, true>(a, s);
         if (tile == 64) return tile_launch<64, 128, 32, 64, 2, true, YT, true>(a, s);
     } else {
-        if (tile == 64) return tile_launch<64, 64, 16, 32, 4, F32, YT, false>(a, s);
+        if (tile == 64) {
+            const int parts = fp8_depth_parts(a.M, a.out, a.n);
+            return parts > 1 ? split_launch<YT>(a, parts, s) : tile_launch<64, 64, 16, 32, 4, F32, YT, false>(a, s);
+        }
     }
     if constexpr (!F32) {
         if (tile == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, GROUPED>(a, s);
@@ -436,6 +474,23 @@ int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, 
     // the largest is taken that gives most of the 256 CUs a tile
     if (!exact && count(256) >= 160) return 256;
     return count(128) >= 160 ? 128 : 64;
+}
+
+// A block of 64 x 64 tiles takes about 0.4 us however few tiles there are, so a long depth is split while each part
+// of each tile has a CU to itself (with two parts per CU 2017 x 117 x 5136 takes 25 us instead of 23) and four blocks,
+// where that saves more than 10 us: the launch that joins the sums costs about 3 us of the card and as much of the
+// host.  141 x 261 x 7920, float32: 19.5 us against 43; 308 x 1099 x 6880: 25 against 32; 64 x 4096 x 4096, not split:
+// 17 against 20.
+int fp8_depth_parts(int64_t M, int64_t out, int64_t n) {
+    if (fp8_tile_rows((double)M, M, out, false, false) != 64) return 1;
+    const int64_t tiles = (M + 63) / 64 * ((out + 63) / 64), nb = (n + kBlock - 1) / kBlock;
+    const int64_t parts = std::min<int64_t>({256 / tiles, nb / 4, 16});
+    return parts > 1 && 0.4 * (double)(nb - (nb + parts - 1) / parts) > 10.0 ? (int)parts : 1;
+}
+
+size_t fp8_sums_bytes(int64_t M, int64_t out, int64_t n) {
+    const int parts = fp8_depth_parts(M, out, n);
+    return parts > 1 ? (size_t)(parts * M * out) * 4 : 0;
 }
 
 hipError_t launch_fp8_tile(const Fp8Launch& a, int tile, hipStream_t s) {

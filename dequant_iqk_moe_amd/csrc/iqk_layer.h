@@ -67,6 +67,7 @@ struct Fp8Launch {
     const int32_t *ids, *offsets, *perm, *tiles;
     void* y;  // [M, out] of y_dtype
     int y_dtype;
+    float* sums;  // dense, where fp8_depth_parts() > 1: fp8_sums_bytes()
 };
 
 hipError_t launch_router(const RouterLaunch& a, hipStream_t s);
@@ -84,6 +85,9 @@ hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s);
 hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s);
 // e4m3 x, many rows; tile = fp8_tile_rows()
 int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact);
+// parts of the depth that workgroups of their own take in the dense product, and the bytes of their sums
+int fp8_depth_parts(int64_t M, int64_t out, int64_t n);
+size_t fp8_sums_bytes(int64_t M, int64_t out, int64_t n);
 hipError_t launch_fp8_tile(const Fp8Launch& a, int tile, hipStream_t s);
 
 }  // namespace iqk

@@ -91,6 +91,11 @@ size_t quantized_bytes(int64_t rows, int64_t n) {
 // Rows of x up to which the dense product passes over the weights once
 // without tiles.
 constexpr int64_t kRowsPass = 32;
+// Workspace of a tiled dense product's partial sums (0: none).
+size_t dense_sums_bytes(int64_t M, int64_t out, int64_t n) {
+    return M > kRowsPass ? round256(iqk::fp8_sums_bytes(M, out, n)) : 0;
+}
+
 // Whether the routed product takes each pair by itself: one launch without
 // grouping, an expert's weights read once for each of its pairs.  Measured,
 // each of its workgroups (16 weight rows) costs 3.3 ns of the card and its
@@ -174,7 +179,7 @@ int iqk_fp8_linear_workspace(const iqk_fp8_weights* w, int64_t M, size_t* bytes)
     if (rc) return rc;
     if (M < 0 || M > kMaxRows) return fail(IQK_E_ARG, "M = %lld outside [0, 2^24]", (long long)M);
     if (M * w->in > kMaxValues) return fail(IQK_E_ARG, "M * in exceeds 2^40");
-    *bytes = iqk::fp8_few_fits(M, w->in) ? 0 : quantized_bytes(M, w->in);
+    *bytes = iqk::fp8_few_fits(M, w->in) ? 0 : dense_sums_bytes(M, w->out, w->in) + quantized_bytes(M, w->in);
     return ok();
 }
 
@@ -190,16 +195,17 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
     if (rc) return rc;
     const bool quantize = x_dtype != IQK_E4M3;
     const bool few = iqk::fp8_few_fits(M, w->in);
-    rc = check_workspace(workspace, ws_bytes, quantize && !few ? quantized_bytes(M, w->in) : 0);
+    const size_t sums = few ? 0 : dense_sums_bytes(M, w->out, w->in);
+    rc = check_workspace(workspace, ws_bytes, sums + (quantize && !few ? quantized_bytes(M, w->in) : 0));
     if (rc) return rc;
     hipStream_t s = (hipStream_t)stream;
     iqk::Fp8Launch L{1, w->out, w->in, (const uint8_t*)w->codes, w->scales, x, x_dtype, x_scales, M, 1, 1,
-                     nullptr, nullptr, nullptr, nullptr, y, y_dtype};
+                     nullptr, nullptr, nullptr, nullptr, y, y_dtype, (float*)workspace};
     hipError_t e;
     if (few) {
         e = iqk::launch_fp8_few(L, s);
     } else {
-        if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace, s)) != hipSuccess)
+        if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace + sums, s)) != hipSuccess)
             return hip_fail(e, "quantize launch");
         e = M <= kRowsPass ? iqk::launch_fp8_rows(L, (int)((M + 15) / 16), s)
                            : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows((double)M, M, w->out, false, y_dtype == IQK_F32), s);
@@ -243,7 +249,7 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
     const int64_t E = w->experts, P = T * k;
     hipStream_t s = (hipStream_t)stream;
     iqk::Fp8Launch L{E, w->out, w->in, (const uint8_t*)w->codes, w->scales, x, x_dtype, x_scales, P, x_slots, k,
-                     ids, nullptr, nullptr, nullptr, y, y_dtype};
+                     ids, nullptr, nullptr, nullptr, y, y_dtype, nullptr};
     hipError_t e;
     if (pair_by_pair(P, E, w->out, w->in)) {
         e = iqk::launch_fp8_few(L, s);

@@ -416,8 +416,10 @@ int iqk_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, uint8_
  * x: device [M, in], IQK_E4M3 with x_scales [M, ceil(in / 128)], or a float
  * type with x_scales null, which the call quantizes as iqk_fp8_quantize does.
  * workspace (16-byte aligned, iqk_fp8_linear_workspace bytes, 0 for a few
- * rows) holds the quantized x; it may be null for IQK_E4M3 x and where 0
- * bytes are needed.  Accuracy against the product
+ * rows) holds sums of parts of the depth, where few tiles have a long one,
+ * and the quantized x, ceil-to-256(M * in) + ceil-to-256(4 * M * ceil(in /
+ * 128)) bytes of it that IQK_E4M3 x does without; it may be null where 0 bytes
+ * are needed.  Accuracy against the product
  * of the same codes and scales: 2e-6 in norm for a float32 y; 16-bit results
  * are off by their rounding.  A NaN or infinity in a row of x makes that row of
  * y NaN or infinite and no other.  x 16-byte aligned; M <= 2^24. */

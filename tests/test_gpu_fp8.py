@@ -444,3 +444,26 @@ def test_a_weight_scale_reaches_its_rows_only(M, N, K, yt):
         y = q.fp8_linear(_device_weights(w, bad), x, out_dtype=DT[yt])
         assert torch.equal(y[:, 128:], clean[:, 128:])
         assert not torch.isfinite(y[:, :128]).any()
+
+
+@pytest.mark.parametrize("M,N,K", [(33, 16, 4096), (40, 33, 2832), (60, 173, 7552), (141, 261, 7920), (700, 1052, 3696),
+                                   (64, 64, 1 << 16), (1030, 70, 2064)])
+def test_linear_of_a_long_depth(M, N, K):
+    """Few tiles of a long depth: sums of its parts, joined."""
+    rng = np.random.default_rng(M + N + K)
+    w, s = _weights(rng, 1, N, K)
+    W = _device_weights(w, s)
+    for xt, yt in (("bf16", "f32"), ("f32", "bf16"), ("bf16", "f16")):
+        t, x = _activations(rng, M, K, xt)
+        rc, rs = layer.quantize(x)
+        buf = torch.full((M * N + 64,), 7.0, dtype=DT[yt], device="cuda")
+        y = q.fp8_linear(W, t, y=buf[1:1 + M * N].view(M, N))
+        assert _off(y, layer.linear(w[0], s[0], rc, rs)) <= BAR[yt], (xt, yt)
+        assert (buf[0] == 7) and (buf[1 + M * N:] == 7).all()
+        ws = torch.full((q.fp8_linear_workspace_bytes(W, M),), 0xFF, dtype=torch.uint8, device="cuda")
+        assert torch.equal(q.fp8_linear(W, t, out_dtype=DT[yt], workspace=ws), y)
+        codes, scales = q.fp8_quantize(t)
+        assert torch.equal(q.fp8_linear(W, codes, scales, out_dtype=DT[yt]), y)
+        t[M // 2, K - 1] = float("nan")
+        bad = torch.isnan(q.fp8_linear(W, t, out_dtype=DT[yt]))
+        assert bad[M // 2].all() and int(bad.sum()) == N
