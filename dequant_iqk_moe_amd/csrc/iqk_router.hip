@@ -22,8 +22,10 @@
 // over the row (DPP), one ballot, and a new best in the lane that won.  Scores
 // are computed only for the experts whose score something needs: a choice by
 // logits with weights divided by their sum needs those of the chosen alone.
-// No LDS, no barrier; all arithmetic is float32.  Bound: vector instructions
-// (about 45 per token and slot with L = 16, V = 16), not bytes.
+// No LDS, no barrier; all arithmetic is float32.  Bound: vector instructions,
+// not bytes: 16384 tokens of 256 bfloat16 logits, k = 6, take 9.6 us where
+// their 9 MB would take 1.9; one token 5.7 us, a launch and a chain of k
+// maxima.
 #include "iqk_layer.h"
 
 namespace iqk {
@@ -329,7 +331,11 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterLaunch 
 // without renorm: dl_e = p_e (ds_e - sum_j ds_j p_j) for every expert, with
 // renorm the second term is zero and w is the softmax of the chosen logits
 // alone: dl_j = w_j (g_j - sum_m g_m w_m).  Only softmax without renorm reads
-// the whole row of logits; the others read the chosen ones.
+// the whole row of logits; the others read the chosen ones.  One wave owns one
+// token, lane e % 64 the logit e, so rows are read and written whole and the
+// sums stay in the wave.  512 tokens of 256 float32 logits: 3.6 us, a launch;
+// 8191 of 160 bfloat16 logits: 5.4 us for 5 MB (1.2 us at a copy's rate), the
+// rest the start of 2048 workgroups and the chain of a row's sums.
 template <int V, int DT>
 __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(RouterGradLaunch p) {
     const int lane = threadIdx.x & 63;
