@@ -82,6 +82,17 @@ def test_linear_refuses(change, code):
     assert _linear(_w(), **change) == code
 
 
+def test_linear_of_a_long_depth_wants_its_sums():
+    """Codes need no memory for codes, but that of the sums of the depth's parts."""
+    w = _w(in_=1 << 14)
+    assert _linear(w, dtype=E4M3, xs=P, ws=None, nbytes=0) == E_SIZE
+    need = ctypes.c_size_t()
+    assert q._lib.iqk_fp8_linear_workspace(ctypes.byref(w), 100, ctypes.byref(need)) == 0
+    codes = 100 * (1 << 14) + 100 * 128 * 4
+    assert need.value > codes and (need.value - codes) % (100 * 256 * 4) == 0
+    assert _linear(w, nbytes=need.value - 1) == E_SIZE
+
+
 def test_linear_takes_one_expert_and_no_rows():
     assert _linear(_w(experts=2)) == E_ARG
     assert _linear(_w(), M=0, x=None, y=None, ws=None, nbytes=0) == 0
