@@ -462,11 +462,19 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
 int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact) {
     auto count = [&](int64_t t) { return (M + t - 1) / t * ((out + t - 1) / t); };
     if (grouped) {
-        // rows a tile holds: what most experts have (their counts spread like a square root)
-        const double most = rows_per_expert + 2.0 * std::sqrt(rows_per_expert);
-        if (most <= 16) return 16;
-        if (most <= 32) return 32;
-        if (most <= 64) return 64;
+        // A block of a small tile takes its time however few there are, less the smaller it is: where workgroups of 16
+        // or of 32 rows about have a CU each, they are taken (8 experts of 1024 x 4096, 37 rows each: tiles of 16, 32
+        // and 64 rows 24, 28 and 37 us; 16 of 1024 x 2048, 50 rows each: 32 rows 23, 64 rows 27, 128 rows 32).
+        const double experts = std::min((double)M, (double)M / rows_per_expert);
+        auto groups = [&](int64_t t) { return ((double)(M / t) + experts / 2) * (double)((out + 127) / 128); };
+        if (groups(16) <= 192) return 16;
+        if (groups(32) <= 288) return 32;
+        // Else the rows a tile holds are what most experts have (their counts spread like a square root; 64 experts of
+        // 4096 x 2048, 24 rows each: tiles of 32 rows 127 us, of 64 rows 145; 128 of 2048 x 2048, 26 rows: the same).
+        const double spread = std::sqrt(rows_per_expert);
+        if (rows_per_expert + 2 * spread <= 16) return 16;
+        if (rows_per_expert + spread <= 32) return 32;
+        if (rows_per_expert + 2 * spread <= 64) return 64;
         // 64 experts of 2048 x 4096, 384 rows each: 256-row tiles 333 us, 128-row ones 380; 96 rows each: 294 and 271
         return !exact && rows_per_expert >= 192 && count(256) >= 160 ? 256 : 128;
     }

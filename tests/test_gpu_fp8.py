@@ -467,3 +467,15 @@ def test_linear_of_a_long_depth(M, N, K):
         t[M // 2, K - 1] = float("nan")
         bad = torch.isnan(q.fp8_linear(W, t, out_dtype=DT[yt]))
         assert bad[M // 2].all() and int(bad.sum()) == N
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(32, 2, 8, 5000, 272), (80, 2, 8, 5000, 144), (160, 2, 8, 5000, 272),
+                                       (400, 2, 8, 5000, 272), (800, 2, 8, 1000, 528), (1200, 2, 8, 5000, 144)])
+def test_moe_tile_sizes(T, k, E, N, K):
+    """Enough workgroups that the tile follows the rows per expert: 16, 32, 64, 128 (both widths) and 256."""
+    rng = np.random.default_rng(T + N)
+    w, s = _weights(rng, E, N, K)
+    ids = rng.integers(0, E, (T, k)).astype(np.int32)
+    ids[0, 0], ids[-1, -1] = -1, E
+    for xt, yt in (("bf16", "f32"), ("f32", "bf16"), ("bf16", "f16")):
+        _moe_check(w, s, ids, 1, xt, yt, rng)
