@@ -8,11 +8,11 @@
 // sums with the product of the two scales, so a matrix instruction's
 // accumulator is never carried from one block to the next.
 //
-// EXACT widens the fragments to float16 in registers and uses
-// v_mfma_f32_16x16x32_f16; otherwise one v_mfma_scale_f32_16x16x128_f8f6f4
-// (both scales 2^0) takes a whole block.
+// EXACT (float32 and float16 results) widens the fragments to float16 in
+// registers and uses v_mfma_f32_16x16x32_f16; otherwise one
+// v_mfma_scale_f32_16x16x128_f8f6f4 (both scales 2^0) takes a whole block.
 //
-// Measured, with 16-bit results: 8192 x 4096 x 4096 in 133 us = 2.06 PFLOP/s,
+// Measured, with bfloat16 results: 8192 x 4096 x 4096 in 133 us = 2.06 PFLOP/s,
 // matrix pipes 41 % busy, where the same instructions with the four
 // multiply-adds each needs, and nothing else, run at 3.1 to 3.9 PFLOP/s.  A
 // block of 256 x 256 tiles takes 3540 cycles of a CU for 2048 of its matrix
@@ -20,7 +20,7 @@
 // barrier, and two waves per SIMD that share its pipe at 40 cycles per
 // instruction of 32.  More stages do not fit its LDS, and smaller tiles, which
 // would leave room for them, move more bytes per product (128 x 256 in three
-// stages 166 us).  float32 results: 290 us = 0.95 PFLOP/s.
+// stages 166 us).  float32 results: 290 us = 0.95 PFLOP/s; float16: 256.
 //
 // Few rows per expert: bytes of the weights.  The copies need no registers, so
 // as many are in flight as the LDS holds, and each is whole 128-byte lines,
@@ -388,15 +388,15 @@ __global__ __launch_bounds__(kJoinThreads) void fp8_join_kernel(const float* sum
 template <int YT>
 hipError_t split_launch(const Fp8Launch& a, int parts, hipStream_t s) {
     using Sh = TileShape<64, 64, 16, 32, 4>;
-    constexpr bool F32 = YT == IQK_F32;
+    constexpr bool EXACT = exact_sums(YT);
     const TileParams p{a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, a.k, a.x_slots,
                        (int)a.E, 1, parts, nullptr, nullptr, nullptr, a.sums};
     const int64_t tiles = (a.M + 63) / 64 * ((a.out + 63) / 64), count = a.M * a.out;
     const dim3 grid((unsigned)((tiles + 7) / 8 * 8), (unsigned)parts), block(64 * Sh::kWaves);
     if (a.n % kBlock)
-        hipLaunchKernelGGL((fp8_tile_kernel<64, 64, 16, 32, 4, IQK_F32, false, F32, true, true>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((fp8_tile_kernel<64, 64, 16, 32, 4, IQK_F32, false, EXACT, true, true>), grid, block, 0, s, p);
     else
-        hipLaunchKernelGGL((fp8_tile_kernel<64, 64, 16, 32, 4, IQK_F32, false, F32, false, true>), grid, block, 0, s, p);
+        hipLaunchKernelGGL((fp8_tile_kernel<64, 64, 16, 32, 4, IQK_F32, false, EXACT, false, true>), grid, block, 0, s, p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((fp8_join_kernel<YT>), dim3((unsigned)((count + kJoinThreads - 1) / kJoinThreads)),
@@ -430,7 +430,7 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
 
 template <int YT, bool GROUPED>
 hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
-    constexpr bool F32 = YT == IQK_F32;
+    constexpr bool EXACT = exact_sums(YT);
     if constexpr (GROUPED) {
         // few rows per expert: the weights stream through, exact sums cost nothing there
         if (tile == 16) return tile_launch<16, 128, 16, 32, 4, true, YT, true>(a, s);
@@ -439,10 +439,10 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
     } else {
         if (tile == 64) {
             const int parts = fp8_depth_parts(a.M, a.out, a.n);
-            return parts > 1 ? split_launch<YT>(a, parts, s) : tile_launch<64, 64, 16, 32, 4, F32, YT, false>(a, s);
+            return parts > 1 ? split_launch<YT>(a, parts, s) : tile_launch<64, 64, 16, 32, 4, EXACT, YT, false>(a, s);
         }
     }
-    if constexpr (!F32) {
+    if constexpr (!EXACT) {
         if (tile == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, GROUPED>(a, s);
     }
     if constexpr (GROUPED) {
@@ -452,9 +452,9 @@ hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
         // against 42; else 171 against 165 for 64 experts of 2048 x 4096, 96 rows each).
         const int64_t rows = a.M / 128 + std::min(a.E, a.M) / 2;
         const int64_t small = rows * ((a.out + 127) / 128), large = rows * ((a.out + 255) / 256);
-        if (small <= 256 || (large > 256 && small <= 512)) return tile_launch<128, 128, 64, 64, 2, F32, YT, true>(a, s);
-        return tile_launch<128, 256, 64, 64, 3, F32, YT, true>(a, s);
-    } else return tile_launch<128, 128, 64, 64, 2, F32, YT, false>(a, s);
+        if (small <= 256 || (large > 256 && small <= 512)) return tile_launch<128, 128, 64, 64, 2, EXACT, YT, true>(a, s);
+        return tile_launch<128, 256, 64, 64, 3, EXACT, YT, true>(a, s);
+    } else return tile_launch<128, 128, 64, 64, 2, EXACT, YT, false>(a, s);
 }
 
 }  // namespace

@@ -70,6 +70,10 @@ struct Fp8Launch {
     float* sums;  // dense, where fp8_depth_parts() > 1: fp8_sums_bytes()
 };
 
+// Whether a product's sums hold every product's bits whatever its path (see the sums' paragraph in iqk_fp8_device.h);
+// bfloat16 results of many rows are summed on the 8-bit matrix instructions instead.
+constexpr bool exact_sums(int y_dtype) { return y_dtype != IQK_BF16; }
+
 hipError_t launch_router(const RouterLaunch& a, hipStream_t s);
 hipError_t launch_router_grad(const RouterGradLaunch& a, hipStream_t s);
 hipError_t launch_fp8_quantize(const Fp8QuantLaunch& a, hipStream_t s);

@@ -208,7 +208,7 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
         if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace + sums, s)) != hipSuccess)
             return hip_fail(e, "quantize launch");
         e = M <= kRowsPass ? iqk::launch_fp8_rows(L, (int)((M + 15) / 16), s)
-                           : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows((double)M, M, w->out, false, y_dtype == IQK_F32), s);
+                           : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows((double)M, M, w->out, false, iqk::exact_sums(y_dtype)), s);
     }
     if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
     return ok();
@@ -263,7 +263,7 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
         return at;
     };
     const double per_expert = (double)P / (double)E;
-    const int tile = iqk::fp8_tile_rows(per_expert, P, w->out, true, y_dtype == IQK_F32);
+    const int tile = iqk::fp8_tile_rows(per_expert, P, w->out, true, iqk::exact_sums(y_dtype));
     iqk::Fp8GroupLaunch G{};
     G.ids = ids;
     G.P = P;

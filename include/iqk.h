@@ -419,10 +419,17 @@ int iqk_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, uint8_
  * rows) holds sums of parts of the depth, where few tiles have a long one,
  * and the quantized x, ceil-to-256(M * in) + ceil-to-256(4 * M * ceil(in /
  * 128)) bytes of it that IQK_E4M3 x does without; it may be null where 0 bytes
- * are needed.  Accuracy against the product
- * of the same codes and scales: 2e-6 in norm for a float32 y; 16-bit results
- * are off by their rounding.  A NaN or infinity in a row of x makes that row of
- * y NaN or infinite and no other.  x 16-byte aligned; M <= 2^24. */
+ * are needed.  Accuracy against the product of the same codes and scales:
+ * sums are float32 ones (2e-6 in norm) and their one rounding is y's, but for
+ * a bfloat16 y of more than 32 rows (routed: where an expert's rows go in
+ * tiles of 128 or 256).  There each product of eight consecutive values of the
+ * depth, counted from 0, is cut toward zero to a multiple of 2^-13 of the
+ * power of two in the largest of the eight (operands' exponents added): below
+ * 7 * 2^-13 = 8.6e-4 of that product, 2e-5 to 1e-4 of y's norm measured, where
+ * the rounding to bfloat16 is 1.7e-3 of it.  An element whose large terms
+ * cancel may be off by more than its rounding; a float32 or float16 y is not.
+ * A NaN or infinity in a row of x makes that row of y NaN or infinite and no
+ * other.  x 16-byte aligned; M <= 2^24. */
 int iqk_fp8_linear_workspace(const iqk_fp8_weights* w, int64_t M, size_t* bytes);
 int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const float* x_scales, int64_t M,
                    void* workspace, size_t ws_bytes, void* y, int y_dtype, void* stream);
