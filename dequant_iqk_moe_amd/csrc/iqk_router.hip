@@ -327,7 +327,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterLaunch 
 // Gradient with respect to the logits.  With g_j = scale * dL/dw_j and
 //   renorm:    ds_j = (g_j - sum_m g_m s_m / D) / D,   D = sum_m s_m
 //   otherwise: ds_j = g_j
-// sigmoid: dl = ds * s (1 - s) at the chosen experts, zero elsewhere; softmax
+// sigmoid: dl = ds * s (1 - s) at the chosen experts (with renorm as w_j (1 - s_j)
+// (g_j - sum_m g_m w_m), w_m = s_m / D), zero elsewhere; softmax
 // without renorm: dl_e = p_e (ds_e - sum_j ds_j p_j) for every expert, with
 // renorm the second term is zero and w is the softmax of the chosen logits
 // alone: dl_j = w_j (g_j - sum_m g_m w_m).  Only softmax without renorm reads
@@ -382,17 +383,19 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(RouterGr
             const float w = sum > 0.f ? e / sum : 0.f;
             d = w * (g - wave_sum(g * w));
         } else {
-            // s = 1 / (1 + exp(-l)), s (1 - s) = q / (1 + q)^2 with q = exp(-|l|)
-            const float q = expf(-fabsf(l));
-            const float slope = in ? q / ((1.f + q) * (1.f + q)) : 0.f;
-            float ds = g;
             if (p.renorm) {
+                // dl_j = w_j (1 - s_j) (g_j - sum_m g_m w_m) with w_j = s_j / D: no factor leaves float32 where D is
+                // tiny (a 1 / D by itself would); 1 - s_j = 1 / (1 + exp(l_j))
                 const float s = in ? sigmoid(l) : 0.f;
                 const float D = wave_sum(s);
-                const float dot = wave_sum(g * s);
-                ds = D > 0.f ? (g - dot / D) / D : 0.f;
+                const float w = D > 0.f ? s / D : 0.f;
+                const float dot = wave_sum(g * w);
+                d = in ? w * sigmoid(-l) * (g - dot) : 0.f;
+            } else {
+                // s = 1 / (1 + exp(-l)), s (1 - s) = q / (1 + q)^2 with q = exp(-|l|)
+                const float q = expf(-fabsf(l));
+                d = in ? g * (q / ((1.f + q) * (1.f + q))) : 0.f;
             }
-            d = ds * slope;
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = 0.f;
