@@ -172,6 +172,9 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterLaunch 
     }
     // scores of all experts, where the choice or the weights need them
     const bool two = p.n_group > 1 && p.group_top == 2;
+    // A group's worth of two: half of their sum where a bias takes part, which orders groups alike (halving is exact)
+    // and does not leave float32 with biases at its ends, so that only a group without an expert is worth -inf.
+    const float part = p.bias ? 0.5f : 1.f;
     float total = 1.f;
     if (p.bias || two || (softmax && !p.renorm)) {
         if (softmax) {
@@ -216,7 +219,8 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterLaunch 
             if (lanes > 2) merge(dpp<kXor2>(a), dpp<kXor2>(b));
             if (lanes > 4) merge(dpp<kHalfMirror>(a), dpp<kHalfMirror>(b));
             if (lanes > 8) merge(dpp<kMirror>(a), dpp<kMirror>(b));
-            float worth = two && b != neg_inf() ? a + b : a;
+            float worth = a;
+            if (two) worth = part * a + (b != neg_inf() ? part * b : 0.f);
             if (left <= 0) worth = neg_inf();
             bool stays = false;
             for (int i = 0; i < p.topk_group; ++i) {
@@ -251,7 +255,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_kernel(RouterLaunch 
                         best = lane_best<V>(a, &at);
                     }
                     const float second = row_max<64>(best);
-                    if (second != neg_inf()) w += second;
+                    w = part * w + (second != neg_inf() ? part * second : 0.f);
                 }
                 if (lane == g) worth = w;
             }

@@ -33,3 +33,22 @@ def test_gradient_of_small_scores(least, dtype):
     assert (np.abs(got - ref) <= room).all()
 
 
+@pytest.mark.parametrize("E,n_group", [(24, 4), (32, 4), (256, 8), (60, 4)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_groups_masked_by_the_lowest_finite_bias(E, n_group, scoring):
+    """A bias of float32's lowest value is no -inf: its experts stay in, last, and the sum of
+    a group's best two does not leave float32."""
+    announce(f"router lowest bias E={E} G={n_group} {scoring}")
+    per = E // n_group
+    rng = np.random.default_rng(E)
+    l = np.stack([rng.permutation(E) - E // 2 for _ in range(5)]) / 64   # scores at least 4e-6 apart (softmax), 1e-3 (sigmoid)
+    bias = np.zeros(E, np.float32)
+    bias[per:] = LOWEST                    # one group is free, the others have the lowest bias throughout
+    k = min(64, per + 3)                   # more slots than that group has experts
+    for keep in (2, n_group):
+        _check(l, "f32", k, scoring, bias=bias, n_group=n_group, topk_group=keep, group_top=2)
+    bias[:] = -LOWEST                      # and the highest
+    bias[per:] = 0
+    _check(l, "f32", k, scoring, bias=bias, n_group=n_group, topk_group=2, group_top=2)
+
+
