@@ -378,7 +378,7 @@ __global__ __launch_bounds__(64 * kRouterWaves) void router_grad_kernel(RouterGr
         const float dot = wave_sum(g * pr);
         d = pr * (g - dot);
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = x[v] == 0.f ? 0.f : -(x[v] / total) * dot;
+        for (int v = 0; v < V; ++v) o[v] = x[v] == 0.f || !__ballot(in) ? 0.f : -(x[v] / total) * dot;
     } else {
         if (p.scoring == IQK_SOFTMAX) {
             const float top = wave_max(l);

@@ -375,8 +375,10 @@ int iqk_router_topk(const void* logits, int dtype, int64_t T, int64_t E, int k, 
  * d_weights = dL/dweights (device float32 [T, k]) and the forward call's
  * ids.  renorm, scoring and scale as in the forward call; the bias and the
  * groups only make the choice and have no gradient.  A slot whose id lies
- * outside [0, E), and one that repeats slot 0, takes no part.  float32
- * arithmetic, one rounding to dtype; deterministic. */
+ * outside [0, E), and one that repeats slot 0, takes no part; a row without
+ * any other gets zeros, whatever its logits.  (The other ids of a row differ, as
+ * the forward call's do.)  float32 arithmetic, one rounding to dtype;
+ * deterministic. */
 int iqk_router_topk_grad(const void* logits, int dtype, const int32_t* ids, const float* d_weights, int64_t T,
                          int64_t E, int k, int scoring, int renorm, float scale, void* d_logits, void* stream);
 

@@ -52,3 +52,20 @@ def test_groups_masked_by_the_lowest_finite_bias(E, n_group, scoring):
     _check(l, "f32", k, scoring, bias=bias, n_group=n_group, topk_group=2, group_top=2)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_of_rows_without_a_choice(scoring, renorm, dtype):
+    """Rows that chose nothing (ids -1) have the gradient zero, whatever their logits."""
+    rng = np.random.default_rng(3)
+    l = np.round(rng.normal(size=(6, 70)) * 16) / 16
+    l[1, 5], l[2, 66], l[3], l[4, 9] = np.nan, INF, -INF, -INF
+    ids, _ = layer.router(l, 4, "softmax")
+    assert (ids[1:4] == -1).all()
+    dw = rng.normal(size=(6, 4)).astype(np.float32)
+    ref = layer.router_grad(l, ids, dw, scoring, renorm, 1.0)
+    got = q.router_topk_grad(_dev(l, DT[dtype]), _dev(ids), _dev(dw), scoring=scoring, renorm=renorm).double().cpu().numpy()
+    assert (got[1:4] == 0).all()
+    rows = [0, 4, 5]
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    assert (np.abs(got - ref)[rows] <= 1e-5 * np.abs(dw).max() + half * np.abs(ref[rows]) + 2.0 ** -25).all()
