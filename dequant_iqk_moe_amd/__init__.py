@@ -577,6 +577,8 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
     best two of each; renorm divides the weights by their sum."""
     lp, dt = _logits(logits)
     T, E = logits.shape
+    if not 1 <= k <= E:
+        raise IqkValueError(_E_ARG, f"k = {k} outside [1, {E}]")
     if ids is None:
         ids = _empty((T, k), torch.int32, logits.device, stream)
     if weights is None:
@@ -630,6 +632,8 @@ class Fp8Weights:
     def __post_init__(self):
         if self.codes.dim() != 3 or self.codes.dtype != torch.float8_e4m3fn:
             raise IqkValueError(_E_ARG, "codes must be float8_e4m3fn [experts, out, in]")
+        if self.codes.numel() == 0:
+            raise IqkValueError(_E_ARG, "codes hold no values")
         self.experts, self.out, self.in_features = self.codes.shape
         if self.scales.dtype != torch.float32 or tuple(self.scales.shape) != (
                 self.experts, _blocks(self.out), _blocks(self.in_features)):
