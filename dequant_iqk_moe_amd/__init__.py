@@ -574,11 +574,13 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
     weights float32 [T, k]), from router logits [T, E].  scoring: "softmax"
     or "sigmoid"; bias [E] (float32) shifts the choice only; n_group > 1 keeps
     the best topk_group groups of experts, by the best or (group_top=2) the
-    best two of each; renorm divides the weights by their sum."""
+    best two of each; renorm divides the weights by their sum.  Where logits
+    require a gradient the weights carry it (through router_topk_grad)."""
     lp, dt = _logits(logits)
     T, E = logits.shape
     if not 1 <= k <= E:
         raise IqkValueError(_E_ARG, f"k = {k} outside [1, {E}]")
+    ids_given = ids is not None
     if ids is None:
         ids = _empty((T, k), torch.int32, logits.device, stream)
     if weights is None:
@@ -587,7 +589,28 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
                                 topk_group, group_top, int(bool(renorm)), scale,
                                 _dev(ids, "ids", torch.int32, T * k), _dev(weights, "weights", torch.float32, T * k),
                                 _stream(stream)))
+    if ids_given and not ids.is_inference():
+        torch.autograd.graph.increment_version(ids)  # an earlier call's gradient that still needs this buffer can tell
+    if logits.requires_grad and torch.is_grad_enabled():
+        weights = _RouterWeights.apply(logits, ids, weights, scoring, renorm, scale)
     return ids, weights
+
+
+class _RouterWeights(torch.autograd.Function):
+    """Joins weights that router_topk has computed to the logits they came from."""
+
+    @staticmethod
+    def forward(ctx, logits, ids, weights, scoring, renorm, scale):
+        ctx.save_for_backward(logits, ids)
+        ctx.mark_dirty(weights)
+        ctx.args = scoring, renorm, scale
+        return weights
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_weights):
+        logits, ids = ctx.saved_tensors
+        return router_topk_grad(logits, ids, d_weights.contiguous(), *ctx.args), None, None, None, None, None
 
 
 def router_topk_grad(logits: torch.Tensor, ids: torch.Tensor, d_weights: torch.Tensor, scoring: str = "softmax",
