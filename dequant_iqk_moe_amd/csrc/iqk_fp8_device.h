@@ -136,21 +136,28 @@ __device__ __forceinline__ float block_amax(const float (&v)[8]) {
 // (an LDS address, the same in every lane).  Written as an instruction because the
 // compiler takes every later LDS read to depend on the builtin's copy and
 // waits for it at once; the kernel waits for its copies before the barrier
-// that publishes them.  The instruction has no register result.
+// that publishes them.  The instruction has no register result.  m0, which the
+// copies write, is a register that the compiler gives to no value but sets for
+// instructions of its own: named, it will not take an earlier setting to hold
+// (its warning is about values kept in such registers).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_copy16(const uint8_t* base, uint32_t off, uint32_t dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void lds_copy16(const uint8_t* src, uint32_t dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
 }
 
 // The same for 4 bytes per lane.
 __device__ __forceinline__ void lds_copy4(const float* src, uint32_t dst) {
     const uint32_t at = __builtin_amdgcn_readfirstlane(dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory", "m0");
 }
+
+#pragma clang diagnostic pop
 
 // Waits for this wave's LDS accesses and all but its last `LATER` memory
 // accesses, then for the other waves'.
