@@ -709,6 +709,11 @@ def _round256(nbytes: int) -> int:
     return -(-nbytes // 256) * 256
 
 
+def _quantized_bytes(rows: int, n: int) -> int:
+    """The share of a workspace that x in codes does without."""
+    return _round256(rows * n) + _round256(rows * _blocks(n) * 4)
+
+
 def _workspace(workspace: torch.Tensor | None, nbytes: int, device, stream):
     """(workspace, pointer, size): the caller's, or a new one where the call needs any."""
     if workspace is None:
@@ -733,8 +738,8 @@ def fp8_linear(w: Fp8Weights, x: torch.Tensor, x_scales: torch.Tensor | None = N
     if y.dtype not in _DT:
         raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
     need = fp8_linear_workspace_bytes(w, M)
-    if xdt == _E4M3 and need:  # (codes are there already)
-        need -= _round256(M * n) + _round256(M * (-(-n // 128)) * 4)
+    if xdt == _E4M3 and need:
+        need -= _quantized_bytes(M, n)
     ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
     cw = w._c()
     _check(_lib.iqk_fp8_linear(ctypes.byref(cw), xp, xdt, sp, M, wp, nbytes, _dev(y, "y", None, M * w.out),
@@ -766,7 +771,10 @@ def moe_fp8(w: Fp8Weights, x: torch.Tensor, ids: torch.Tensor, x_slots: int = 1,
         y = _empty((T, k, w.out), out_dtype, x.device, stream)
     if y.dtype not in _DT:
         raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
-    ws, wp, nbytes = _workspace(workspace, moe_fp8_workspace_bytes(w, T, k, x_slots), x.device, stream)
+    need = moe_fp8_workspace_bytes(w, T, k, x_slots)
+    if xdt == _E4M3 and need:
+        need -= _quantized_bytes(T * x_slots, w.in_features)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
     cw = w._c()
     _check(_lib.iqk_moe_fp8(ctypes.byref(cw), xp, xdt, sp, x_slots, ip, T, k, int(bool(sorted)), wp, nbytes,
                             _dev(y, "y", None, T * k * w.out), _DT[y.dtype], _stream(stream)))

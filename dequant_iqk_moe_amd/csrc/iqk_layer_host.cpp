@@ -244,6 +244,7 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
     rc = check_fp8_io(x, x_dtype, x_scales, y, y_dtype);
     if (rc) return rc;
     if (!ids) return fail(IQK_E_ARG, "null ids");
+    if (x_dtype == IQK_E4M3 && need) need -= quantized_bytes(T * x_slots, w->in);
     rc = check_workspace(workspace, ws_bytes, need);
     if (rc) return rc;
     const int64_t E = w->experts, P = T * k;

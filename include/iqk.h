@@ -439,7 +439,9 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
 /* The same product at routed pairs, y[t, j, :] = W_{ids[t, j]} x[t, s, :]
  * (s and x_slots as in iqk_moe_gemv): y device [T, k, out] of y_dtype.  ids,
  * sorted and the NaN rows of invalid ids as in iqk_moe_prefill; x, x_scales
- * (rows t * x_slots + s) and accuracy as in iqk_fp8_linear.  T * k <= 2^24. */
+ * (rows t * x_slots + s) and accuracy as in iqk_fp8_linear; workspace holds
+ * the grouped pairs and, last, T * x_slots rows of quantized x, which IQK_E4M3
+ * x does without as there.  T * k <= 2^24. */
 int iqk_moe_fp8_workspace(const iqk_fp8_weights* w, int64_t T, int k, int x_slots, size_t* bytes);
 int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const float* x_scales, int x_slots,
                 const int32_t* ids, int64_t T, int k, int sorted, void* workspace, size_t ws_bytes,
