@@ -29,7 +29,7 @@ __all__ = [
     "route", "grouped_gemm", "prefill_workspace_bytes", "moe_prefill", "floor_gemv",
     "floor_dequant", "stream_read", "stream_write", "library_path",
     "router_topk", "router_topk_grad", "Fp8Weights", "fp8_quantize", "fp8_linear",
-    "fp8_linear_workspace_bytes", "moe_fp8", "moe_fp8_workspace_bytes",
+    "fp8_linear_workspace_bytes", "moe_fp8", "moe_fp8_workspace_bytes", "fp8_path",
 ]
 
 IQ2_KS, IQ2_K, IQ1_S_R4 = 1, 2, 3
@@ -113,6 +113,7 @@ def _load():
         "iqk_fp8_quantize": (i32, [p, i32, i64, i64, p, p, p]),
         "iqk_fp8_linear_workspace": (i32, [F, i64, p]),
         "iqk_fp8_linear": (i32, [F, p, i32, p, i64, p, sz, p, i32, p]),
+        "iqk_fp8_path": (i32, [F, i64, i32, i32, p]),
         "iqk_moe_fp8_workspace": (i32, [F, i64, i32, i32, p]),
         "iqk_moe_fp8": (i32, [F, p, i32, p, i32, p, i64, i32, i32, p, sz, p, i32, p]),
         "iqk_last_error": (ctypes.c_char_p, []),
@@ -703,6 +704,15 @@ def _fp8_linear_bytes(experts: int, out: int, n: int, M: int) -> int:
 def fp8_linear_workspace_bytes(w: Fp8Weights, M: int) -> int:
     """Workspace fp8_linear needs for M rows (0: none, a few rows are quantized where they are used)."""
     return _fp8_linear_bytes(w.experts, w.out, w.in_features, M)
+
+
+def fp8_path(experts: int, out: int, n: int, T: int, k: int = 0, out_dtype=torch.float32):
+    """Which kernels fp8_linear (k 0, T rows) or moe_fp8 (T tokens of k pairs)
+    run on for weights [experts, out, n], for tests and profiles: ("few",),
+    ("rows",) or ("tiles", rows of x, weight rows, parts of the depth)."""
+    path = (ctypes.c_int32 * 4)()
+    _check(_lib.iqk_fp8_path(ctypes.byref(_Fp8Weights(experts, out, n)), T, k, _DT[out_dtype], path))
+    return ("few", "rows", "tiles")[path[0]], *(path[1:] if path[0] == 2 else ())
 
 
 def _round256(nbytes: int) -> int:

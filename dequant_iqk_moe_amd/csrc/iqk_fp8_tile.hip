@@ -428,84 +428,103 @@ hipError_t tile_launch(const Fp8Launch& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int YT, bool GROUPED>
-hipError_t tile_choose(const Fp8Launch& a, int tile, hipStream_t s) {
+template <int YT>
+hipError_t grouped_launch(const Fp8Launch& a, const Fp8Tile& t, hipStream_t s) {
     constexpr bool EXACT = exact_sums(YT);
-    if constexpr (GROUPED) {
-        // few rows per expert: the weights stream through, exact sums cost nothing there
-        if (tile == 16) return tile_launch<16, 128, 16, 32, 4, true, YT, true>(a, s);
-        if (tile == 32) return tile_launch<32, 128, 32, 32, 3, true, YT, true>(a, s);
-        if (tile == 64) return tile_launch<64, 128, 32, 64, 2, true, YT, true>(a, s);
-    } else {
-        if (tile == 64) {
-            const int parts = fp8_depth_parts(a.M, a.out, a.n);
-            return parts > 1 ? split_launch<YT>(a, parts, s) : tile_launch<64, 64, 16, 32, 4, EXACT, YT, false>(a, s);
-        }
-    }
+    // few rows per expert: the weights stream through, exact sums cost nothing there
+    if (t.rows == 16) return tile_launch<16, 128, 16, 32, 4, true, YT, true>(a, s);
+    if (t.rows == 32) return tile_launch<32, 128, 32, 32, 3, true, YT, true>(a, s);
+    if (t.rows == 64) return tile_launch<64, 128, 32, 64, 2, true, YT, true>(a, s);
     if constexpr (!EXACT) {
-        if (tile == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, GROUPED>(a, s);
+        if (t.rows == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, true>(a, s);
     }
-    if constexpr (GROUPED) {
-        // A CU holds one workgroup of 128 x 256 tiles or two of 128 x 128 ones, which take as long together.  The
-        // small ones are taken where each has a CU to itself, or where they fit at once and the others do not (16
-        // experts of 310 x 2960, 1000 rows each: 62 us against 81; float32 results of 312 x 1456, 433 rows: 34
-        // against 42; else 171 against 165 for 64 experts of 2048 x 4096, 96 rows each).
-        const int64_t rows = a.M / 128 + std::min(a.E, a.M) / 2;
-        const int64_t small = rows * ((a.out + 127) / 128), large = rows * ((a.out + 255) / 256);
-        if (small <= 256 || (large > 256 && small <= 512)) return tile_launch<128, 128, 64, 64, 2, EXACT, YT, true>(a, s);
-        return tile_launch<128, 256, 64, 64, 3, EXACT, YT, true>(a, s);
-    } else return tile_launch<128, 128, 64, 64, 2, EXACT, YT, false>(a, s);
+    if (t.cols == 128) return tile_launch<128, 128, 64, 64, 2, EXACT, YT, true>(a, s);
+    return tile_launch<128, 256, 64, 64, 3, EXACT, YT, true>(a, s);
 }
 
-}  // namespace
-
-int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact) {
-    auto count = [&](int64_t t) { return (M + t - 1) / t * ((out + t - 1) / t); };
-    if (grouped) {
-        // A block of a small tile takes its time however few there are, less the smaller it is: where workgroups of 16
-        // or of 32 rows about have a CU each, they are taken (8 experts of 1024 x 4096, 37 rows each: tiles of 16, 32
-        // and 64 rows 24, 28 and 37 us; 16 of 1024 x 2048, 50 rows each: 32 rows 23, 64 rows 27, 128 rows 32).
-        const double experts = std::min((double)M, (double)M / rows_per_expert);
-        auto groups = [&](int64_t t) { return ((double)(M / t) + experts / 2) * (double)((out + 127) / 128); };
-        if (groups(16) <= 192) return 16;
-        if (groups(32) <= 288) return 32;
-        // Else the rows a tile holds are what most experts have (their counts spread like a square root; 64 experts of
-        // 4096 x 2048, 24 rows each: tiles of 32 rows 127 us, of 64 rows 145; 128 of 2048 x 2048, 26 rows: the same).
-        const double spread = std::sqrt(rows_per_expert);
-        if (rows_per_expert + 2 * spread <= 16) return 16;
-        if (rows_per_expert + spread <= 32) return 32;
-        if (rows_per_expert + 2 * spread <= 64) return 64;
-        // 64 experts of 2048 x 4096, 384 rows each: 256-row tiles 333 us, 128-row ones 380; 96 rows each: 294 and 271
-        return !exact && rows_per_expert >= 192 && count(256) >= 160 ? 256 : 128;
+template <int YT>
+hipError_t dense_launch(const Fp8Launch& a, const Fp8Tile& t, hipStream_t s) {
+    constexpr bool EXACT = exact_sums(YT);
+    if (t.parts > 1) return split_launch<YT>(a, t.parts, s);
+    if (t.rows == 64) return tile_launch<64, 64, 16, 32, 4, EXACT, YT, false>(a, s);
+    if constexpr (!EXACT) {
+        if (t.rows == 256) return tile_launch<256, 256, 64, 128, 2, false, YT, false>(a, s);
     }
-    // 256 x 256 tiles move half the bytes per product that 128 x 128 ones do, and those half of what 64 x 64 do;
-    // the largest is taken that gives most of the 256 CUs a tile
+    return tile_launch<128, 128, 64, 64, 2, EXACT, YT, false>(a, s);
+}
+
+// Rows of x in a tile of the grouped product.
+int grouped_rows(int64_t M, int64_t E, int64_t out, bool exact) {
+    auto count = [&](int64_t t) { return (M + t - 1) / t * ((out + t - 1) / t); };
+    const double rows_per_expert = (double)M / (double)E;
+    // A block of a small tile takes its time however few there are, less the smaller it is: where workgroups of 16
+    // or of 32 rows about have a CU each, they are taken (8 experts of 1024 x 4096, 37 rows each: tiles of 16, 32
+    // and 64 rows 24, 28 and 37 us; 16 of 1024 x 2048, 50 rows each: 32 rows 23, 64 rows 27, 128 rows 32).
+    const double experts = std::min((double)M, (double)M / rows_per_expert);
+    auto groups = [&](int64_t t) { return ((double)(M / t) + experts / 2) * (double)((out + 127) / 128); };
+    if (groups(16) <= 192) return 16;
+    if (groups(32) <= 288) return 32;
+    // Else the rows a tile holds are what most experts have (their counts spread like a square root; 64 experts of
+    // 4096 x 2048, 24 rows each: tiles of 32 rows 127 us, of 64 rows 145; 128 of 2048 x 2048, 26 rows: the same).
+    const double spread = std::sqrt(rows_per_expert);
+    if (rows_per_expert + 2 * spread <= 16) return 16;
+    if (rows_per_expert + spread <= 32) return 32;
+    if (rows_per_expert + 2 * spread <= 64) return 64;
+    // 64 experts of 2048 x 4096, 384 rows each: 256-row tiles 333 us, 128-row ones 380; 96 rows each: 294 and 271
+    return !exact && rows_per_expert >= 192 && count(256) >= 160 ? 256 : 128;
+}
+
+// Side of a tile of the dense product.  256 x 256 tiles move half the bytes per product that 128 x 128 ones do, and
+// those half of what 64 x 64 do; the largest is taken that gives most of the 256 CUs a tile.
+int dense_side(int64_t M, int64_t out, bool exact) {
+    auto count = [&](int64_t t) { return (M + t - 1) / t * ((out + t - 1) / t); };
     if (!exact && count(256) >= 160) return 256;
     return count(128) >= 160 ? 128 : 64;
 }
 
+// Parts of the depth of the dense product that workgroups of their own take.
 // A block of 64 x 64 tiles takes about 0.4 us however few tiles there are, so a long depth is split while each part
 // of each tile has a CU to itself (with two parts per CU 2017 x 117 x 5136 takes 25 us instead of 23) and four blocks,
 // where that saves more than 10 us: the launch that joins the sums costs about 3 us of the card and as much of the
 // host.  141 x 261 x 7920, float32: 19.5 us against 43; 308 x 1099 x 6880: 25 against 32; 64 x 4096 x 4096, not split:
 // 17 against 20.
-int fp8_depth_parts(int64_t M, int64_t out, int64_t n) {
-    if (fp8_tile_rows((double)M, M, out, false, false) != 64) return 1;
+int depth_parts(int64_t M, int64_t out, int64_t n) {
+    if (dense_side(M, out, true) != 64) return 1;  // (the same whatever y's type: where it is 64, it is for all)
     const int64_t tiles = (M + 63) / 64 * ((out + 63) / 64), nb = (n + kBlock - 1) / kBlock;
     const int64_t parts = std::min<int64_t>({256 / tiles, nb / 4, 16});
     return parts > 1 && 0.4 * (double)(nb - (nb + parts - 1) / parts) > 10.0 ? (int)parts : 1;
 }
 
+}  // namespace
+
+Fp8Tile fp8_grouped_tile(int64_t M, int64_t E, int64_t out, bool exact) {
+    const int tm = grouped_rows(M, E, out, exact);
+    if (tm < 128) return Fp8Tile{tm, 128, 1};
+    if (tm == 256) return Fp8Tile{256, 256, 1};
+    // A CU holds one workgroup of 128 x 256 tiles or two of 128 x 128 ones, which take as long together.  The
+    // small ones are taken where each has a CU to itself, or where they fit at once and the others do not (16
+    // experts of 310 x 2960, 1000 rows each: 62 us against 81; float32 results of 312 x 1456, 433 rows: 34
+    // against 42; else 171 against 165 for 64 experts of 2048 x 4096, 96 rows each).
+    const int64_t rows = M / 128 + std::min(E, M) / 2;
+    const int64_t small = rows * ((out + 127) / 128), large = rows * ((out + 255) / 256);
+    return Fp8Tile{128, small <= 256 || (large > 256 && small <= 512) ? 128 : 256, 1};
+}
+
+Fp8Tile fp8_dense_tile(int64_t M, int64_t out, int64_t n, bool exact) {
+    const int side = dense_side(M, out, exact);
+    return Fp8Tile{side, side, depth_parts(M, out, n)};
+}
+
 size_t fp8_sums_bytes(int64_t M, int64_t out, int64_t n) {
-    const int parts = fp8_depth_parts(M, out, n);
+    const int parts = depth_parts(M, out, n);
     return parts > 1 ? (size_t)(parts * M * out) * 4 : 0;
 }
 
-hipError_t launch_fp8_tile(const Fp8Launch& a, int tile, hipStream_t s) {
+hipError_t launch_fp8_tile(const Fp8Launch& a, const Fp8Tile& tile, hipStream_t s) {
     hipError_t e = hipSuccess;
     by_float(a.y_dtype, [&](auto yt) {
         constexpr int YT = decltype(yt)::value;
-        e = a.offsets ? tile_choose<YT, true>(a, tile, s) : tile_choose<YT, false>(a, tile, s);
+        e = a.offsets ? grouped_launch<YT>(a, tile, s) : dense_launch<YT>(a, tile, s);
     });
     return e;
 }

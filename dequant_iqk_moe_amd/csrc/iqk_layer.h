@@ -67,7 +67,7 @@ struct Fp8Launch {
     const int32_t *ids, *offsets, *perm, *tiles;
     void* y;  // [M, out] of y_dtype
     int y_dtype;
-    float* sums;  // dense, where fp8_depth_parts() > 1: fp8_sums_bytes()
+    float* sums;  // dense, where the depth is split: fp8_sums_bytes()
 };
 
 // Whether a product's sums hold every product's bits whatever its path (see the sums' paragraph in iqk_fp8_device.h);
@@ -87,11 +87,15 @@ bool fp8_few_fits(int64_t rows, int64_t n);
 hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s);
 // e4m3 x: 16 * min(passes16, 2) rows in a pass over the weights
 hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s);
-// e4m3 x, many rows; tile = fp8_tile_rows()
-int fp8_tile_rows(double rows_per_expert, int64_t M, int64_t out, bool grouped, bool exact);
-// parts of the depth that workgroups of their own take in the dense product, and the bytes of their sums
-int fp8_depth_parts(int64_t M, int64_t out, int64_t n);
+// e4m3 x, many rows, by tiles of `rows` rows of x and `cols` weight rows, the
+// depth in `parts` (each tile by a workgroup of its own per part)
+struct Fp8Tile {
+    int rows, cols, parts;
+};
+Fp8Tile fp8_grouped_tile(int64_t M, int64_t E, int64_t out, bool exact);
+Fp8Tile fp8_dense_tile(int64_t M, int64_t out, int64_t n, bool exact);
+// bytes of the parts' sums (0: not split), the same for every type of y
 size_t fp8_sums_bytes(int64_t M, int64_t out, int64_t n);
-hipError_t launch_fp8_tile(const Fp8Launch& a, int tile, hipStream_t s);
+hipError_t launch_fp8_tile(const Fp8Launch& a, const Fp8Tile& tile, hipStream_t s);
 
 }  // namespace iqk

@@ -208,9 +208,29 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
         if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace + sums, s)) != hipSuccess)
             return hip_fail(e, "quantize launch");
         e = M <= kRowsPass ? iqk::launch_fp8_rows(L, (int)((M + 15) / 16), s)
-                           : iqk::launch_fp8_tile(L, iqk::fp8_tile_rows((double)M, M, w->out, false, iqk::exact_sums(y_dtype)), s);
+                           : iqk::launch_fp8_tile(L, iqk::fp8_dense_tile(M, w->out, w->in, iqk::exact_sums(y_dtype)), s);
     }
     if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
+    return ok();
+}
+
+int iqk_fp8_path(const iqk_fp8_weights* w, int64_t T, int k, int y_dtype, int32_t* path) {
+    if (!path) return fail(IQK_E_ARG, "null pointer");
+    int rc = check_fp8_shape(w);
+    if (rc) return rc;
+    if (k < 0 || T < 1 || T > kMaxRows / std::max(k, 1)) return fail(IQK_E_ARG, "T * max(k, 1) must lie in [1, 2^24]");
+    if (k == 0 && w->experts != 1) return fail(IQK_E_ARG, "the dense product takes one expert's weights");
+    if (!is_float(y_dtype)) return fail(IQK_E_ARG, "y must be IQK_F32, IQK_F16 or IQK_BF16");
+    const bool exact = iqk::exact_sums(y_dtype);
+    path[0] = path[1] = path[2] = path[3] = 0;
+    if (k == 0 ? iqk::fp8_few_fits(T, w->in) : pair_by_pair(T * k, w->experts, w->out, w->in)) return ok();
+    path[0] = k == 0 && T <= kRowsPass ? 1 : 2;
+    if (path[0] == 1) return ok();
+    const iqk::Fp8Tile t = k == 0 ? iqk::fp8_dense_tile(T, w->out, w->in, exact)
+                                  : iqk::fp8_grouped_tile(T * k, w->experts, w->out, exact);
+    path[1] = t.rows;
+    path[2] = t.cols;
+    path[3] = t.parts;
     return ok();
 }
 
@@ -263,13 +283,12 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
         ws += round256(bytes);
         return at;
     };
-    const double per_expert = (double)P / (double)E;
-    const int tile = iqk::fp8_tile_rows(per_expert, P, w->out, true, iqk::exact_sums(y_dtype));
+    const iqk::Fp8Tile tile = iqk::fp8_grouped_tile(P, E, w->out, iqk::exact_sums(y_dtype));
     iqk::Fp8GroupLaunch G{};
     G.ids = ids;
     G.P = P;
     G.E = (int)E;
-    G.tile = tile;
+    G.tile = tile.rows;
     G.counts = (int32_t*)take((size_t)E * 4);
     G.offsets = (int32_t*)take((size_t)(E + 1) * 4);
     G.tiles = (int32_t*)take((size_t)(E + 1) * 4);

@@ -447,6 +447,13 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
                 const int32_t* ids, int64_t T, int k, int sorted, void* workspace, size_t ws_bytes,
                 void* y, int y_dtype, void* stream);
 
+/* Which kernels a product of these sizes runs on, for tests and profiles: T
+ * rows of a dense product (k 0) or T tokens of k pairs.  path (host, 4 values):
+ * [0] 0 = few rows, x quantized by every workgroup (routed: pair by pair), 1 =
+ * up to 32 dense rows in a pass over the weights, 2 = tiles; and for 2: [1]
+ * rows of x and [2] weight rows in a tile, [3] parts of the depth; else 0. */
+int iqk_fp8_path(const iqk_fp8_weights* w, int64_t T, int k, int y_dtype, int32_t* path);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* iqk_last_error(void);
 
