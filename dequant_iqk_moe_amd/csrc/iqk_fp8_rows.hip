@@ -190,10 +190,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(RowsParams p) {
 }
 
 // ---------------------------------------------------------------------------
-// more rows of x, quantized before: 16 NT rows in a pass over the weights
+// up to 16 NT rows of x, quantized before, in one pass over the weights
 // ---------------------------------------------------------------------------
 
-// A workgroup owns 16 weight rows; it holds the sums of 16 NT rows of x and
+// A workgroup owns 16 weight rows; it holds the sums of the rows of x and
 // requests the next block's weights and x while it multiplies the last ones.
 // (One weight tile per workgroup and the depth split over its waves: the dense
 // product of few rows has no other way to occupy the card.)
@@ -206,77 +206,73 @@ __global__ __launch_bounds__(64 * kRowsWaves, 4) void fp8_rows_kernel(RowsParams
     const int li = lane & 15, g = lane >> 4;
     const int n = p.n, nb = (n + kBlock - 1) / kBlock;
     const int row0 = blockIdx.x * 16;
-    const int64_t count = p.M;
     const int left = min(16, p.out - row0);
     const Rsrc wr = make_rsrc(p.W + (int64_t)row0 * n, (uint32_t)left * (uint32_t)n);  // (rows past the last read zero)
     const uint32_t woff = (uint32_t)li * (uint32_t)n;
     const float* sw = p.sw + (int64_t)(row0 / kBlock) * nb;
-    for (int64_t m0 = 0; m0 < count; m0 += 16 * NT) {
-        const uint8_t* xr[NT];
-        const float* sx[NT];
+    const uint8_t* xr[NT];
+    const float* sx[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int64_t r = min((int64_t)16 * t + li, p.M - 1);  // rows past the last repeat it, their results are dropped
+        xr[t] = (const uint8_t*)p.x + r * n;
+        sx[t] = p.sx + r * nb;
+    }
+    f32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Stage {
+        Frag w, x[NT];
+        float f[NT];
+    } st[2];
+    // (blocks past the last, which the loop requests and multiplies like any other, have zero weights)
+    auto request = [&](int b, Stage& s) {
+        const int c0 = b * kBlock + 16 * g, c1 = c0 + 64;
+        const uint32_t o0 = c0 < n ? woff + c0 : kOob, o1 = c1 < n ? woff + c1 : kOob;
+        s.w = Frag{ld128(wr, o0), ld128(wr, o1)};
+        // a chunk of x past the depth meets zero weights; its row's first bytes are read instead of the next
+        // row's, which could be NaN
+        const int x0 = c0 < n ? c0 : 0, x1 = c1 < n ? c1 : 0, sb = min(b, nb - 1);
+        const float fw = sw[sb];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int64_t r = min(m0 + 16 * t + li, count - 1);  // rows past the last repeat it, their results are dropped
-            xr[t] = (const uint8_t*)p.x + r * n;
-            sx[t] = p.sx + r * nb;
+            s.x[t].lo = *(const uint4*)(xr[t] + x0);
+            s.x[t].hi = *(const uint4*)(xr[t] + x1);
+            s.f[t] = sx[t][sb] * fw;
         }
-        f32x4 acc[NT];
+    };
+    auto multiply = [&](const Stage& s) {
+        const Wide w = widen_frag(s.w);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        struct Stage {
-            Frag w, x[NT];
-            float f[NT];
-        } st[2];
-        // (blocks past the last, which the loop requests and multiplies like any other, have zero weights)
-        auto request = [&](int b, Stage& s) {
-            const int c0 = b * kBlock + 16 * g, c1 = c0 + 64;
-            const uint32_t o0 = c0 < n ? woff + c0 : kOob, o1 = c1 < n ? woff + c1 : kOob;
-            s.w = Frag{ld128(wr, o0), ld128(wr, o1)};
-            // a chunk of x past the depth meets zero weights; its row's first bytes are read instead of the next
-            // row's, which could be NaN
-            const int x0 = c0 < n ? c0 : 0, x1 = c1 < n ? c1 : 0, sb = min(b, nb - 1);
-            const float fw = sw[sb];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                s.x[t].lo = *(const uint4*)(xr[t] + x0);
-                s.x[t].hi = *(const uint4*)(xr[t] + x1);
-                s.f[t] = sx[t][sb] * fw;
-            }
-        };
-        auto multiply = [&](const Stage& s) {
-            const Wide w = widen_frag(s.w);
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                add_scaled(acc[t], block_product(w, widen_frag(s.x[t])), s.f[t]);
-                __builtin_amdgcn_sched_barrier(0);  // (else all tiles are widened at once, and registers run out)
-            }
-        };
-        request(wave, st[0]);
-        for (int b = wave; b < nb; b += 2 * kRowsWaves) {
-            request(b + kRowsWaves, st[1]);
-            multiply(st[0]);
-            request(b + 2 * kRowsWaves, st[0]);
-            multiply(st[1]);
+        for (int t = 0; t < NT; ++t) {
+            add_scaled(acc[t], block_product(w, widen_frag(s.x[t])), s.f[t]);
+            __builtin_amdgcn_sched_barrier(0);  // (else all tiles are widened at once, and registers run out)
         }
+    };
+    request(wave, st[0]);
+    for (int b = wave; b < nb; b += 2 * kRowsWaves) {
+        request(b + kRowsWaves, st[1]);
+        multiply(st[0]);
+        request(b + 2 * kRowsWaves, st[0]);
+        multiply(st[1]);
+    }
 #pragma unroll
-        for (int t = 0; t < NT; ++t) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
-        __syncthreads();
-        // four neighbouring threads write the 16 results of one row of x
-        for (int u = threadIdx.x; u < 16 * NT * 4; u += 64 * kRowsWaves) {
-            const int q = u & 3, r = u >> 2, o = 4 * q;
-            if (m0 + r >= count || o >= left) continue;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < NT; ++t) red[wave][t][lane] = make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    __syncthreads();
+    // four neighbouring threads write the 16 results of one row of x
+    for (int u = threadIdx.x; u < 16 * NT * 4; u += 64 * kRowsWaves) {
+        const int q = u & 3, r = u >> 2, o = 4 * q;
+        if (r >= p.M || o >= left) continue;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kRowsWaves; ++w) {
-                const float4 a = red[w][r >> 4][16 * q + (r & 15)];
-                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-            }
-            const int64_t at = (m0 + r) * p.out + row0 + o;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (o + j < left) store_y<YT>(p.y, at + j, v[j]);
+        for (int w = 0; w < kRowsWaves; ++w) {
+            const float4 a = red[w][r >> 4][16 * q + (r & 15)];
+            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         }
-        __syncthreads();
+        const int64_t at = (int64_t)r * p.out + row0 + o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (o + j < left) store_y<YT>(p.y, at + j, v[j]);
     }
 }
 
@@ -312,11 +308,12 @@ hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s) {
+hipError_t launch_fp8_rows(const Fp8Launch& a, hipStream_t s) {
+    if (a.M > 32) return hipErrorInvalidValue;
     const RowsParams p = rows_params(a);
     by_float(a.y_dtype, [&](auto yt) {
         constexpr int YT = decltype(yt)::value;
-        if (passes16 <= 1) rows_launch<1, YT>(p, s);
+        if (a.M <= 16) rows_launch<1, YT>(p, s);
         else rows_launch<2, YT>(p, s);
     });
     return hipGetLastError();

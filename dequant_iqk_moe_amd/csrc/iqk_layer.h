@@ -85,8 +85,8 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
 bool fp8_few_fits(int64_t rows, int64_t n);
 // few rows (or one pair per workgroup row), x of any type
 hipError_t launch_fp8_few(const Fp8Launch& a, hipStream_t s);
-// e4m3 x: 16 * min(passes16, 2) rows in a pass over the weights
-hipError_t launch_fp8_rows(const Fp8Launch& a, int passes16, hipStream_t s);
+// e4m3 x, up to 32 rows, in a pass over the weights
+hipError_t launch_fp8_rows(const Fp8Launch& a, hipStream_t s);
 // e4m3 x, many rows, by tiles of `rows` rows of x and `cols` weight rows, the
 // depth in `parts` (each tile by a workgroup of its own per part)
 struct Fp8Tile {

@@ -207,7 +207,7 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
     } else {
         if (quantize && (e = quantize_into(&L, M, (uint8_t*)workspace + sums, s)) != hipSuccess)
             return hip_fail(e, "quantize launch");
-        e = M <= kRowsPass ? iqk::launch_fp8_rows(L, (int)((M + 15) / 16), s)
+        e = M <= kRowsPass ? iqk::launch_fp8_rows(L, s)
                            : iqk::launch_fp8_tile(L, iqk::fp8_dense_tile(M, w->out, w->in, iqk::exact_sums(y_dtype)), s);
     }
     if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
