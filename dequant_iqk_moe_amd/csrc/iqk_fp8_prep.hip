@@ -4,8 +4,8 @@
 // The grouping here is not iqk_route's: the product of a pair does not depend
 // on its place in its expert's group, so pairs take places as they come (LDS
 // atomics) instead of in order, and the ranking that a stable order costs
-// goes.  One launch quantizes and groups: the first workgroups group, the
-// others quantize (3072 pairs of 256 experts and 3072 x 2048 values: 8 us;
+// goes.  One launch quantizes, groups and writes the NaN rows of pairs that no
+// expert here takes, each by workgroups of its own (3072 pairs of 256 experts and 3072 x 2048 values: 8 us;
 // iqk_route alone takes 9.5 in the kernel trace).  Above 8192 pairs several
 // workgroups count and a second launch places (24576 pairs: 10 + 7.6 us).
 #include <algorithm>
@@ -71,34 +71,36 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* part) {
     return v + before;
 }
 
-// Rows of y for the pairs of this wave's 64 ids (from pair q0) that lie outside
-// [0, E) become NaN.
-__device__ __forceinline__ void nan_rows(const Fp8GroupLaunch& p, int64_t q0, bool in) {
+// Rows of y for pairs whose id lies outside [0, E) become NaN: a wave looks at
+// kNanPairs of them.  (By workgroups of their own: written by those that group,
+// the rows of 24576 pairs of 2048 bfloat16 values, 7 of 8 outside as on a device
+// that holds an eighth of the experts, made the product 820 us long; it takes 195
+// so, and 310 with every id inside.)
+constexpr int kNanPairs = 8;
+__device__ __forceinline__ void nan_rows(const Fp8GroupLaunch& p, int64_t first) {
     const int lane = threadIdx.x & 63;
-    uint64_t bad = __ballot(!in);
+    const int64_t q = first + lane;
+    const int e = lane < kNanPairs && q < p.P ? p.ids[q] : 0;
+    uint64_t bad = __ballot(e < 0 || e >= p.E);
+    const int size = p.y_half ? 2 : 4, bytes = p.out * size;
+    const uint32_t nan = p.y_half ? 0x7FFF7FFFu : 0x7FC00000u;  // (0x7FFF: in float16 and in bfloat16)
+    const uint4 four = {nan, nan, nan, nan};
     while (bad) {
-        const int64_t row = (q0 + __builtin_ctzll(bad)) * p.out;
+        char* row = (char*)p.y + (first + __builtin_ctzll(bad)) * (int64_t)bytes;
         bad &= bad - 1;
-        if (p.y_half) {  // 0x7FFF is a quiet NaN in float16 and in bfloat16
-            for (int o = lane; o < p.out; o += 64) ((uint16_t*)p.y)[row + o] = 0x7FFFu;
-        } else {
-            for (int o = lane; o < p.out; o += 64) ((float*)p.y)[row + o] = __builtin_nanf("");
-        }
+        for (int i = 16 * lane; i + 16 <= bytes; i += 16 * 64) __builtin_memcpy(row + i, &four, 16);  // (any address)
+        const int i = (bytes & ~15) + size * lane;
+        if (i < bytes) __builtin_memcpy(row + i, &nan, size == 2 ? 2 : 4);
     }
 }
 
-// Counts of a slice's pairs per expert, and the NaN rows of its other pairs.
+// Counts of a slice's pairs per expert.
 __device__ __forceinline__ void count_slice(const Fp8GroupLaunch& p, int64_t p0, int64_t p1, int32_t* cnt) {
-    const int E = p.E;
-    for (int e = threadIdx.x; e < E; e += kPrepThreads) cnt[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += kPrepThreads) cnt[e] = 0;
     __syncthreads();
-    const int lane = threadIdx.x & 63;
-    for (int64_t q0 = p0 + (threadIdx.x & ~63); q0 < p1; q0 += kPrepThreads) {
-        const int64_t q = q0 + lane;
-        const int e = q < p1 ? p.ids[q] : 0;
-        const bool in = e >= 0 && e < E;
-        if (q < p1 && in) atomicAdd(&cnt[e], 1);
-        nan_rows(p, q0, in);
+    for (int64_t q = p0 + threadIdx.x; q < p1; q += kPrepThreads) {
+        const int e = p.ids[q];
+        if (e >= 0 && e < p.E) atomicAdd(&cnt[e], 1);
     }
     __syncthreads();
 }
@@ -127,13 +129,14 @@ __device__ __forceinline__ void place_slice(const Fp8GroupLaunch& p, int h, int6
     }
 }
 
-// Workgroups below p.slices group (one slice: count and place; more: count,
-// the next kernel places), the others quantize.
+// Workgroups below p.slices group (one slice: count and place; more: count, the
+// next kernel places), then as many as `quantizing` quantize, the others write
+// NaN rows.
 template <int DT>
-__global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p, Fp8QuantLaunch q) {
+__global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p, Fp8QuantLaunch q, int64_t quantizing) {
     __shared__ int32_t cnt[kGroupE];
     __shared__ uint64_t part[kPrepWaves];
-    const int64_t group = plane_index();
+    int64_t group = plane_index();
     if (group < p.slices) {
         const int h = (int)group;
         const int64_t p0 = h * p.slice, p1 = min(p0 + p.slice, p.P);
@@ -146,7 +149,11 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p
         }
         return;
     }
-    if constexpr (DT != IQK_E4M3) quantize_blocks<DT>(q, group - p.slices, kPrepThreads);
+    group -= p.slices;
+    if constexpr (DT != IQK_E4M3) {
+        if (group < quantizing) return quantize_blocks<DT>(q, group, kPrepThreads);
+    }
+    nan_rows(p, ((group - quantizing) * kPrepWaves + (threadIdx.x >> 6)) * kNanPairs);
 }
 
 __global__ __launch_bounds__(kPrepThreads) void fp8_place_kernel(Fp8GroupLaunch p) {
@@ -168,9 +175,7 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_place_kernel(Fp8GroupLaunch 
 // For more experts than one workgroup counts: the NaN rows that iqk_route's
 // grouping leaves out, and tile counts from its offsets.
 __global__ __launch_bounds__(kPrepThreads) void fp8_nan_kernel(Fp8GroupLaunch p) {
-    const int64_t q = (int64_t)blockIdx.x * kPrepThreads + threadIdx.x;
-    const int e = q < p.P ? p.ids[q] : 0;
-    nan_rows(p, q - (threadIdx.x & 63), e >= 0 && e < p.E);
+    nan_rows(p, ((int64_t)blockIdx.x * kPrepWaves + (threadIdx.x >> 6)) * kNanPairs);
 }
 
 __global__ __launch_bounds__(kPrepThreads) void fp8_tiles_kernel(Fp8GroupLaunch p) {
@@ -209,11 +214,11 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
     const bool quantize = q.x_dtype != IQK_E4M3;
     const int64_t blocks128 = quantize ? q.rows * ((q.n + kBlock - 1) / kBlock) : 0;
     const int64_t qb = (blocks128 + kPrepBlocks - 1) / kPrepBlocks;
+    const int64_t nans = (g.P + kPrepWaves * kNanPairs - 1) / (kPrepWaves * kNanPairs);
     if (g.E > kGroupE) {
         hipError_t e = launch_route(RouteLaunch{g.ids, g.P, g.E, 0, g.counts, g.offsets, g.perm}, s);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(fp8_nan_kernel, dim3((unsigned)((g.P + kPrepThreads - 1) / kPrepThreads)), dim3(kPrepThreads), 0,
-                           s, g);
+        hipLaunchKernelGGL(fp8_nan_kernel, dim3((unsigned)nans), dim3(kPrepThreads), 0, s, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL(fp8_tiles_kernel, dim3(1), dim3(kPrepThreads), 0, s, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -221,13 +226,13 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
     }
     g.slices = fp8_group_slices(g.P);
     g.slice = (g.P + g.slices - 1) / g.slices;
-    const dim3 grid = plane(g.slices + qb);
+    const dim3 grid = plane(g.slices + qb + nans);
     if (quantize) {
         by_float(q.x_dtype, [&](auto dt) {
-            hipLaunchKernelGGL((fp8_prep_kernel<decltype(dt)::value>), grid, dim3(kPrepThreads), 0, s, g, q);
+            hipLaunchKernelGGL((fp8_prep_kernel<decltype(dt)::value>), grid, dim3(kPrepThreads), 0, s, g, q, qb);
         });
     } else {
-        hipLaunchKernelGGL((fp8_prep_kernel<IQK_E4M3>), grid, dim3(kPrepThreads), 0, s, g, q);
+        hipLaunchKernelGGL((fp8_prep_kernel<IQK_E4M3>), grid, dim3(kPrepThreads), 0, s, g, q, qb);
     }
     if (g.slices > 1) {
         hipError_t e = hipGetLastError();
