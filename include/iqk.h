@@ -430,6 +430,8 @@ int iqk_fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, uint8_
  * 7 * 2^-13 = 8.6e-4 of that product, 2e-5 to 1e-4 of y's norm measured, where
  * the rounding to bfloat16 is 1.7e-3 of it.  An element whose large terms
  * cancel may be off by more than its rounding; a float32 or float16 y is not.
+ * The two scales are multiplied first, in float32: where that product leaves
+ * its range, a block counts as infinite (NaN where its sum is zero) or zero.
  * A NaN or infinity in a row of x makes that row of y NaN or infinite and no
  * other.  x 16-byte aligned; M <= 2^24. */
 int iqk_fp8_linear_workspace(const iqk_fp8_weights* w, int64_t M, size_t* bytes);
@@ -437,8 +439,9 @@ int iqk_fp8_linear(const iqk_fp8_weights* w, const void* x, int x_dtype, const f
                    void* workspace, size_t ws_bytes, void* y, int y_dtype, void* stream);
 
 /* The same product at routed pairs, y[t, j, :] = W_{ids[t, j]} x[t, s, :]
- * (s and x_slots as in iqk_moe_gemv): y device [T, k, out] of y_dtype.  ids,
- * sorted and the NaN rows of invalid ids as in iqk_moe_prefill; x, x_scales
+ * (s and x_slots as in iqk_moe_gemv): y device [T, k, out] of y_dtype.  ids
+ * and the NaN rows of invalid ids as in iqk_moe_prefill; sorted is the caller's
+ * flag as there and makes no difference (pairs are grouped either way); x, x_scales
  * (rows t * x_slots + s) and accuracy as in iqk_fp8_linear; workspace holds
  * the grouped pairs and, last, T * x_slots rows of quantized x, which IQK_E4M3
  * x does without as there.  T * k <= 2^24. */
