@@ -72,15 +72,14 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* part) {
 }
 
 // Rows of y for pairs whose id lies outside [0, E) become NaN: a wave looks at
-// kNanPairs of them.  (By workgroups of their own: written by those that group,
+// p.nan_pairs of them.  By workgroups of their own: written by those that group,
 // the rows of 24576 pairs of 2048 bfloat16 values, 7 of 8 outside as on a device
-// that holds an eighth of the experts, made the product 820 us long; it takes 195
-// so, and 310 with every id inside.)
-constexpr int kNanPairs = 8;
+// that holds an eighth of the experts, made the product 820 us long; it takes 200
+// so, and 300 with every id inside.
 __device__ __forceinline__ void nan_rows(const Fp8GroupLaunch& p, int64_t first) {
     const int lane = threadIdx.x & 63;
     const int64_t q = first + lane;
-    const int e = lane < kNanPairs && q < p.P ? p.ids[q] : 0;
+    const int e = lane < p.nan_pairs && q < p.P ? p.ids[q] : 0;
     uint64_t bad = __ballot(e < 0 || e >= p.E);
     const int size = p.y_half ? 2 : 4, bytes = p.out * size;
     const uint32_t nan = p.y_half ? 0x7FFF7FFFu : 0x7FC00000u;  // (0x7FFF: in float16 and in bfloat16)
@@ -130,10 +129,9 @@ __device__ __forceinline__ void place_slice(const Fp8GroupLaunch& p, int h, int6
 }
 
 // Workgroups below p.slices group (one slice: count and place; more: count, the
-// next kernel places), then as many as `quantizing` quantize, the others write
-// NaN rows.
+// next kernel places), the next p.nans write NaN rows, the others quantize.
 template <int DT>
-__global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p, Fp8QuantLaunch q, int64_t quantizing) {
+__global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p, Fp8QuantLaunch q) {
     __shared__ int32_t cnt[kGroupE];
     __shared__ uint64_t part[kPrepWaves];
     int64_t group = plane_index();
@@ -150,10 +148,8 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_prep_kernel(Fp8GroupLaunch p
         return;
     }
     group -= p.slices;
-    if constexpr (DT != IQK_E4M3) {
-        if (group < quantizing) return quantize_blocks<DT>(q, group, kPrepThreads);
-    }
-    nan_rows(p, ((group - quantizing) * kPrepWaves + (threadIdx.x >> 6)) * kNanPairs);
+    if (group < p.nans) return nan_rows(p, (group * kPrepWaves + (threadIdx.x >> 6)) * p.nan_pairs);
+    if constexpr (DT != IQK_E4M3) quantize_blocks<DT>(q, group - p.nans, kPrepThreads);
 }
 
 __global__ __launch_bounds__(kPrepThreads) void fp8_place_kernel(Fp8GroupLaunch p) {
@@ -175,7 +171,7 @@ __global__ __launch_bounds__(kPrepThreads) void fp8_place_kernel(Fp8GroupLaunch 
 // For more experts than one workgroup counts: the NaN rows that iqk_route's
 // grouping leaves out, and tile counts from its offsets.
 __global__ __launch_bounds__(kPrepThreads) void fp8_nan_kernel(Fp8GroupLaunch p) {
-    nan_rows(p, ((int64_t)blockIdx.x * kPrepWaves + (threadIdx.x >> 6)) * kNanPairs);
+    nan_rows(p, ((int64_t)blockIdx.x * kPrepWaves + (threadIdx.x >> 6)) * p.nan_pairs);
 }
 
 __global__ __launch_bounds__(kPrepThreads) void fp8_tiles_kernel(Fp8GroupLaunch p) {
@@ -214,11 +210,15 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
     const bool quantize = q.x_dtype != IQK_E4M3;
     const int64_t blocks128 = quantize ? q.rows * ((q.n + kBlock - 1) / kBlock) : 0;
     const int64_t qb = (blocks128 + kPrepBlocks - 1) / kPrepBlocks;
-    const int64_t nans = (g.P + kPrepWaves * kNanPairs - 1) / (kPrepWaves * kNanPairs);
+    // Eight pairs a wave spread few pairs' rows over the card (3072 pairs of 4096 float32 values, none inside: 28 us
+    // against 67 with 32 a wave); of many pairs, that many waves hold up the quantization behind them (24576: 19 us
+    // for this launch with 8 a wave, 13 with 32, as without any).
+    g.nan_pairs = g.P <= 8192 ? 8 : 32;
+    g.nans = (g.P + kPrepWaves * g.nan_pairs - 1) / (kPrepWaves * g.nan_pairs);
     if (g.E > kGroupE) {
         hipError_t e = launch_route(RouteLaunch{g.ids, g.P, g.E, 0, g.counts, g.offsets, g.perm}, s);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(fp8_nan_kernel, dim3((unsigned)nans), dim3(kPrepThreads), 0, s, g);
+        hipLaunchKernelGGL(fp8_nan_kernel, dim3((unsigned)g.nans), dim3(kPrepThreads), 0, s, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         hipLaunchKernelGGL(fp8_tiles_kernel, dim3(1), dim3(kPrepThreads), 0, s, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -226,13 +226,13 @@ hipError_t launch_fp8_prep(Fp8GroupLaunch g, const Fp8QuantLaunch& q, hipStream_
     }
     g.slices = fp8_group_slices(g.P);
     g.slice = (g.P + g.slices - 1) / g.slices;
-    const dim3 grid = plane(g.slices + qb + nans);
+    const dim3 grid = plane(g.slices + qb + g.nans);
     if (quantize) {
         by_float(q.x_dtype, [&](auto dt) {
-            hipLaunchKernelGGL((fp8_prep_kernel<decltype(dt)::value>), grid, dim3(kPrepThreads), 0, s, g, q, qb);
+            hipLaunchKernelGGL((fp8_prep_kernel<decltype(dt)::value>), grid, dim3(kPrepThreads), 0, s, g, q);
         });
     } else {
-        hipLaunchKernelGGL((fp8_prep_kernel<IQK_E4M3>), grid, dim3(kPrepThreads), 0, s, g, q, qb);
+        hipLaunchKernelGGL((fp8_prep_kernel<IQK_E4M3>), grid, dim3(kPrepThreads), 0, s, g, q);
     }
     if (g.slices > 1) {
         hipError_t e = hipGetLastError();

@@ -49,8 +49,8 @@ struct Fp8GroupLaunch {
     int32_t *counts, *offsets, *perm, *tiles, *hist;  // [E], [E + 1], [P], [E + 1], [slices, E]
     void* y;  // rows [P, out] of the call's result: NaN for pairs with an invalid id
     int out, y_half;
-    int slices;  // set by the launch
-    int64_t slice;
+    int slices, nan_pairs;  // set by the launch
+    int64_t slice, nans;
 };
 
 // The 8-bit product, dense (ids, offsets and perm null: M rows of x) or over
