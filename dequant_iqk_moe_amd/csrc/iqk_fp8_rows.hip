@@ -12,8 +12,8 @@
 //
 // Bound: bytes of the weights, and a launch's start.  A widened weight costs
 // half a vector instruction and an eighth of a matrix instruction's lane slot,
-// well below what memory delivers.  One row of x by 4096 x 4096 weights: 6.0
-// us (2.8 TB/s of 16.8 MB); one token at six experts of that size: 22 us (4.5
+// well below what memory delivers.  One row of x by 4096 x 4096 weights: 5.6
+// us (3.0 TB/s of 16.8 MB); one token at six experts of that size: 22 us (4.5
 // TB/s; a plain read of as many bytes 17.7 us).
 #include "iqk_fp8_device.h"
 
@@ -196,7 +196,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void fp8_few_kernel(RowsParams p) {
 // A workgroup owns 16 weight rows; it holds the sums of the rows of x and
 // requests the next block's weights and x while it multiplies the last ones.
 // (One weight tile per workgroup and the depth split over its waves: the dense
-// product of few rows has no other way to occupy the card.)
+// product of few rows has no other way to occupy the card.)  Bound: bytes of
+// the weights and a launch's start, and x, which every workgroup reads again: 17
+// rows by 4096 x 4096 8.6 us, 32 rows 11.0 (1.5 TB/s of weights).
 constexpr int kRowsWaves = 4;
 
 template <int NT, int YT>

@@ -12,15 +12,17 @@
 // registers and uses v_mfma_f32_16x16x32_f16; otherwise one
 // v_mfma_scale_f32_16x16x128_f8f6f4 (both scales 2^0) takes a whole block.
 //
-// Measured, with bfloat16 results: 8192 x 4096 x 4096 in 133 us = 2.06 PFLOP/s,
-// matrix pipes 41 % busy, where the same instructions with the four
-// multiply-adds each needs, and nothing else, run at 3.1 to 3.9 PFLOP/s.  A
-// block of 256 x 256 tiles takes 3540 cycles of a CU for 2048 of its matrix
-// pipes: about 450 until a block's first fragments are there, 250 at its
-// barrier, and two waves per SIMD that share its pipe at 40 cycles per
-// instruction of 32.  More stages do not fit its LDS, and smaller tiles, which
-// would leave room for them, move more bytes per product (128 x 256 in three
-// stages 166 us).  float32 results: 290 us = 0.95 PFLOP/s; float16: 256.
+// Measured, with bfloat16 results: 8192 x 4096 x 4096 in 127 us = 2.16 PFLOP/s
+// (137 us behind the quantization of activations with loud channels), matrix
+// pipes busy 52 % of the launch's CU cycles by the counters, where the same
+// instructions with the four multiply-adds each needs, and nothing else, run at
+// 3.1 to 3.9 PFLOP/s.  A block of 256 x 256 tiles takes 3540 cycles of a CU for
+// 2048 of its matrix pipes (58 %; the rest of the launch is its start and end):
+// about 450 until a block's first fragments are there, 250 at its barrier, and
+// two waves per SIMD that share its pipe at 40 cycles per instruction of 32.
+// More stages do not fit its LDS, and smaller tiles, which would leave room for
+// them, move more bytes per product (128 x 256 in three stages 166 us).  float32
+// results: 300 us = 0.92 PFLOP/s; float16: 265.
 //
 // Few rows per expert: bytes of the weights.  The copies need no registers, so
 // as many are in flight as the LDS holds, and each is whole 128-byte lines,
