@@ -69,3 +69,14 @@ def test_gradient_of_rows_without_a_choice(scoring, renorm, dtype):
     rows = [0, 4, 5]
     half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
     assert (np.abs(got - ref)[rows] <= 1e-5 * np.abs(dw).max() + half * np.abs(ref[rows]) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_gradient_of_one_expert_by_its_own_score_is_zero(scoring, dtype):
+    """One slot divided by itself is one whatever the logits."""
+    rng = np.random.default_rng(1)
+    l = rng.normal(size=(50, 64)) * 3
+    ids, _ = q.router_topk(_dev(l, DT[dtype]), 1, scoring=scoring)
+    dw = _dev(rng.normal(size=(50, 1)).astype(np.float32) * 1000)
+    assert not q.router_topk_grad(_dev(l, DT[dtype]), ids, dw, scoring=scoring).any()
