@@ -576,12 +576,13 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
     or "sigmoid"; bias [E] (float32) shifts the choice only; n_group > 1 keeps
     the best topk_group groups of experts, by the best or (group_top=2) the
     best two of each; renorm divides the weights by their sum.  Where logits
-    require a gradient the weights carry it (through router_topk_grad)."""
+    require a gradient the weights carry it (through router_topk_grad), as a
+    new tensor over the caller's buffer if one is given."""
     lp, dt = _logits(logits)
     T, E = logits.shape
     if not 1 <= k <= E:
         raise IqkValueError(_E_ARG, f"k = {k} outside [1, {E}]")
-    ids_given = ids is not None
+    given = [t for t in (ids, weights) if t is not None]
     if ids is None:
         ids = _empty((T, k), torch.int32, logits.device, stream)
     if weights is None:
@@ -590,10 +591,11 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
                                 topk_group, group_top, int(bool(renorm)), scale,
                                 _dev(ids, "ids", torch.int32, T * k), _dev(weights, "weights", torch.float32, T * k),
                                 _stream(stream)))
-    if ids_given and not ids.is_inference():
-        torch.autograd.graph.increment_version(ids)  # an earlier call's gradient that still needs this buffer can tell
+    for t in given:  # a gradient of an earlier call that still needs a caller's buffer can tell
+        if not t.is_inference():
+            torch.autograd.graph.increment_version(t)
     if logits.requires_grad and torch.is_grad_enabled():
-        weights = _RouterWeights.apply(logits, ids, weights, scoring, renorm, scale)
+        weights = _RouterWeights.apply(logits, ids, weights.detach(), scoring, renorm, scale)
     return ids, weights
 
 

@@ -59,3 +59,24 @@ def test_inference_mode_with_caller_buffers():
         l = torch.randn(3, 60, device="cuda")
         ids = torch.empty(3, 6, dtype=torch.int32, device="cuda")
         assert torch.equal(q.router_topk(l, 6, ids=ids)[1], q.router_topk(l, 6)[1])
+
+
+def test_the_same_buffers_in_every_step():
+    l = _logits()
+    ids = torch.empty(37, 6, dtype=torch.int32, device="cuda")
+    buf = torch.empty(37, 6, device="cuda")
+    dw = torch.randn(37, 6, device="cuda")
+    for step in range(3):
+        l.grad = None
+        _, w = q.router_topk(l, 6, ids=ids, weights=buf)
+        (w * dw).sum().backward()
+        assert torch.equal(l.grad, q.router_topk_grad(l.detach(), ids, dw))
+        with torch.no_grad():
+            l -= l.grad
+    assert not buf.requires_grad
+    # a step whose weights are needed after the next call overwrote them
+    _, w = q.router_topk(l, 6, ids=ids, weights=buf)
+    loss = (w * w).sum()
+    q.router_topk(l.detach() * -1, 6, weights=buf)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
