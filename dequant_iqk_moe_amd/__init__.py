@@ -713,7 +713,7 @@ def fp8_path(experts: int, out: int, n: int, T: int, k: int = 0, out_dtype=torch
     run on for weights [experts, out, n], for tests and profiles: ("few",),
     ("rows",) or ("tiles", rows of x, weight rows, parts of the depth)."""
     path = (ctypes.c_int32 * 4)()
-    _check(_lib.iqk_fp8_path(ctypes.byref(_Fp8Weights(experts, out, n)), T, k, _DT[out_dtype], path))
+    _check(_lib.iqk_fp8_path(ctypes.byref(_Fp8Weights(experts, out, n)), T, k, _DT.get(out_dtype, -1), path))
     return ("few", "rows", "tiles")[path[0]], *(path[1:] if path[0] == 2 else ())
 
 

@@ -49,3 +49,5 @@ def test_refusals():
     assert call(4, 2, 0) == 0
     for bad in ((0, 2, 0), (4, -1, 0), (1 << 24, 2, 0), (4, 2, 3), (4, 0, 0), (4, 2, 0, None)):
         assert call(*bad) == -1
+    with pytest.raises(q.IqkValueError):
+        q.fp8_path(2, 128, 256, 4, 2, torch.int8)
