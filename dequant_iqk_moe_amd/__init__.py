@@ -15,6 +15,7 @@ reconstruction of "Format" (``dequant``), and the switch-linear call of
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -30,11 +31,14 @@ __all__ = [
     "floor_dequant", "stream_read", "stream_write", "library_path",
     "router_topk", "router_topk_grad", "Fp8Weights", "fp8_quantize", "fp8_linear",
     "fp8_linear_workspace_bytes", "moe_fp8", "moe_fp8_workspace_bytes", "fp8_path",
+    "moe_sort", "moe_sort_workspace_bytes", "moe_unsort", "moe_unsort_grad", "Int8Weights", "int8_quantize", "int8_linear",
+    "int8_linear_workspace_bytes", "int8_grouped", "int8_grouped_workspace_bytes", "int8_path",
+    "block_norm", "block_norm_grad", "block_norm_grad_workspace_bytes",
 ]
 
 IQ2_KS, IQ2_K, IQ1_S_R4 = 1, 2, 3
 FORMAT_NAMES = {"iq2_ks": IQ2_KS, "iq2_k": IQ2_K, "iq1_s_r4": IQ1_S_R4}
-_F32, _F16, _BF16, _E4M3 = 0, 1, 2, 3
+_F32, _F16, _BF16, _E4M3, _INT8 = 0, 1, 2, 3, 4
 _DT = {torch.float32: _F32, torch.float16: _F16, torch.bfloat16: _BF16}
 
 _E_ARG, _E_FORMAT, _E_SHAPE, _E_WIDTH, _E_ROWS4, _E_SIZE, _E_TABLE, _E_HIP = -1, -2, -3, -4, -5, -6, -7, -8
@@ -71,6 +75,18 @@ class _Fp8Weights(ctypes.Structure):
                 ("scales_count", ctypes.c_size_t)]
 
 
+class _Int8Weights(ctypes.Structure):
+    _fields_ = _Fp8Weights._fields_
+
+
+class _Block(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("next_weight", ctypes.c_void_p)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -81,7 +97,7 @@ def _load():
     L = ctypes.CDLL(_LIB_PATH)
     p, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
     f32 = ctypes.c_float
-    W, F = ctypes.POINTER(_Weights), ctypes.POINTER(_Fp8Weights)
+    W, F, I, B = (ctypes.POINTER(c) for c in (_Weights, _Fp8Weights, _Int8Weights, _Block))
     sig = {
         "iqk_row_bytes": (sz, [i32, i64]),
         "iqk_plane_offsets": (i32, [i32, i64, i64, p, p]),
@@ -116,6 +132,19 @@ def _load():
         "iqk_fp8_path": (i32, [F, i64, i32, i32, p]),
         "iqk_moe_fp8_workspace": (i32, [F, i64, i32, i32, p]),
         "iqk_moe_fp8": (i32, [F, p, i32, p, i32, p, i64, i32, i32, p, sz, p, i32, p]),
+        "iqk_moe_sort_workspace": (i32, [i64, i32, i64, p]),
+        "iqk_moe_sort": (i32, [p, i32, p, i64, i32, i64, i64, p, sz, p, p, p, p]),
+        "iqk_moe_unsort": (i32, [p, i32, p, p, i64, i32, i64, p, i32, p]),
+        "iqk_moe_unsort_grad": (i32, [p, i32, p, i32, p, p, i64, i32, i64, p, p, p]),
+        "iqk_int8_quantize": (i32, [p, i32, i64, i64, p, p, p]),
+        "iqk_int8_linear_workspace": (i32, [I, i64, i32, p]),
+        "iqk_int8_linear": (i32, [I, p, i32, p, i64, p, sz, p, i32, p]),
+        "iqk_int8_grouped_workspace": (i32, [I, i64, i32, p]),
+        "iqk_int8_grouped": (i32, [I, p, i32, p, p, i64, p, sz, p, i32, p]),
+        "iqk_int8_path": (i32, [I, i64, i32, p]),
+        "iqk_block_norm": (i32, [B, p, p, p]),
+        "iqk_block_norm_grad_workspace": (i32, [B, p]),
+        "iqk_block_norm_grad": (i32, [B, p, p, p, p, p, p, p, p, sz, p]),
         "iqk_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -791,3 +820,443 @@ def moe_fp8(w: Fp8Weights, x: torch.Tensor, ids: torch.Tensor, x_slots: int = 1,
     _check(_lib.iqk_moe_fp8(ctypes.byref(cw), xp, xdt, sp, x_slots, ip, T, k, int(bool(sorted)), wp, nbytes,
                             _dev(y, "y", None, T * k * w.out), _DT[y.dtype], _stream(stream)))
     return y
+
+
+# ---------------------------------------------------------------------------
+# rows sorted by expert, and back
+# ---------------------------------------------------------------------------
+
+
+def _float_dtype(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _DT:
+        raise IqkValueError(_E_ARG, f"{what} must be float32, float16 or bfloat16")
+    return _DT[t.dtype]
+
+
+def _one_device(first: torch.Tensor, *others: torch.Tensor | None):
+    """All tensors of a call lie on the current device, whose memory its kernels reach."""
+    here = None
+    for t in (first, *others):
+        at = None if t is None else getattr(t.device, "index", None)
+        if not isinstance(at, int):  # (host tensors have none)
+            continue
+        if here is None:
+            here = torch.cuda.current_device()
+        if at != here:
+            raise IqkValueError(_E_ARG, f"a tensor on {t.device} where cuda:{here} is current")
+
+
+def _wants_grad(*tensors: torch.Tensor | None) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def _written(*given: torch.Tensor | None):
+    """Caller's buffers that a call wrote: a gradient of an earlier call that still needs one can tell."""
+    for t in given:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
+def _on(stream):
+    """The given stream as the current one (backward passes run on the stream of their forward call)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+@functools.lru_cache(maxsize=1024)
+def moe_sort_workspace_bytes(T: int, k: int, E: int) -> int:
+    """Workspace moe_sort needs for T tokens of k slots (0 up to 8192 pairs)."""
+    b = ctypes.c_size_t()
+    _check(_lib.iqk_moe_sort_workspace(T, k, E, ctypes.byref(b)))
+    return b.value
+
+
+def _sort(x, ids, E, xs, offsets, place, workspace, stream):
+    xp, dt, ip = _dev(x, "x"), _float_dtype(x, "x"), _ids(ids)
+    T, k = ids.shape
+    n = x.shape[1]
+    need = moe_sort_workspace_bytes(T, k, E)
+    if xs is None:
+        xs = _empty((T * k, n), x.dtype, x.device, stream)
+    if offsets is None:
+        offsets = _empty((E + 1,), torch.int32, x.device, stream)
+    if place is None:
+        place = _empty((T, k), torch.int32, x.device, stream)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
+    _check(_lib.iqk_moe_sort(xp, dt, ip, T, k, E, n, wp, nbytes, _dev(xs, "xs", x.dtype, T * k * n), _dev(offsets, "offsets", torch.int32, E + 1),
+                             _dev(place, "place", torch.int32, T * k), _stream(stream)))
+    return xs, offsets, place
+
+
+def moe_sort(x: torch.Tensor, ids: torch.Tensor, E: int, xs: torch.Tensor | None = None,
+             offsets: torch.Tensor | None = None, place: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None):
+    """Token rows x [T, n] in the order of their experts ids [T, k]: (xs
+    [T * k, n], offsets int32 [E + 1], place int32 [T, k]).  Expert e's rows are
+    offsets[e] .. offsets[e + 1] - 1 in the order of their pairs; place is each
+    pair's row, or -1 - row (a row of zeros behind the experts') where its id is
+    outside [0, E).  Where x requires a gradient xs carries it (through
+    moe_unsort without weights)."""
+    if x.dim() != 2 or ids.dim() != 2 or ids.shape[0] != x.shape[0]:
+        raise IqkValueError(_E_ARG, "x must be [T, n] and ids [T, k]")
+    _one_device(x, ids, xs, offsets, place, workspace)
+    if not _wants_grad(x):
+        out = _sort(x, ids, E, xs, offsets, place, workspace, stream)
+        _written(xs, offsets, place)
+        return out
+    if xs is not None:
+        raise IqkValueError(_E_ARG, "xs given where x requires a gradient")
+    with _on(stream):
+        return _Sort.apply(x, ids, E, offsets, place, workspace)
+
+
+class _Sort(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, ids, E, offsets, place, workspace):
+        given = [t for t in (offsets, place) if t is not None]
+        xs, offsets, place = _sort(x.detach(), ids, E, None, offsets, place, workspace, None)
+        ctx.mark_dirty(*given)
+        ctx.mark_non_differentiable(offsets, place)
+        ctx.save_for_backward(place)
+        return xs, offsets, place
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, d_xs, *_):
+        (place,) = ctx.saved_tensors
+        return moe_unsort(d_xs.contiguous(), place, out_dtype=d_xs.dtype), None, None, None, None, None
+
+
+def _check_unsort(ys, place, weights):
+    if ys.dim() != 2 or place.dim() != 2 or ys.shape[0] != place.numel():
+        raise IqkValueError(_E_ARG, "ys must be [T * k, n] and place [T, k]")
+    T, k = place.shape
+    return (_dev(ys, "ys"), _float_dtype(ys, "ys"), _dev(place, "place", torch.int32),
+            _dev(weights, "weights", torch.float32, T * k), T, k, ys.shape[1])
+
+
+def _unsort(ys, place, weights, out_dtype, y, stream):
+    yp, dt, pp, wp, T, k, n = _check_unsort(ys, place, weights)
+    if y is None:
+        y = _empty((T, n), out_dtype, ys.device, stream)
+    _check(_lib.iqk_moe_unsort(yp, dt, pp, wp, T, k, n, _dev(y, "y", None, T * n), _float_dtype(y, "y"), _stream(stream)))
+    return y
+
+
+def moe_unsort(ys: torch.Tensor, place: torch.Tensor, weights: torch.Tensor | None = None, out_dtype=torch.float32,
+               y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Expert rows ys [T * k, n] back to their tokens: y[t] = sum_j weights[t, j] *
+    ys[place[t, j]] (float32 sums in slot order; weights None: ones), with place
+    from moe_sort.  Pairs of no expert count as rows of zeros.  Where ys or weights
+    require a gradient y carries it (through moe_unsort_grad)."""
+    _one_device(ys, place, weights, y)
+    if not _wants_grad(ys, weights):
+        out = _unsort(ys, place, weights, out_dtype, y, stream)
+        _written(y)
+        return out
+    if y is not None:
+        raise IqkValueError(_E_ARG, "y given where ys or weights require a gradient")
+    if out_dtype not in _DT:
+        raise IqkValueError(_E_ARG, "y must be float32, float16 or bfloat16")
+    with _on(stream):
+        return _Unsort.apply(ys, place, weights, out_dtype)
+
+
+class _Unsort(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ys, place, weights, out_dtype):
+        ctx.save_for_backward(ys, place, weights)
+        return _unsort(ys.detach(), place, None if weights is None else weights.detach(), out_dtype, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        ys, place, weights = ctx.saved_tensors
+        want_ys, _, want_w = ctx.needs_input_grad[:3]
+        d_ys, d_w = moe_unsort_grad(dy.contiguous(), ys, place, weights, want_ys=want_ys, want_weights=want_w)
+        return d_ys, None, d_w, None
+
+
+def moe_unsort_grad(dy: torch.Tensor, ys: torch.Tensor, place: torch.Tensor, weights: torch.Tensor | None = None,
+                    d_ys: torch.Tensor | None = None, d_weights: torch.Tensor | None = None, want_ys: bool = True,
+                    want_weights: bool = True, stream=None):
+    """Gradient of moe_unsort from dy [T, n]: (d_ys [T * k, n] of ys' type,
+    d_weights float32 [T, k]); None for one that is not wanted, and for d_weights
+    where weights is None."""
+    _one_device(dy, ys, place, weights, d_ys, d_weights)
+    yp, dt, pp, wp, T, k, n = _check_unsort(ys, place, weights)
+    dp, ddt = _dev(dy, "dy", None, T * n), _float_dtype(dy, "dy")
+    want_weights = want_weights and weights is not None
+    if not want_ys and not want_weights:
+        raise IqkValueError(_E_ARG, "neither gradient is wanted")
+    d_ys, d_weights = given = d_ys if want_ys else None, d_weights if want_weights else None
+    if want_ys and d_ys is None:
+        d_ys = _empty(ys.shape, ys.dtype, ys.device, stream)
+    if want_weights and d_weights is None:
+        d_weights = _empty((T, k), torch.float32, ys.device, stream)
+    _check(_lib.iqk_moe_unsort_grad(dp, ddt, yp, dt, pp, wp, T, k, n, _dev(d_ys, "d_ys", ys.dtype, T * k * n),
+                                    _dev(d_weights, "d_weights", torch.float32, T * k), _stream(stream)))
+    _written(*given)
+    return d_ys, d_weights
+
+
+# ---------------------------------------------------------------------------
+# products in 8-bit integers, a scale for each token and output channel
+# ---------------------------------------------------------------------------
+
+_IDT = {**_DT, torch.int8: _INT8}
+
+
+@dataclass
+class Int8Weights:
+    """8-bit integer weights: codes int8 [experts, out, in] with scales float32
+    [experts, out], one per output channel."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def __post_init__(self):
+        if self.codes.dim() != 3 or self.codes.dtype != torch.int8:
+            raise IqkValueError(_E_ARG, "codes must be int8 [experts, out, in]")
+        if self.codes.numel() == 0:
+            raise IqkValueError(_E_ARG, "codes hold no values")
+        self.experts, self.out, self.in_features = self.codes.shape
+        if self.scales.dtype != torch.float32 or tuple(self.scales.shape) != (self.experts, self.out):
+            raise IqkValueError(_E_SIZE, "scales must be float32 [experts, out]")
+
+    def _c(self) -> _Int8Weights:
+        cp, sp = _dev(self.codes, "codes"), _dev(self.scales, "scales")
+        return _Int8Weights(self.experts, self.out, self.in_features, cp, self.codes.numel(), sp, self.scales.numel())
+
+
+def int8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
+    """x [..., n] -> (codes int8 [..., n], scales float32 [...]), one scale per row."""
+    dt = _float_dtype(x, "x")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise IqkValueError(_E_ARG, "x must be [..., n] with n > 0")
+    _one_device(x, codes, scales)
+    n = x.shape[-1]
+    rows = x.numel() // n
+    xp = _dev(x, "x")
+    given = codes, scales
+    if codes is None:
+        codes = _empty(x.shape, torch.int8, x.device, stream)
+    if scales is None:
+        scales = _empty(x.shape[:-1], torch.float32, x.device, stream)
+    _check(_lib.iqk_int8_quantize(xp, dt, rows, n, _dev(codes, "codes", torch.int8, rows * n),
+                                  _dev(scales, "scales", torch.float32, rows), _stream(stream)))
+    _written(*given)
+    return codes, scales
+
+
+def _int8_x(x: torch.Tensor, x_scales: torch.Tensor | None, rows: int, n: int):
+    if x.dtype not in _IDT:
+        raise IqkValueError(_E_ARG, "x must be float32, float16, bfloat16 or int8")
+    return _dev(x, "x", None, rows * n), _IDT[x.dtype], _dev(x_scales, "x_scales", torch.float32, rows)
+
+
+@functools.lru_cache(maxsize=1024)
+def _int8_bytes(call: str, experts: int, out: int, n: int, rows: int, xdt: int) -> int:
+    b = ctypes.c_size_t()
+    _check(getattr(_lib, call)(ctypes.byref(_Int8Weights(experts, out, n)), rows, xdt, ctypes.byref(b)))
+    return b.value
+
+
+def int8_linear_workspace_bytes(w: Int8Weights, M: int, x_dtype=torch.bfloat16) -> int:
+    """Workspace int8_linear needs for M rows (0: none, a few rows are quantized where they are used)."""
+    return _int8_bytes("iqk_int8_linear_workspace", w.experts, w.out, w.in_features, M, _IDT.get(x_dtype, -1))
+
+
+def int8_grouped_workspace_bytes(w: Int8Weights, rows: int, x_dtype=torch.bfloat16) -> int:
+    """Workspace int8_grouped needs for so many rows (0: none)."""
+    return _int8_bytes("iqk_int8_grouped_workspace", w.experts, w.out, w.in_features, rows, _IDT.get(x_dtype, -1))
+
+
+def int8_path(experts: int, out: int, n: int, rows: int, grouped: bool = False):
+    """Which kernel int8_linear or int8_grouped runs on for weights [experts, out,
+    n], for tests and profiles: ("few",) or ("tiles", rows of x, weight rows)."""
+    path = (ctypes.c_int32 * 3)()
+    _check(_lib.iqk_int8_path(ctypes.byref(_Int8Weights(experts, out, n)), rows, int(bool(grouped)), path))
+    return ("tiles", path[1], path[2]) if path[0] else ("few",)
+
+
+def int8_linear(w: Int8Weights, x: torch.Tensor, x_scales: torch.Tensor | None = None, out_dtype=torch.float32,
+                workspace: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y [..., out] = x [..., in] times 8-bit integer weights.  x in a float type
+    is quantized on the way (as int8_quantize does); codes come with their
+    x_scales."""
+    n = w.in_features
+    if x.dim() == 0 or x.shape[-1] != n:
+        raise IqkValueError(_E_SIZE, f"x must be [..., {n}]")
+    _one_device(x, w.codes, x_scales, workspace, y)
+    M = x.numel() // n
+    xp, xdt, sp = _int8_x(x, x_scales, M, n)
+    cw = w._c()
+    given = y
+    if y is None:
+        y = _empty((*x.shape[:-1], w.out), out_dtype, x.device, stream)
+    need = _int8_bytes("iqk_int8_linear_workspace", w.experts, w.out, n, M, xdt)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
+    _check(_lib.iqk_int8_linear(ctypes.byref(cw), xp, xdt, sp, M, wp, nbytes, _dev(y, "y", None, M * w.out),
+                                _float_dtype(y, "y"), _stream(stream)))
+    _written(given)
+    return y
+
+
+def int8_grouped(w: Int8Weights, x: torch.Tensor, offsets: torch.Tensor, x_scales: torch.Tensor | None = None,
+                 out_dtype=torch.float32, workspace: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """y [rows, out]: rows offsets[e] .. offsets[e + 1] - 1 of x [rows, in] times
+    expert e's weights (x and offsets as moe_sort makes them); rows behind the last
+    expert's are zeros.  x as in int8_linear."""
+    if x.dim() != 2 or x.shape[1] != w.in_features:
+        raise IqkValueError(_E_SIZE, f"x must be [rows, {w.in_features}]")
+    _one_device(x, w.codes, offsets, x_scales, workspace, y)
+    rows, n = x.shape
+    xp, xdt, sp = _int8_x(x, x_scales, rows, n)
+    op = _dev(offsets, "offsets", torch.int32, w.experts + 1)
+    cw = w._c()
+    given = y
+    if y is None:
+        y = _empty((rows, w.out), out_dtype, x.device, stream)
+    need = _int8_bytes("iqk_int8_grouped_workspace", w.experts, w.out, n, rows, xdt)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
+    _check(_lib.iqk_int8_grouped(ctypes.byref(cw), xp, xdt, sp, op, rows, wp, nbytes,
+                                 _dev(y, "y", None, rows * w.out), _float_dtype(y, "y"), _stream(stream)))
+    _written(given)
+    return y
+
+
+# ---------------------------------------------------------------------------
+# the norms around a block
+# ---------------------------------------------------------------------------
+
+
+def _block(x, y, post_weight, gate, next_weight, alpha, beta, eps) -> _Block:
+    """The call's descriptor, after checking every tensor's type and size."""
+    dt = _float_dtype(x, "x")
+    if x.dim() == 0 or x.shape[-1] == 0:
+        raise IqkValueError(_E_ARG, "x must be [..., n] with n > 0")
+    n = x.shape[-1]
+    T = x.numel() // n
+    ydt = dt
+    if y is not None:
+        ydt = _float_dtype(y, "y")
+    weights = [t for t in (post_weight, next_weight) if t is not None]
+    if len(weights) == 2 and weights[0].dtype != weights[1].dtype:
+        raise IqkValueError(_E_ARG, "post_weight and next_weight must be of one type")
+    kind, gdt, size = 0, _F32, None
+    if gate is not None:
+        gdt = _float_dtype(gate, "gate")
+        shape = tuple(gate.shape)
+        if shape == (n,):
+            kind, size = 1, n
+        elif shape == (*x.shape[:-1], 1):
+            kind, size = 2, T
+        elif shape == tuple(x.shape):
+            kind, size = 3, T * n
+        else:
+            raise IqkValueError(_E_SIZE, f"gate must be [{n}], {[*x.shape[:-1], 1]} or {list(x.shape)}")
+    return _Block(T, n, dt, ydt, _float_dtype(weights[0], "weights") if weights else _F32, gdt, kind, alpha, beta, eps,
+                  _dev(x, "x"), _dev(y, "y", None, T * n), _dev(post_weight, "post_weight", None, n),
+                  _dev(gate, "gate", None, size), _dev(next_weight, "next_weight", None, n))
+
+
+def _block_norm(x, y, post_weight, gate, next_weight, alpha, beta, eps, r, h, stream):
+    b = _block(x, y, post_weight, gate, next_weight, alpha, beta, eps)
+    numel = b.T * b.n
+    if y is not None and r is None:
+        r = _empty(x.shape, x.dtype, x.device, stream)
+    if next_weight is not None and h is None:
+        h = _empty(x.shape, x.dtype, x.device, stream)
+    _check(_lib.iqk_block_norm(ctypes.byref(b), _dev(r, "r", x.dtype, numel), _dev(h, "h", x.dtype, numel), _stream(stream)))
+    return r, h
+
+
+def block_norm(x: torch.Tensor, y: torch.Tensor | None = None, post_weight: torch.Tensor | None = None,
+               gate: torch.Tensor | None = None, next_weight: torch.Tensor | None = None, alpha: float = 1.0,
+               beta: float = 1.0, eps: float = 1e-6, r: torch.Tensor | None = None, h: torch.Tensor | None = None,
+               stream=None):
+    """The norms around a block, its gate and the scaled residual, in one pass:
+    (r, h) with
+
+        u = y * s(y) * post_weight        (u = y without post_weight)
+        r = alpha * x + beta * gate * u
+        h = r * s(r) * next_weight        s(v) = 1 / sqrt(mean(v^2) + eps)
+
+    x [..., n] is the residual stream, y [..., n] the block's output (of x's type
+    or float32), gate [n], [..., 1] or [..., n]; r and h are of x's type, h from r
+    before its rounding.  h is None without next_weight.  Without y it is the norm
+    before the first block: (x, h).  Where an input requires a gradient the
+    results carry it (through block_norm_grad)."""
+    _one_device(x, y, post_weight, gate, next_weight, r, h)
+    if not _wants_grad(x, y, post_weight, gate, next_weight):
+        given = r, h
+        r, h = _block_norm(x, y, post_weight, gate, next_weight, alpha, beta, eps, r, h, stream)
+        _written(*given)
+        return x if y is None else r, h
+    if r is not None or h is not None:
+        raise IqkValueError(_E_ARG, "r or h given where an input requires a gradient")
+    with _on(stream):
+        out = _BlockNorm.apply(x, y, post_weight, gate, next_weight, alpha, beta, eps)
+    return (x, out[0]) if y is None else (out[0], out[1] if len(out) > 1 else None)
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, y, post_weight, gate, next_weight, alpha, beta, eps):
+        ctx.save_for_backward(x, y, post_weight, gate, next_weight)
+        ctx.args = alpha, beta, eps
+        ctx.set_materialize_grads(False)
+        plain = [None if t is None else t.detach() for t in (x, y, post_weight, gate, next_weight)]
+        return tuple(t for t in _block_norm(*plain, alpha, beta, eps, None, None, None) if t is not None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, *grads):
+        x, y, post_weight, gate, next_weight = ctx.saved_tensors
+        grads = [None if g is None else g.contiguous() for g in grads]
+        dr = grads[0] if y is not None else None
+        dh = grads[-1] if next_weight is not None else None
+        if dr is None and dh is None:
+            return (None,) * 8
+        alpha, beta, eps = ctx.args
+        got = block_norm_grad(x, y, dr, dh, post_weight=post_weight, gate=gate, next_weight=next_weight, alpha=alpha,
+                              beta=beta, eps=eps, want=ctx.needs_input_grad[:5])
+        return (*got, None, None, None)
+
+
+def block_norm_grad_workspace_bytes(T: int, n: int, post_weight: bool = True, next_weight: bool = True,
+                                    channel_gate: bool = False) -> int:
+    """Workspace block_norm_grad needs for the gradients of these parameters."""
+    return _block_grad_bytes(T, n, bool(post_weight), bool(next_weight), bool(channel_gate))
+
+
+@functools.lru_cache(maxsize=1024)
+def _block_grad_bytes(T: int, n: int, post: bool, nxt: bool, channel: bool) -> int:
+    b = ctypes.c_size_t()
+    blk = _Block(T, n, gate_kind=int(channel), post_weight=1 if post else None, next_weight=1 if nxt else None)
+    _check(_lib.iqk_block_norm_grad_workspace(ctypes.byref(blk), ctypes.byref(b)))
+    return b.value
+
+
+def block_norm_grad(x: torch.Tensor, y: torch.Tensor | None, dr: torch.Tensor | None, dh: torch.Tensor | None = None,
+                    post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                    next_weight: torch.Tensor | None = None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                    want=(True,) * 5, workspace: torch.Tensor | None = None, stream=None):
+    """Gradient of block_norm from those of r and h (None: zero): (dx, dy,
+    d_post_weight, d_gate, d_next_weight), each of its input's type and shape; None
+    for inputs that are None and where want is false."""
+    _one_device(x, y, dr, dh, post_weight, gate, next_weight, workspace)
+    b = _block(x, y, post_weight, gate, next_weight, alpha, beta, eps)
+    numel = b.T * b.n
+    drp, dhp = _dev(dr, "dr", x.dtype, numel), _dev(dh, "dh", x.dtype, numel)
+    out = [_empty(t.shape, t.dtype, t.device, stream) if t is not None and wanted else None
+           for t, wanted in zip((x, y, post_weight, gate, next_weight), want)]
+    channel = b.gate_kind == 1 and out[3] is not None
+    need = _block_grad_bytes(b.T, b.n, out[2] is not None, out[4] is not None, channel)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
+    _check(_lib.iqk_block_norm_grad(ctypes.byref(b), drp, dhp, *(None if t is None else t.data_ptr() for t in out), wp,
+                                    nbytes, _stream(stream)))
+    return tuple(out)

@@ -31,8 +31,14 @@ PER_FILE = {
     "iqk_fp8_prep.hip": [],
     "iqk_fp8_rows.hip": [],
     "iqk_fp8_tile.hip": [],
+    "iqk_sort.hip": [],
+    "iqk_norm.hip": [],
+    "iqk_int8_rows.hip": [],
+    "iqk_int8_tile.hip": [],
     "iqk_host.cpp": [],
     "iqk_layer_host.cpp": [],
+    "iqk_block_host.cpp": [],
+    "iqk_int8_host.cpp": [],
     "iqk_relayout.cpp": [],
     "iqk_status.cpp": [],
 }
@@ -65,7 +71,7 @@ def build(verbose: bool = False) -> str:
     os.makedirs(objdir, exist_ok=True)
     srcs = sorted(PER_FILE)
     objs = [os.path.join(objdir, s + ".o") for s in srcs]
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         list(ex.map(_compile, srcs, objs))
     tmp = OUT + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]

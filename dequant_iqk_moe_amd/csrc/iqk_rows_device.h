@@ -1,0 +1,96 @@
+// iqk_rows_device.h -- device helpers for kernels that pass over rows of any
+// length: eight consecutive values of a row at any alignment, sums over a wave.
+#pragma once
+
+#include "iqk_fp8_device.h"
+
+namespace iqk {
+
+// V (4 or 8) consecutive values as they lie in memory.
+template <int DT, int V = 8>
+struct Raw {
+    uint32_t w[DT == IQK_F32 ? V : V / 2];
+};
+
+// Values i .. i + V - 1 of p, of which `left` are there; the others are zero.
+// (Rows begin wherever their length puts them: loads take any address.)
+template <int DT, int V = 8>
+__device__ __forceinline__ Raw<DT, V> load_raw(const void* p, int64_t i, int left) {
+    Raw<DT, V> r;
+    constexpr int kSize = DT == IQK_F32 ? 4 : 2;
+    if (left >= V) {
+        __builtin_memcpy(r.w, (const char*)p + i * kSize, V * kSize);
+        return r;
+    }
+#pragma unroll
+    for (int j = 0; j < V * kSize / 4; ++j) r.w[j] = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (j >= left) continue;
+        if constexpr (DT == IQK_F32) r.w[j] = ((const uint32_t*)p)[i + j];
+        else r.w[j / 2] |= (uint32_t)((const uint16_t*)p)[i + j] << (j % 2 * 16);
+    }
+    return r;
+}
+
+template <int DT, int V>
+__device__ __forceinline__ void widen_raw(const Raw<DT, V>& r, float (&v)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if constexpr (DT == IQK_F32) v[j] = __uint_as_float(r.w[j]);
+        else if constexpr (DT == IQK_BF16) v[j] = __uint_as_float(j % 2 ? r.w[j / 2] & 0xFFFF0000u : r.w[j / 2] << 16);
+        else v[j] = half_to_float(j % 2 ? r.w[j / 2] >> 16 : r.w[j / 2] & 0xFFFFu);
+    }
+}
+
+// The same for a type known at run time only (the same in every lane).
+template <int V>
+__device__ __forceinline__ void load_any(const void* p, int dtype, int64_t i, int left, float (&v)[V]) {
+    if (dtype == IQK_F32) widen_raw(load_raw<IQK_F32, V>(p, i, left), v);
+    else if (dtype == IQK_BF16) widen_raw(load_raw<IQK_BF16, V>(p, i, left), v);
+    else widen_raw(load_raw<IQK_F16, V>(p, i, left), v);
+}
+
+// min(left, V) values of v to y + i
+template <int DT, int V>
+__device__ __forceinline__ void store_some(void* y, int64_t i, const float (&v)[V], int left) {
+    if (left <= 0) return;
+    if constexpr (V == 8) {
+        store8<DT>(y, i, v, left);
+    } else if (left >= V) {
+        if constexpr (DT == IQK_F32) {
+            __builtin_memcpy((float*)y + i, v, 4 * V);
+        } else {
+            uint16_t w[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) store_y<DT>(w, j, v[j]);
+            __builtin_memcpy((uint16_t*)y + i, w, 2 * V);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j < left) store_y<DT>(y, i + j, v[j]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_any(void* y, int dtype, int64_t i, const float (&v)[V], int left) {
+    if (dtype == IQK_F32) store_some<IQK_F32>(y, i, v, left);
+    else if (dtype == IQK_BF16) store_some<IQK_BF16>(y, i, v, left);
+    else store_some<IQK_F16>(y, i, v, left);
+}
+
+// x summed over the wave, in every lane: rotations within each 16 lanes, then
+// the four sums in their order (the same result every time).
+__device__ __forceinline__ float wave_sum(float x) {
+    auto ror = [](float v, auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    x += ror(x, std::integral_constant<int, 0x128>{});
+    x += ror(x, std::integral_constant<int, 0x124>{});
+    x += ror(x, std::integral_constant<int, 0x122>{});
+    x += ror(x, std::integral_constant<int, 0x121>{});
+    auto lane = [&](int l) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), l)); };
+    return ((lane(0) + lane(16)) + lane(32)) + lane(48);
+}
+
+}  // namespace iqk

@@ -1,0 +1,451 @@
+// iqk_sort.hip -- token rows in the order of their experts, back again with
+// the router's weights, and the gradient of that.
+//
+//   xs[row(t, j)] = x[t],  y[t] = sum_j w[t, j] ys[row(t, j)],
+//   d_ys[row(t, j)] = w[t, j] dy[t],  d_w[t, j] = <dy[t], ys[row(t, j)]>
+//
+// where row(t, j) is the place of pair t k + j in a stable sort by expert, the
+// pairs whose id is outside [0, E) last.  place[t, j] = row(t, j), and
+// -1 - row(t, j) for those, whose rows count as zeros.
+//
+// Bound: bytes.  All row kernels go token by token, so a token's own row is
+// read or written once for its k expert rows.
+#include <algorithm>
+
+#include "iqk_block.h"
+#include "iqk_rows_device.h"
+
+namespace iqk {
+namespace {
+
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kKeys = 8;  // keys that a pass over the ids counts at once
+
+struct SortParams {
+    const uint8_t* x;
+    const int32_t* ids;
+    int64_t T, P;
+    int k, E;
+    int64_t row;  // bytes
+    int32_t* hist;
+    int slices;
+    int64_t slice;
+    int tokens, share;  // direct: tokens and offsets of a workgroup
+    uint8_t* xs;
+    int32_t *offsets, *place;
+};
+
+// The expert of pair p, E for an id outside [0, E).
+__device__ __forceinline__ int expert_of(const SortParams& p, int64_t pair) {
+    const int e = p.ids[pair];
+    return (unsigned)e < (unsigned)p.E ? e : p.E;
+}
+
+// Copies part `part` of `parts` of token t's row to its pairs' rows (zeros where
+// they have no expert); at(j) is place[t, j].
+template <class At>
+__device__ __forceinline__ void copy_row(const SortParams& p, int64_t t, int part, int parts, At at) {
+    const int64_t chunks = p.row / 16;
+    const uint8_t* src = p.x + t * p.row;
+    for (int64_t c = (int64_t)part * kThreads + threadIdx.x; c < chunks; c += (int64_t)parts * kThreads) {
+        uint4 v;
+        __builtin_memcpy(&v, src + 16 * c, 16);
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t to = at(j);
+            const uint4 z = to < 0 ? make_uint4(0, 0, 0, 0) : v;
+            __builtin_memcpy(p.xs + (int64_t)(to < 0 ? -1 - to : to) * p.row + 16 * c, &z, 16);
+        }
+    }
+    // what no 16 bytes hold, two at a time
+    const int64_t tail = 16 * chunks + 2 * threadIdx.x;
+    if (part == parts - 1 && tail < p.row) {
+        const uint16_t v = *(const uint16_t*)(src + tail);
+        for (int j = 0; j < p.k; ++j) {
+            const int32_t to = at(j);
+            *(uint16_t*)(p.xs + (int64_t)(to < 0 ? -1 - to : to) * p.row + tail) = to < 0 ? 0 : v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// few pairs: one launch
+// ---------------------------------------------------------------------------
+
+// The place of pair p is the number of pairs q with (expert, q) below its own,
+// which every workgroup counts for its own pairs: P^2 / 64 comparisons of a
+// wave in all, on the whole card, and no pass that waits for another.  offsets[e]
+// is the count of pairs below (e, 0).
+constexpr int64_t kDirect = 8192;  // pairs up to which the ids go this way
+constexpr int kShift = 13;         // (a key holds a pair's index below 2^13 and its expert)
+constexpr int kMost = 64 + kKeys;  // places and offsets of a workgroup, whole groups of keys
+
+__global__ __launch_bounds__(kThreads) void sort_direct_kernel(SortParams p) {
+    __shared__ int32_t part[kWaves][kMost];
+    __shared__ int32_t at[kMost];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens, t1 = min(t0 + p.tokens, p.T);
+    const int pairs = t0 < t1 ? (int)(t1 - t0) * p.k : 0;
+    // offsets: the first workgroups of the launch, `share` each
+    const int wg = blockIdx.y * gridDim.x + blockIdx.x;
+    const int e0 = wg * p.share, e1 = min(e0 + p.share, p.E + 1);
+    const int count = pairs + max(e1 - e0, 0);
+    const int p0 = (int)t0 * p.k;
+    for (int i0 = 0; i0 < count; i0 += kKeys) {
+        uint32_t key[kKeys];
+        int below[kKeys];
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) {
+            const int u = i0 + i;
+            uint32_t v = 0;
+            if (u < pairs) v = (uint32_t)expert_of(p, p0 + u) << kShift | (uint32_t)(p0 + u);
+            else if (u < count) v = (uint32_t)(e0 + u - pairs) << kShift;
+            key[i] = __builtin_amdgcn_readfirstlane(v);
+            below[i] = 0;
+        }
+        for (int64_t q0 = wave * 64; q0 < p.P; q0 += kThreads) {
+            const int64_t q = q0 + lane;
+            const uint32_t v = q < p.P ? (uint32_t)expert_of(p, q) << kShift | (uint32_t)q : 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) below[i] += __builtin_popcountll(__ballot(v < key[i]));
+        }
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) part[wave][i0 + i] = below[i];
+        }
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < count) {
+        const int u = threadIdx.x;
+        int32_t v = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) v += part[w][u];
+        if (u < pairs) {
+            if (expert_of(p, p0 + u) == p.E) v = -1 - v;
+            at[u] = v;
+            if (blockIdx.y == 0) p.place[p0 + u] = v;
+        } else {
+            p.offsets[e0 + u - pairs] = v;
+        }
+    }
+    __syncthreads();
+    for (int64_t t = t0; t < t1; ++t)
+        copy_row(p, t, blockIdx.y, gridDim.y, [&](int j) { return __builtin_amdgcn_readfirstlane(at[(int)(t - t0) * p.k + j]); });
+}
+
+// ---------------------------------------------------------------------------
+// many pairs: slices are counted, then placed, then the rows are copied
+// ---------------------------------------------------------------------------
+
+constexpr int64_t kSlices = 128, kSlicePairs = 1024;
+
+__global__ __launch_bounds__(kThreads) void sort_count_kernel(SortParams p) {
+    extern __shared__ int32_t counts[];
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) counts[e] = 0;
+    __syncthreads();
+    const int64_t q1 = min(((int64_t)blockIdx.x + 1) * p.slice, p.P);
+    for (int64_t q = (int64_t)blockIdx.x * p.slice + threadIdx.x; q < q1; q += kThreads) atomicAdd(&counts[expert_of(p, q)], 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) p.hist[(int64_t)blockIdx.x * (p.E + 1) + e] = counts[e];
+}
+
+// A slice's pairs take the places behind those of lower experts and of the same
+// expert in earlier slices, in order: the slice is cut into a run for each wave,
+// whose counts are made first (of pairs, so their order does not matter), and a
+// wave ranks 64 pairs at a time by the lanes before them with the same expert.
+__global__ __launch_bounds__(kThreads) void sort_place_kernel(SortParams p) {
+    extern __shared__ int32_t next[];  // [kWaves][E + 1]
+    __shared__ int32_t sums[kWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int stride = p.E + 1;
+    for (int i = threadIdx.x; i < kWaves * stride; i += kThreads) next[i] = 0;
+    __syncthreads();
+    const int64_t q0 = (int64_t)blockIdx.x * p.slice, run = (p.slice / kWaves + 63) / 64 * 64;
+    const int64_t end = min(q0 + p.slice, p.P), r0 = min(q0 + wave * run, end), r1 = wave == kWaves - 1 ? end : min(r0 + run, end);
+    for (int64_t q = r0 + lane; q < r1; q += 64) atomicAdd(&next[wave * stride + expert_of(p, q)], 1);
+    __syncthreads();
+    int before = 0;  // pairs of the experts below those of this pass
+    for (int base = 0; base < stride; base += kThreads) {
+        const int e = base + threadIdx.x;
+        int total = 0, earlier = 0;
+        if (e < stride) {
+#pragma unroll 16
+            for (int s = 0; s < p.slices; ++s) {
+                const int v = p.hist[(int64_t)s * stride + e];
+                total += v;
+                earlier += s < (int)blockIdx.x ? v : 0;
+            }
+        }
+        int upto = total;  // inclusive sum over the wave
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_up(upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 63) sums[wave] = upto;
+        __syncthreads();
+        int at = before + upto - total;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < wave) at += sums[w];
+            before += sums[w];
+        }
+        if (e < stride) {
+            if (blockIdx.x == 0) p.offsets[e] = at;
+            at += earlier;
+            for (int w = 0; w < kWaves; ++w) {
+                const int v = next[w * stride + e];
+                next[w * stride + e] = at;
+                at += v;
+            }
+        }
+        __syncthreads();
+    }
+    const int bits = 32 - __builtin_clz(p.E);  // an expert index, E among them
+    for (int64_t q = r0; q < r1; q += 64) {
+        const bool there = q + lane < r1;
+        const int e = there ? expert_of(p, q + lane) : -1;
+        uint64_t same = __ballot(there);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t set = __ballot(e >> b & 1);
+            same &= e >> b & 1 ? set : ~set;
+        }
+        if (there) {
+            const uint64_t before_me = same & ((1ull << lane) - 1);
+            const int32_t row = next[wave * stride + e] + __builtin_popcountll(before_me);
+            p.place[q + lane] = e == p.E ? -1 - row : row;
+            __builtin_amdgcn_wave_barrier();
+            if (same >> lane == 1) next[wave * stride + e] = row + 1;  // the last of its expert
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void sort_copy_kernel(SortParams p) {
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const int32_t* place = p.place + t * p.k;
+        copy_row(p, t, blockIdx.y, gridDim.y, [&](int j) { return place[j]; });
+    }
+}
+
+// ---------------------------------------------------------------------------
+// back to the tokens
+// ---------------------------------------------------------------------------
+
+struct UnsortParams {
+    const void* ys;
+    const int32_t* place;
+    const float* w;
+    int64_t T, P, n;
+    int k;
+    void* y;
+    const void* dy;
+    void* d_ys;
+    float* d_w;
+};
+
+// A row of ys to read for a pair: its own, or row 0, which is then not used.
+__device__ __forceinline__ int64_t known(const UnsortParams& p, int32_t row) { return (uint32_t)row < (uint64_t)p.P ? row : 0; }
+
+// Slots are added in their order, each product rounded by itself, as iqk_combine
+// does: the two agree bit for bit.
+template <int ST, int YT>
+__global__ __launch_bounds__(kThreads) void unsort_kernel(UnsortParams p) {
+    const int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 8;
+    if (c >= p.n) return;
+    const int left = (int)min(p.n - c, (int64_t)8);
+    constexpr int kAhead = 8;  // rows asked for together
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        const int32_t* place = p.place + t * p.k;
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+            Raw<ST> r[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (j0 + j < p.k) r[j] = load_raw<ST>(p.ys, known(p, place[j0 + j]) * p.n + c, left);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (j0 + j >= p.k) continue;
+                float v[8];
+                widen_raw(r[j], v);
+                const float w = p.w ? p.w[t * p.k + j0 + j] : 1.f;
+                const bool there = (uint32_t)place[j0 + j] < (uint64_t)p.P;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float m = __fmul_rn(w, there ? v[i] : 0.f);
+                    acc[i] = j0 + j == 0 ? m : __fadd_rn(acc[i], m);
+                }
+            }
+        }
+        store_some<YT>(p.y, t * p.n + c, acc, left);
+    }
+}
+
+// A workgroup owns a token: dy's chunks are read once for all of its pairs (of
+// up to kKeys; further ones read them again), whose dot products are summed over
+// lanes and waves in a fixed order.
+template <int ST, int YT>
+__global__ __launch_bounds__(kThreads) void unsort_grad_kernel(UnsortParams p) {
+    __shared__ float part[kWaves][kKeys];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+        for (int j0 = 0; j0 < p.k; j0 += kKeys) {
+            const int32_t* place = p.place + t * p.k + j0;
+            const float* weight = p.w ? p.w + t * p.k + j0 : nullptr;
+            const int slots = min(kKeys, p.k - j0);
+            float dot[kKeys];
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) dot[j] = 0.f;
+            for (int64_t c = (int64_t)threadIdx.x * 8; c < p.n; c += kThreads * 8) {
+                const int left = (int)min(p.n - c, (int64_t)8);
+                float d[8];
+                const Raw<YT> dr = load_raw<YT>(p.dy, t * p.n + c, left);
+                Raw<ST> r[kKeys];
+                if (p.d_w) {
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j)
+                        if (j < slots) r[j] = load_raw<ST>(p.ys, known(p, place[j]) * p.n + c, left);
+                }
+                widen_raw(dr, d);
+                if (p.d_ys) {
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j) {
+                        if (j >= slots) continue;
+                        const int64_t row = place[j], to = row < 0 ? -1 - row : row;
+                        if (to >= p.P) continue;
+                        const float w = weight ? weight[j] : 1.f;
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = row < 0 ? 0.f : w * d[i];
+                        store_some<ST>(p.d_ys, to * p.n + c, v, left);
+                    }
+                }
+                if (p.d_w) {
+#pragma unroll
+                    for (int j = 0; j < kKeys; ++j) {
+                        if (j >= slots) continue;
+                        float v[8];
+                        widen_raw(r[j], v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
+                    }
+                }
+            }
+            if (!p.d_w) continue;
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) dot[j] = wave_sum(dot[j]);
+            if (lane == 0) {
+#pragma unroll
+                for (int j = 0; j < kKeys; ++j) part[wave][j] = dot[j];
+            }
+            __syncthreads();
+            if ((int)threadIdx.x < slots) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) v += part[w][threadIdx.x];
+                const bool there = (uint32_t)place[threadIdx.x] < (uint64_t)p.P;
+                p.d_w[t * p.k + j0 + threadIdx.x] = there ? v : 0.f;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+int64_t size_of(int dtype) { return dtype == IQK_F32 ? 4 : 2; }
+
+// Workgroups that share a token's row of `chunks` pieces of 16 bytes or 8 values:
+// each thread has one piece where tokens are few, more where they fill the card.
+unsigned row_parts(int64_t T, int64_t chunks) {
+    const int64_t most = std::max<int64_t>(1, (chunks + kThreads - 1) / kThreads);
+    return (unsigned)std::max<int64_t>(1, std::min(most, 2048 / std::max<int64_t>(T, 1)));
+}
+
+// Tokens that workgroups of their own start on; they step on by as many.
+unsigned token_groups(int64_t T) { return (unsigned)std::min<int64_t>(T, 1 << 22); }
+
+}  // namespace
+
+int sort_slices(int64_t P) {
+    if (P <= kDirect) return 0;
+    return (int)std::min(kSlices, (P + kSlicePairs - 1) / kSlicePairs);
+}
+
+hipError_t launch_sort(const SortLaunch& a, hipStream_t s) {
+    SortParams p{};
+    p.x = (const uint8_t*)a.x;
+    p.ids = a.ids;
+    p.T = a.T;
+    p.P = a.T * a.k;
+    p.k = a.k;
+    p.E = a.E;
+    p.row = a.n * size_of(a.dtype);
+    p.hist = a.hist;
+    p.xs = (uint8_t*)a.xs;
+    p.offsets = a.offsets;
+    p.place = a.place;
+    p.slices = sort_slices(p.P);
+    const int64_t chunks = p.row / 16;
+    if (p.slices == 0) {
+        p.tokens = 1;  // (kDirect tokens at most)
+        const int64_t groups = std::max<int64_t>(a.T, 1), parts = row_parts(a.T, chunks);
+        // (kKeys at least, and no more than the kMost - 64 + 64 / k .. entries a workgroup keeps: E <= 2048)
+        p.share = (int)std::max<int64_t>(kKeys, (a.E + groups * parts) / (groups * parts));
+        dim3 grid((unsigned)groups, (unsigned)parts);
+        if (p.share > kMost - a.k) {  // few workgroups and many experts: more of them, without rows
+            p.share = kKeys;
+            grid.x = (unsigned)std::max<int64_t>(groups, (a.E + kKeys) / kKeys);
+        }
+        hipLaunchKernelGGL(sort_direct_kernel, grid, dim3(kThreads), 0, s, p);
+        return hipGetLastError();
+    }
+    p.slice = (p.P + p.slices - 1) / p.slices;
+    const unsigned lds = (unsigned)(a.E + 1) * 4;
+    hipLaunchKernelGGL(sort_count_kernel, dim3((unsigned)p.slices), dim3(kThreads), lds, s, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sort_place_kernel, dim3((unsigned)p.slices), dim3(kThreads), kWaves * lds, s, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(sort_copy_kernel, dim3(token_groups(a.T), row_parts(a.T, chunks)), dim3(kThreads), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_unsort(const UnsortLaunch& a, hipStream_t s) {
+    UnsortParams p{};
+    p.ys = a.ys;
+    p.place = a.place;
+    p.w = a.weights;
+    p.T = a.T;
+    p.P = a.T * a.k;
+    p.n = a.n;
+    p.k = a.k;
+    p.y = a.y;
+    const dim3 grid(token_groups(a.T), (unsigned)((a.n + 8 * kThreads - 1) / (8 * kThreads)));
+    by_float(a.ys_dtype, [&](auto st) {
+        by_float(a.y_dtype, [&](auto yt) {
+            hipLaunchKernelGGL((unsort_kernel<decltype(st)::value, decltype(yt)::value>), grid, dim3(kThreads), 0, s, p);
+        });
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_unsort_grad(const UnsortGradLaunch& a, hipStream_t s) {
+    UnsortParams p{};
+    p.ys = a.ys;
+    p.place = a.place;
+    p.w = a.weights;
+    p.T = a.T;
+    p.P = a.T * a.k;
+    p.n = a.n;
+    p.k = a.k;
+    p.dy = a.dy;
+    p.d_ys = a.d_ys;
+    p.d_w = a.d_weights;
+    by_float(a.ys_dtype, [&](auto st) {
+        by_float(a.dy_dtype, [&](auto yt) {
+            hipLaunchKernelGGL((unsort_grad_kernel<decltype(st)::value, decltype(yt)::value>), dim3(token_groups(a.T)),
+                               dim3(kThreads), 0, s, p);
+        });
+    });
+    return hipGetLastError();
+}
+
+}  // namespace iqk

@@ -75,8 +75,9 @@ extern "C" {
 #endif
 
 typedef enum { IQK_IQ2_KS = 1, IQK_IQ2_K = 2, IQK_IQ1_S_R4 = 3 } iqk_format;
-typedef enum { IQK_F32 = 0, IQK_F16 = 1, IQK_BF16 = 2, IQK_E4M3 = 3 } iqk_dtype; /* E4M3: 8-bit products only */
+typedef enum { IQK_F32 = 0, IQK_F16 = 1, IQK_BF16 = 2, IQK_E4M3 = 3, IQK_INT8 = 4 } iqk_dtype; /* E4M3, INT8: 8-bit products only */
 typedef enum { IQK_SOFTMAX = 0, IQK_SIGMOID = 1 } iqk_scoring;
+typedef enum { IQK_GATE_NONE = 0, IQK_GATE_CHANNEL = 1, IQK_GATE_TOKEN = 2, IQK_GATE_ELEMENT = 3 } iqk_gate;
 typedef enum {
     IQK_OK = 0,
     IQK_E_ARG = -1,     /* null pointer, negative size, bad enum, bad count */
@@ -456,6 +457,142 @@ int iqk_moe_fp8(const iqk_fp8_weights* w, const void* x, int x_dtype, const floa
  * up to 32 dense rows in a pass over the weights, 2 = tiles; and for 2: [1]
  * rows of x and [2] weight rows in a tile, [3] parts of the depth; else 0. */
 int iqk_fp8_path(const iqk_fp8_weights* w, int64_t T, int k, int y_dtype, int32_t* path);
+
+/* ------------------------------------------------------------------------
+ * Token rows in the order of their experts, and back (iqk_route makes the order
+ * alone): for products over contiguous rows, experts of the caller's own, or an
+ * exchange between devices.
+ *
+ * Pair t * k + j of token t and slot j has the row it takes in a stable sort of
+ * all pairs by ids[t, j]; pairs whose id lies outside [0, E) come last and have
+ * no expert.  iqk_moe_sort: x device [T, n] and ids device int32 [T, k] -> xs
+ * device [T * k, n] with row(t, j) = x[t], zeros in rows of no expert; offsets
+ * device int32 [E + 1], offsets[e] = first row of expert e and offsets[E] = rows
+ * that have one; place device int32 [T, k], the pair's row, or -1 - row where it
+ * has no expert.  dtype IQK_F32, IQK_F16 or IQK_BF16, for x and xs.  workspace:
+ * iqk_moe_sort_workspace bytes (0 up to 8192 pairs; it may be null there),
+ * 4-byte aligned; its contents before the call make no difference.
+ * T >= 0, k in [1, 64], T * k <= 2^24, E <= 2048, n in [1, 2^20], n of any
+ * size (IQK_E_ARG); rows and pointers are aligned to their type. */
+int iqk_moe_sort_workspace(int64_t T, int k, int64_t E, size_t* bytes);
+int iqk_moe_sort(const void* x, int dtype, const int32_t* ids, int64_t T, int k, int64_t E, int64_t n,
+                 void* workspace, size_t ws_bytes, void* xs, int32_t* offsets, int32_t* place, void* stream);
+
+/* y[t] = sum_j weights[t, j] * ys[place[t, j]]: ys device [T * k, n] of ys_dtype,
+ * place from iqk_moe_sort, weights device float32 [T, k] or null for ones (the
+ * gradient of iqk_moe_sort by x, from that of xs) -> y device [T, n] of y_dtype
+ * (float types both).  A pair of no expert (place < 0, or not below T * k)
+ * counts as a row of zeros, so that the devices of a group sum up to the whole;
+ * its weight is still applied: a NaN weight (iqk_router_topk's for a row it
+ * could not choose for) makes the row NaN.  float32 sums in slot order, each
+ * product rounded by itself as in iqk_combine, one rounding to y_dtype. */
+int iqk_moe_unsort(const void* ys, int ys_dtype, const int32_t* place, const float* weights, int64_t T, int k,
+                   int64_t n, void* y, int y_dtype, void* stream);
+
+/* Gradient of iqk_moe_unsort from dy device [T, n] of dy_dtype: d_ys device
+ * [T * k, n] of ys_dtype, d_ys[row(t, j)] = weights[t, j] * dy[t], zeros in rows
+ * of no expert; d_weights device float32 [T, k], the dot product of dy[t] and
+ * ys[place[t, j]] (0 for a pair of no expert), float32 sums, the same every time.
+ * Either result may be null and is then not computed (ys may be null without
+ * d_weights).  place holds every row once, as iqk_moe_sort makes it. */
+int iqk_moe_unsort_grad(const void* dy, int dy_dtype, const void* ys, int ys_dtype, const int32_t* place,
+                        const float* weights, int64_t T, int k, int64_t n, void* d_ys, float* d_weights,
+                        void* stream);
+
+/* ------------------------------------------------------------------------
+ * Products in 8-bit integers, a float32 scale for each token and each output
+ * channel, dense and over rows sorted by expert.
+ *
+ * Weights: codes int8 [experts, out, in] and scales [experts, out], device,
+ * dense, row-major: the weight is code * scale of its row.  in % 16 == 0
+ * (IQK_E_SHAPE); in <= 2^16, out <= 2^20, out * in < 2^31, experts <= 2048;
+ * codes 16-byte aligned. */
+typedef struct iqk_int8_weights {
+    int64_t experts, out, in;
+    const void* codes;
+    size_t codes_bytes;  /* experts * out * in */
+    const float* scales;
+    size_t scales_count; /* experts * out */
+} iqk_int8_weights;
+
+/* Quantization of activations: x device [rows, n] (IQK_F32, IQK_F16 or IQK_BF16)
+ * -> codes int8 [rows, n], scales float32 [rows].  Per row: a = max(max |x|,
+ * 2^-100), scale = a / 127, code = x * (127 / a), the quotients and the product
+ * rounded to float32, the code to the nearest whole number, ties to even.  A row
+ * with a NaN or an infinity gets the scale NaN and codes zero.  n % 16 == 0
+ * (IQK_E_SHAPE), n <= 2^16, rows <= 2^24 (IQK_E_ARG); x and codes 16-byte
+ * aligned. */
+int iqk_int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, int8_t* codes, float* scales,
+                      void* stream);
+
+/* y[m, o] = (sum_i x_code[m, i] * w_code[o, i]) * (x_scale[m] * w_scale[o]); y
+ * device [M, out] of y_dtype (IQK_F32, IQK_F16 or IQK_BF16).  The sum is exact
+ * (in 32 bits); it, the product of the scales and theirs are rounded to float32,
+ * then once to y_dtype.  w->experts must be 1.  x: device [M, in], IQK_INT8 with
+ * x_scales [M], or a float type with x_scales null, which the call quantizes as
+ * iqk_int8_quantize does.  workspace (16-byte aligned, iqk_int8_linear_workspace
+ * bytes, 0 for a few rows) holds the quantized x, which IQK_INT8 x does without;
+ * it may be null where 0 bytes are needed.  x 16-byte aligned; M <= 2^24. */
+int iqk_int8_linear_workspace(const iqk_int8_weights* w, int64_t M, int x_dtype, size_t* bytes);
+int iqk_int8_linear(const iqk_int8_weights* w, const void* x, int x_dtype, const float* x_scales, int64_t M,
+                    void* workspace, size_t ws_bytes, void* y, int y_dtype, void* stream);
+
+/* The same product over rows in the order of their experts (iqk_moe_sort's xs
+ * and offsets): rows offsets[e] .. offsets[e + 1] - 1 of x device [rows, in] by
+ * expert e's weights -> y device [rows, out].  offsets device int32 [experts +
+ * 1], from 0, not falling, up to rows at most (others are cut to [0, rows]);
+ * rows from offsets[experts] on have no expert and get zeros.  rows <= 2^24. */
+int iqk_int8_grouped_workspace(const iqk_int8_weights* w, int64_t rows, int x_dtype, size_t* bytes);
+int iqk_int8_grouped(const iqk_int8_weights* w, const void* x, int x_dtype, const float* x_scales,
+                     const int32_t* offsets, int64_t rows, void* workspace, size_t ws_bytes, void* y, int y_dtype,
+                     void* stream);
+
+/* Which kernel a product of `rows` rows runs on, for tests and profiles: path
+ * (host, 3 values): [0] 0 = few rows, x quantized by every workgroup, 1 = tiles;
+ * and for 1: [1] rows of x and [2] weight rows in a tile; else 0. */
+int iqk_int8_path(const iqk_int8_weights* w, int64_t rows, int grouped, int32_t* path);
+
+/* ------------------------------------------------------------------------
+ * The norms around a block, its gate and the scaled residual, in one pass:
+ *
+ *   u = y * s(y) * post_weight   (u = y where post_weight is null)
+ *   r = alpha * x + beta * gate * u
+ *   h = r * s(r) * next_weight   s(v) = 1 / sqrt(mean(v^2) + eps) over a row
+ *
+ * x: the residual stream, y: the block's output (iqk_moe_unsort's or
+ * iqk_combine's among others), r: the stream behind the block, h: the next
+ * block's input.  h is taken from r before r's rounding.  All device, dense:
+ * x, r, h [T, n] of dtype; y [T, n] of y_dtype, which is dtype or IQK_F32;
+ * post_weight and next_weight [n] of weight_dtype; gate of gate_dtype: [n]
+ * (IQK_GATE_CHANNEL), [T] (IQK_GATE_TOKEN), [T, n] (IQK_GATE_ELEMENT), or null
+ * with IQK_GATE_NONE.  Float types all.  y may be null: then r = x, alpha must
+ * be 1, post_weight and gate null, and no r is written (the norm before the first
+ * block).  float32 arithmetic, one rounding to each result; squares are summed in
+ * float32, so rows of values beyond 1e17 are out of its range.  n in [1, 8192],
+ * n of any size; T <= 2^24; eps > 0; pointers aligned to their types. */
+typedef struct iqk_block {
+    int64_t T, n;
+    int32_t dtype, y_dtype, weight_dtype, gate_dtype, gate_kind;
+    float alpha, beta, eps;
+    const void *x, *y, *post_weight, *gate, *next_weight;
+} iqk_block;
+
+/* r: null exactly where y is; h: null exactly where next_weight is.  r may be x
+ * or y, and h as well (rows are read before they are written), where the types
+ * are the same; r and h differ. */
+int iqk_block_norm(const iqk_block* b, void* r, void* h, void* stream);
+
+/* Gradient of the above from dr and dh [T, n] of dtype (either may be null: zero;
+ * dh must be null where next_weight is): dx of dtype, dy of y_dtype, d_post and
+ * d_next [n] of weight_dtype, d_gate as gate.  Each result may be null and is then
+ * not computed; those of null inputs must be.  r is computed again from x and
+ * y.  Parameters' gradients are float32 sums over the tokens, in an order that
+ * depends on T and n alone, rounded once; results overlap no input.  workspace (16-byte aligned,
+ * iqk_block_norm_grad_workspace bytes) holds parts of those sums; it may be null
+ * where none are asked for. */
+int iqk_block_norm_grad_workspace(const iqk_block* b, size_t* bytes);
+int iqk_block_norm_grad(const iqk_block* b, const void* dr, const void* dh, void* dx, void* dy, void* d_post,
+                        void* d_gate, void* d_next, void* workspace, size_t ws_bytes, void* stream);
 
 /* Message of the last failed call on this thread ("" if none). */
 const char* iqk_last_error(void);
