@@ -1075,10 +1075,10 @@ def int8_grouped_workspace_bytes(w: Int8Weights, rows: int, x_dtype=torch.bfloat
 
 def int8_path(experts: int, out: int, n: int, rows: int, grouped: bool = False):
     """Which kernel int8_linear or int8_grouped runs on for weights [experts, out,
-    n], for tests and profiles: ("few",) or ("tiles", rows of x, weight rows)."""
+    n], for tests and profiles: ("few",), ("rows",) or ("tiles", rows of x, weight rows)."""
     path = (ctypes.c_int32 * 3)()
     _check(_lib.iqk_int8_path(ctypes.byref(_Int8Weights(experts, out, n)), rows, int(bool(grouped)), path))
-    return ("tiles", path[1], path[2]) if path[0] else ("few",)
+    return ("few", "rows", "tiles")[path[0]], *(path[1:] if path[0] == 2 else ())
 
 
 def int8_linear(w: Int8Weights, x: torch.Tensor, x_scales: torch.Tensor | None = None, out_dtype=torch.float32,

@@ -91,8 +91,12 @@ hipError_t launch_int8_prep(const Int8QuantLaunch& q, const Int8Plan& g, hipStre
 bool int8_few_fits(int64_t M, int64_t n, bool grouped);
 // few rows, x of any type
 hipError_t launch_int8_few(const Int8Launch& a, hipStream_t s);
+// whether launch_int8_rows takes M rows
+bool int8_rows_fits(int64_t M, int64_t out);
+// dense, x in codes, up to 32 rows
+hipError_t launch_int8_rows(const Int8Launch& a, hipStream_t s);
 // x in codes, by tiles
-Int8Tile int8_tile(int64_t M, int64_t E, int64_t out, bool grouped);
+Int8Tile int8_tile(int64_t M, int64_t E, int64_t out, int64_t n, bool grouped);
 hipError_t launch_int8_tile(const Int8Launch& a, const Int8Tile& tile, hipStream_t s);
 
 // What the gradient of a block's norms is taken from and written to (any may be

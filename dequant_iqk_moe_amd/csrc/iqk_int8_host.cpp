@@ -102,7 +102,8 @@ int product(const iqk_int8_weights* w, const void* x, int x_dtype, const float* 
     if (iqk::int8_few_fits(rows, w->in, grouped)) {
         e = iqk::launch_int8_few(L, s);
     } else {
-        const iqk::Int8Tile tile = iqk::int8_tile(rows, w->experts, w->out, grouped);
+        const bool few = !grouped && iqk::int8_rows_fits(rows, w->out);
+        const iqk::Int8Tile tile = iqk::int8_tile(rows, w->experts, w->out, w->in, grouped);
         uint8_t* at = (uint8_t*)workspace;
         iqk::Int8Plan plan{grouped ? offsets : nullptr, (int)w->experts, tile.rows, (int32_t*)at};
         at += plan_bytes(w, grouped);
@@ -115,7 +116,7 @@ int product(const iqk_int8_weights* w, const void* x, int x_dtype, const float* 
             L.x_dtype = IQK_INT8;
         }
         L.tiles = plan.tiles;
-        e = iqk::launch_int8_tile(L, tile, s);
+        e = few ? iqk::launch_int8_rows(L, s) : iqk::launch_int8_tile(L, tile, s);
     }
     if (e != hipSuccess) return hip_fail(e, "8-bit product launch");
     return ok();
@@ -180,8 +181,9 @@ int iqk_int8_path(const iqk_int8_weights* w, int64_t rows, int grouped, int32_t*
     if (!grouped && w->experts != 1) return fail(IQK_E_ARG, "the dense product takes one expert's weights");
     path[0] = path[1] = path[2] = 0;
     if (iqk::int8_few_fits(rows, w->in, grouped != 0)) return ok();
-    const iqk::Int8Tile t = iqk::int8_tile(rows, w->experts, w->out, grouped != 0);
-    path[0] = 1;
+    path[0] = !grouped && iqk::int8_rows_fits(rows, w->out) ? 1 : 2;
+    if (path[0] == 1) return ok();
+    const iqk::Int8Tile t = iqk::int8_tile(rows, w->experts, w->out, w->in, grouped != 0);
     path[1] = t.rows;
     path[2] = t.cols;
     return ok();

@@ -182,6 +182,8 @@ constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 constexpr int kFewAhead = 4;          // blocks of the depth a wave requests together
 constexpr int kFewBytes = 33 * 1024;  // most codes of x a workgroup keeps
 constexpr int64_t kFewGrouped = 32;   // rows of a grouped product up to which each may start a workgroup
+constexpr int kFewDense = 4;          // of a dense one (out = in = 4096: 4 rows 8.1 us against 9.1 with a launch for quantizing
+                                      // and int8_rows_kernel, 8 rows 11.0 against 9.5)
 constexpr int kFewRows = 16;
 constexpr int kDepth = 128;           // of a block
 
@@ -348,12 +350,82 @@ __global__ __launch_bounds__(kFewThreads) void int8_few_kernel(FewParams p) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// up to 16 NT rows of x in codes, dense
+// ---------------------------------------------------------------------------
+
+// As above, with x's fragments straight from memory (the L2, after the first
+// workgroups): each is used by one wave of the workgroup.  The next blocks are asked
+// for while the last ones are multiplied.
+// Bound: the fragments of x, which every 16 weight rows read again.
+template <int NT, int YT>
+__global__ __launch_bounds__(kFewThreads) void int8_rows_kernel(FewParams p) {
+    __shared__ int red[kFewWaves][NT][64][4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int li = lane & 15, g = lane >> 4;
+    const int n = p.n, nb = (n + kDepth - 1) / kDepth;
+    const int row0 = blockIdx.x * 16, left = min(16, p.out - row0);
+    const Rsrc wr = make_rsrc(p.W + (int64_t)row0 * n, (uint32_t)left * (uint32_t)n);  // (rows past the last read zero)
+    const uint32_t woff = (uint32_t)li * (uint32_t)n;
+    const int8_t* xr[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xr[t] = (const int8_t*)p.x + (int64_t)min(16 * t + li, p.M - 1) * n;  // (rows past the last repeat it)
+    struct Stage {
+        i32x4 w[2], x[NT][2];
+    } st[2];
+    // (blocks past the last have zero weights; a chunk of x past the depth is its row's first)
+    auto request = [&](int b, Stage& s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = b * kDepth + 16 * g + 64 * h;
+            const uint4 u = ld128(wr, c < n ? woff + c : kOob);
+            s.w[h] = i32x4{(int)u.x, (int)u.y, (int)u.z, (int)u.w};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s.x[t][h] = *(const i32x4*)(xr[t] + (c < n ? c : 0));
+        }
+    };
+    i32x4 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+    auto multiply = [&](const Stage& s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(s.w[h], s.x[t][h], acc[t], 0, 0, 0);
+    };
+    request(wave, st[0]);
+    for (int b = wave; b < nb; b += 2 * kFewWaves) {
+        request(b + kFewWaves, st[1]);
+        multiply(st[0]);
+        request(b + 2 * kFewWaves, st[0]);
+        multiply(st[1]);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) *(i32x4*)red[wave][t][lane] = acc[t];
+    __syncthreads();
+    // sixteen neighbouring threads write the results of one row of x
+    for (int i = threadIdx.x; i < 256 * NT; i += kFewThreads) {
+        const int r = i >> 4, o = i & 15;
+        if (r >= p.M || o >= left) continue;
+        int v = 0;
+#pragma unroll
+        for (int u = 0; u < kFewWaves; ++u) v += red[u][r >> 4][16 * (o >> 2) + (r & 15)][o & 3];
+        float f = (float)v * (p.sx[r] * p.sw[row0 + o]);
+        if constexpr (YT == IQK_F16) asm("" : "+v"(f));
+        store_y<YT>(p.y, (int64_t)r * p.out + row0 + o, f);
+    }
+}
+
 }  // namespace
 
 bool int8_few_fits(int64_t M, int64_t n, bool grouped) {
-    const int rows = few_rows(n);
-    return rows >= 1 && (grouped ? M <= kFewGrouped : M <= rows);
+    return grouped ? M <= kFewGrouped && few_rows(n) >= 1 : M <= std::min(kFewDense, few_rows(n));
 }
+
+// Every 16 weight rows read x again, which tiles of 128 do less often: out = 4096, in = 4096, 17 rows 10.9 us with the
+// quantization against 15.0 in tiles of 16 x 128, 33 rows (four fragments of x a weight) 14.9 against 15.0; out = 8192,
+// 32 rows 17.8 against 17.4; out = 16384, in = 2048, 17 rows 14.4 against 12.7.
+bool int8_rows_fits(int64_t M, int64_t out) { return M <= 32 && out <= 8192; }
 
 hipError_t launch_int8_prep(const Int8QuantLaunch& q, const Int8Plan& g, hipStream_t s) {
     const bool quantize = q.x_dtype != IQK_INT8;
@@ -387,6 +459,18 @@ hipError_t launch_int8_few(const Int8Launch& a, hipStream_t s) {
         };
         if (a.x_dtype == IQK_INT8) go(std::integral_constant<int, IQK_INT8>{});
         else by_float(a.x_dtype, go);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_rows(const Int8Launch& a, hipStream_t s) {
+    if (a.M > 32) return hipErrorInvalidValue;
+    const FewParams p{a.codes, a.scales, a.x, a.x_scales, (int)a.M, 1, (int)a.out, (int)a.n, nullptr, a.y};
+    const dim3 grid((unsigned)((a.out + 15) / 16)), block(kFewThreads);
+    by_float(a.y_dtype, [&](auto yt) {
+        constexpr int YT = decltype(yt)::value;
+        if (a.M <= 16) hipLaunchKernelGGL((int8_rows_kernel<1, YT>), grid, block, 0, s, p);
+        else hipLaunchKernelGGL((int8_rows_kernel<2, YT>), grid, block, 0, s, p);
     });
     return hipGetLastError();
 }

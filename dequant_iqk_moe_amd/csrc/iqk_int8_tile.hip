@@ -1,7 +1,7 @@
 // iqk_int8_tile.hip -- the 8-bit integer product tile by tile, dense or over rows
 // sorted by expert.
 //
-// A workgroup owns TM rows of x by TN weight rows.  Each block of BK of the depth goes
+// A workgroup owns TM rows of x by TN weight rows.  Each block of 128 of the depth goes
 // from memory straight into LDS, S - 1 blocks ahead.  The sums are int32 and exact, so they stay in the matrix instructions'
 // accumulators over the whole depth, and the scales are applied once at the end.
 #include <algorithm>
@@ -26,7 +26,6 @@ struct TileParams {
     int run;  // weight tiles a workgroup takes one after the other
     const int32_t *offsets, *tiles;
     void* y;
-    bool whole;  // y's rows begin at multiples of 16 bytes
 };
 
 // 16 bytes per lane from a buffer straight into LDS (zeros where the offset is past
@@ -46,15 +45,17 @@ __device__ __forceinline__ u32x4 tile_rsrc(const uint8_t* base, uint32_t bytes) 
     return u32x4{uniform((uint32_t)a), uniform((uint32_t)(a >> 32)), uniform(bytes), (uint32_t)kRsrcWord3};
 }
 
-// The 16-byte chunk c of a row in LDS is kept at slot c ^ key(row), so that eight
-// neighbouring lanes of a fragment, which read chunk c of eight rows, meet 128 bytes
-// no two of which are in one bank.  Rows of x: lane l reads row l + const.  Weight
-// rows: eight lanes' rows differ in bits 0, 1 and 3.  Two rows of 64 bytes share the
-// 128, which their lowest bit tells apart.
-template <int BK>
-__device__ __forceinline__ int xkey_of(int r) { return BK == 128 ? r & 7 : (r >> 1) & 3; }
-template <int BK>
-__device__ __forceinline__ int wkey_of(int r) { return BK == 128 ? (r & 3) | ((r >> 1) & 4) : ((r >> 1) & 1) | ((r >> 2) & 2); }
+// The 16-byte chunk c of a row in LDS is kept at slot c ^ key(row).  The 64 lanes of a
+// 16-byte read go in four turns of 256 bytes, lanes {0-3, 12-15, 20-27} of each 32
+// together and the others together (read off the conflict counter), so the sixteen of
+// a turn have to differ in their place modulo 256.  A fragment of 32 rows reads one
+// chunk of rows l, or of weight rows that are the same two sets, whose lowest bit
+// tells halves of the 256 apart.  Fragments of 16 rows read four chunks: rows l, and
+// weight rows that differ in bits 0, 1 and 3.
+template <int MF>
+__device__ __forceinline__ int xkey_of(int r) { return MF == 32 ? (r >> 1) & 7 : xkey(r); }
+template <int MF>
+__device__ __forceinline__ int wkey_of(int r) { return MF == 32 ? (r >> 1) & 7 : (r & 3) | ((r >> 1) & 4); }
 
 // Two results as 16-bit values, rounded to nearest even (the hardware's conversions).
 template <int YT>
@@ -62,6 +63,25 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     if constexpr (YT == IQK_F16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// min(left, 8) results
+template <int YT>
+__device__ __forceinline__ void store_eight(void* y, int64_t i, const float (&v)[8], int left) {
+    if constexpr (YT == IQK_F32) {
+        store8<YT>(y, i, v, left);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = pack2<YT>(v[2 * q], v[2 * q + 1]);
+        if (left >= 8) {
+            __builtin_memcpy((uint16_t*)y + i, w, 16);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < left) ((uint16_t*)y)[i + q] = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
+        }
+    }
 }
 
 // Matrix instructions of side MF (32: depth 32, 16: depth 64) and their accumulators.
@@ -80,35 +100,30 @@ struct Mfma<16> {
     static __device__ __forceinline__ Acc run(i32x4 a, i32x4 b, Acc c) { return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0); }
 };
 
-template <int TM, int TN, int WM, int WN, int BK, int S, int MF>
+template <int TM, int TN, int WM, int WN, int S, int MF>
 struct TileShape {
     static constexpr int kWaves = (TM / WM) * (TN / WN);
-    static_assert(MF == 32 || WN % 32 == 0, "tiles of 16 weight rows come in pairs");
-    // a tile of x with at most half of its rows there is one row of waves, each with fewer weight rows
-    static constexpr bool kHalves = TM == 256 && WM == 128;
-    static constexpr int kSteps = BK / Mfma<MF>::kDepth;         // instructions' depths in a block
-    static constexpr int kLanes = BK / 16;                       // lanes of a copy that share a row
-    static constexpr int kRowsPerCopy = 64 / kLanes * kWaves;    // rows one copy instruction of all waves covers
+    static_assert(WN % 32 == 0, "tiles of 16 weight rows come in pairs");
+    static constexpr int kSteps = kBlock / Mfma<MF>::kDepth;  // instructions' depths in a block
+    static constexpr int kRowsPerCopy = 8 * kWaves;           // rows one copy instruction of all waves covers
     static constexpr int kCW = TN / kRowsPerCopy;
     static constexpr int kCX = (TM + kRowsPerCopy - 1) / kRowsPerCopy;
     static constexpr int kCopies = kCW + kCX;  // memory instructions of a wave per block
-    static constexpr int kX = TN * BK;         // offset of x's rows in a stage
-    static constexpr int kStage = kX + kCX * kRowsPerCopy * BK;
-    // Results of large tiles go through LDS, 8 KiB of a wave at a time, and leave in whole rows of it.
-    static constexpr bool kStaged = kHalves;
-    static constexpr int kOut = 8192, kLds = S * kStage + (kStaged ? kWaves * kOut : 0);
+    static constexpr int kX = TN * kBlock;         // offset of x's rows in a stage
+    static constexpr int kStage = kX + kCX * kRowsPerCopy * kBlock;
+    static constexpr int kLds = S * kStage;
     static_assert(kLds <= 160 * 1024, "LDS");
     static constexpr int kResident = 2 * kLds <= 160 * 1024 ? 2 : 1;  // workgroups of a CU
 };
 
-template <int TM, int TN, int WM, int WN, int BK, int S, int MF, int YT, bool GROUPED, bool PART>
-__global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, WN, BK, S, MF>::kResident)) void int8_tile_kernel(TileParams p) {
-    using Sh = TileShape<TM, TN, WM, WN, BK, S, MF>;
+template <int TM, int TN, int WM, int WN, int S, int MF, int YT, bool GROUPED, bool PART>
+__global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, WN, S, MF>::kResident)) void int8_tile_kernel(TileParams p) {
+    using Sh = TileShape<TM, TN, WM, WN, S, MF>;
     using Mf = Mfma<MF>;
     constexpr int kSteps = Sh::kSteps;
     __shared__ __align__(16) uint8_t sh[Sh::kLds];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nb = (p.n + BK - 1) / BK;
+    const int nb = (p.n + kBlock - 1) / kBlock;
     const int ntn = (p.out + TN - 1) / TN, runs = (ntn + p.run - 1) / p.run;
 
     // which tile of x and run of weight tiles: those of one XCD (workgroups b with equal b % 8) are neighbours
@@ -155,10 +170,10 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
         }
     }
 
-    // copies: kLanes lanes move the slots of a row; rows past the last are past the buffer's records
-    const int crow = (wave * 64 + lane) / Sh::kLanes, cslot = lane % Sh::kLanes;
+    // copies: eight lanes move the slots of a row; rows past the last are past the buffer's records
+    const int crow = wave * 8 + (lane >> 3), cslot = lane & 7;
     static_assert(Sh::kRowsPerCopy % 16 == 0, "a lane's chunk is the same in all of its copies");
-    const int wch = 16 * (cslot ^ wkey_of<BK>(crow)), xch = 16 * (cslot ^ xkey_of<BK>(crow));
+    const int wch = 16 * (cslot ^ wkey_of<MF>(crow)), xch = 16 * (cslot ^ xkey_of<MF>(crow));
     const uint32_t woff = (uint32_t)(crow * p.n + wch), xoff = (uint32_t)(crow * p.n + xch);
     const uint32_t apart = (uint32_t)(Sh::kRowsPerCopy * p.n);  // of a lane's rows in two copies
     const uint8_t* xbase = p.x + (begin + m0) * p.n;
@@ -177,14 +192,14 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
     // block is partial, and chunks past the depth are zero.  (Once the last block is on its way the last tile's first
     // one is copied again, which nothing reads: every step takes as many instructions, and the waits count them.)
     auto copy = [&](int c, int slot) {
-        const uint32_t k0 = cb * BK, at = sh0 + slot * Sh::kStage + wave * 1024;
+        const uint32_t k0 = cb * kBlock, at = sh0 + slot * Sh::kStage + wave * 1024;
         if (c < Sh::kCW) {
             const uint32_t off = PART && (int)k0 + wch >= p.n ? kOob : woff;
-            lds_copy16(tile_rsrc(wbase + k0, wbytes - k0), off + c * apart, at + c * Sh::kRowsPerCopy * BK);
+            lds_copy16(tile_rsrc(wbase + k0, wbytes - k0), off + c * apart, at + c * Sh::kRowsPerCopy * kBlock);
         } else {
             const int i = c - Sh::kCW;
             const uint32_t off = PART && (int)k0 + xch >= p.n ? kOob : xoff;
-            lds_copy16(tile_rsrc(xbase + k0, xbytes - k0), off + i * apart, at + Sh::kX + i * Sh::kRowsPerCopy * BK);
+            lds_copy16(tile_rsrc(xbase + k0, xbytes - k0), off + i * apart, at + Sh::kX + i * Sh::kRowsPerCopy * kBlock);
         }
     };
     auto advance = [&]() {
@@ -213,8 +228,8 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
     publish<kBehind>();
 
     // the tiles by this wave: kI tiles of weight rows from wn on and kJ of x from wm on
-    auto multiply = [&](auto ki, auto kj, const int wn, const int wm) {
-        constexpr int kI = decltype(ki)::value, kJ = decltype(kj)::value;
+    auto multiply = [&](const int wn, const int wm) {
+        constexpr int kI = WN / MF, kJ = WM / MF;
         int slot = 0;
         if (wm >= rows) {  // none of its rows of x is there: it copies for the others
             for (int step = 0; step < steps; ++step) {
@@ -228,23 +243,18 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
             return;
         }
         typename Mf::Acc acc[kI][kJ];
-        const int aoff = (wn + afirst) * BK + 16 * (g ^ wkey_of<BK>(afirst));
-        const int boff = Sh::kX + (wm + l) * BK + 16 * (g ^ xkey_of<BK>(l));
+        const int aoff = (wn + afirst) * kBlock + 16 * (g ^ wkey_of<MF>(afirst));
+        const int boff = Sh::kX + (wm + l) * kBlock + 16 * (g ^ xkey_of<MF>(l));
         // fragments of weight tile i and x tile j at depth step k of the stage at s
         auto afrag = [&](const uint8_t* s, int i, int k) {
-            const int tile = (MF == 32 ? i * 32 : (i >> 1) * 32 + (i & 1) * 4) * BK;
+            const int tile = (MF == 32 ? i * 32 : (i >> 1) * 32 + (i & 1) * 4) * kBlock;
             return *(const i32x4*)(s + (aoff ^ (k * Mf::kDepth)) + tile);
         };
-        auto bfrag = [&](const uint8_t* s, int j, int k) { return *(const i32x4*)(s + (boff ^ (k * Mf::kDepth)) + j * MF * BK); };
+        auto bfrag = [&](const uint8_t* s, int j, int k) { return *(const i32x4*)(s + (boff ^ (k * Mf::kDepth)) + j * MF * kBlock); };
 
         // value q of the eight of piece h (of 16 outputs, or of 32 of two tiles of 16 rows) in x tile j
         auto value = [&](int h, int j, int q, float scale) {
-            int a = MF == 32 ? acc[h >> 1][j][8 * (h & 1) + q] : acc[2 * h + (q >> 2)][j][q & 3];
-            // (a large tile's sums fill the accumulation registers, and the compiler would move all of them at once)
-            if constexpr (Sh::kStaged) {
-                const int in = a;
-                asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(a) : "a"(in));
-            }
+            const int a = MF == 32 ? acc[h >> 1][j][8 * (h & 1) + q] : acc[2 * h + (q >> 2)][j][q & 3];
             float v = (float)a * scale;
             // (fused with the conversion to f16 the product would round once, where the definition's rounds twice)
             if constexpr (YT == IQK_F16) asm("" : "+v"(v));
@@ -266,82 +276,18 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
             for (int h = 0; h < kPieces; ++h)
 #pragma unroll
                 for (int q = 0; q < 8; ++q) sw[h][q] = __uint_as_float(ld32(sr, (uint32_t)(n0 + wn + 8 * g) * 4 + (kPiece * h + q) * 4));
-            if constexpr (!Sh::kStaged) {
 #pragma unroll
-                for (int h = 0; h < kPieces; ++h) {
-                    const int o = n0 + wn + kPiece * h + 8 * g;
+            for (int h = 0; h < kPieces; ++h) {
+                const int o = n0 + wn + kPiece * h + 8 * g;
 #pragma unroll
-                    for (int j = 0; j < kJ; ++j) {
-                        const int i = wm + MF * j + l;
-                        float v[8];
+                for (int j = 0; j < kJ; ++j) {
+                    const int i = wm + MF * j + l;
+                    float v[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] = value(h, j, q, sx[j] * sw[h][q]);
-                        if (i < rows && o < p.out) store8<YT>(p.y, (begin + m0 + i) * p.out + o, v, p.out - o);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);  // (else all of the tile's values are wanted at once)
+                    for (int q = 0; q < 8; ++q) v[q] = value(h, j, q, sx[j] * sw[h][q]);
+                    if (i < rows && o < p.out) store_eight<YT>(p.y, (begin + m0 + i) * p.out + o, v, p.out - o);
                 }
-            } else {
-                // (the reads below are not the compiler's: the last products' results are waited for here)
-                __builtin_amdgcn_sched_barrier(0);
-                asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
-                // 32 rows of x by kCols outputs, 16 bytes at slot c ^ (row & 15 or less) of a row; lanes then take
-                // neighbouring chunks of a row
-                constexpr int kSize = YT == IQK_F32 ? 4 : 2, kAll = kI * 32, kCols = kAll * kSize > 256 ? 256 / kSize : kAll;
-                constexpr int kChunks = kCols * kSize / 16, kPer = 16 / kSize;  // chunks of a row, values of a chunk
-                uint8_t* mine = sh + S * Sh::kStage + wave * Sh::kOut;
-                const Rsrc yr = make_rsrc((uint8_t*)p.y + (begin + m0) * p.out * kSize, (uint32_t)rows * (uint32_t)p.out * kSize);
-#pragma unroll
-                for (int c0 = 0; c0 < kAll; c0 += kCols) {
-#pragma unroll
-                    for (int j = 0; j < kJ; ++j) {
-#pragma unroll
-                        for (int h = c0 / 16; h < (c0 + kCols) / 16; ++h) {
-                            float v[8];
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) v[q] = value(h, j, q, sx[j] * sw[h][q]);
-                            const int chunk = ((16 * h - c0) + 8 * g) / kPer;
-                            auto slot = [&](int c) { return (uint4*)(mine + l * kChunks * 16 + 16 * (c ^ (l & (kChunks - 1)))); };
-                            if constexpr (YT == IQK_F32) {
-                                *(float4*)slot(chunk) = make_float4(v[0], v[1], v[2], v[3]);
-                                *(float4*)slot(chunk + 1) = make_float4(v[4], v[5], v[6], v[7]);
-                            } else {
-                                uint4 w;
-                                w.x = pack2<YT>(v[0], v[1]), w.y = pack2<YT>(v[2], v[3]), w.z = pack2<YT>(v[4], v[5]), w.w = pack2<YT>(v[6], v[7]);
-                                *slot(chunk) = w;
-                            }
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                        auto piece = [&](int u) { return *(const uint4*)(mine + u / kChunks * kChunks * 16 + 16 * (u % kChunks ^ (u / kChunks & (kChunks - 1)))); };
-                        if (p.whole) {  // (rows past the last are past the records, outputs are made so)
-                            constexpr int kTurns = 32 * kChunks / 64;
-                            uint4 w[kTurns];
-#pragma unroll
-                            for (int u = 0; u < kTurns; ++u) w[u] = piece(u * 64 + lane_);
-#pragma unroll
-                            for (int u = 0; u < kTurns; ++u) {
-                                const int at = u * 64 + lane_, o = n0 + wn + c0 + at % kChunks * kPer;
-                                const uint32_t to = (uint32_t)((wm + 32 * j + at / kChunks) * p.out + o) * kSize;
-                                __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[u].x, w[u].y, w[u].z, w[u].w}, yr, o < p.out ? to : kOob, 0, 0);
-                            }
-                        } else {
-#pragma unroll 1
-                            for (int u = lane_; u < 32 * kChunks; u += 64) {
-                                const int i = wm + 32 * j + u / kChunks, o = n0 + wn + c0 + u % kChunks * kPer;
-                                if (i >= rows || o >= p.out) continue;
-                                const uint4 w = piece(u);
-                                const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                for (int q = 0; q < kPer; ++q) {
-                                    if (o + q >= p.out) continue;
-                                    const int64_t at = (begin + m0 + i) * p.out + o + q;
-                                    if constexpr (YT == IQK_F32) ((uint32_t*)p.y)[at] = a[q];
-                                    else ((uint16_t*)p.y)[at] = (uint16_t)(a[q / 2] >> (16 * (q & 1)));
-                                }
-                            }
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
+                __builtin_amdgcn_sched_barrier(0);  // (else all of the tile's values are wanted at once)
             }
         };
 
@@ -406,14 +352,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
             store_tile();
         }
     };
-    constexpr int kI = WN / MF, kJ = WM / MF;
-    const int wn = (wave % (TN / WN)) * WN, wm = (wave / (TN / WN)) * WM;
-    if (Sh::kHalves && rows <= TM / 2) {
-        constexpr int kRows = TM / WM;
-        multiply(std::integral_constant<int, Sh::kHalves ? kI / kRows : kI>{}, std::integral_constant<int, kJ>{}, wave * (WN / kRows), 0);
-    } else {
-        multiply(std::integral_constant<int, kI>{}, std::integral_constant<int, kJ>{}, wn, wm);
-    }
+    multiply((wave % (TN / WN)) * WN, (wave / (TN / WN)) * WM);
     // no copy may land in the LDS of the workgroup that gets it next
     __builtin_amdgcn_s_waitcnt(0x0070);
 }
@@ -421,52 +360,71 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
 constexpr int64_t kMaxRun = 2;
 
 // TM x TN tiles by waves of WM x WN, S stages
-template <int TM, int TN, int WM, int WN, int BK, int S, int MF, int YT, bool GROUPED>
+template <int TM, int TN, int WM, int WN, int S, int MF, int YT, bool GROUPED>
 hipError_t tile_launch(const Int8Launch& a, hipStream_t s) {
-    using Sh = TileShape<TM, TN, WM, WN, BK, S, MF>;
+    using Sh = TileShape<TM, TN, WM, WN, S, MF>;
     const int64_t ntn = (a.out + TN - 1) / TN;
     const int64_t tiles = (a.M + TM - 1) / TM + (GROUPED ? std::min<int64_t>(a.E + 1, a.M) : 0);  // (partial last tiles)
     constexpr int64_t kResident = 256 * Sh::kResident;
     auto turns = [&](int64_t run) { return (tiles * ((ntn + run - 1) / run) + kResident - 1) / kResident * run; };
     int64_t run = 1;
-    while ((TM <= 64 || !GROUPED) && run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
+    while (!GROUPED && run < kMaxRun && 2 * run <= ntn && turns(2 * run) * 16 <= turns(1) * 17) run *= 2;
     const TileParams p{(const uint8_t*)a.codes, a.scales, (const uint8_t*)a.x, a.x_scales, a.M, (int)a.out, (int)a.n, (int)a.E,
-                       (int)run, a.offsets, a.tiles, a.y, a.out % (a.y_dtype == IQK_F32 ? 4 : 8) == 0 && (uintptr_t)a.y % 16 == 0};
+                       (int)run, a.offsets, a.tiles, a.y};
     const int64_t total = tiles * ((ntn + run - 1) / run);
     if (total >= (int64_t)(UINT32_MAX / (64 * Sh::kWaves))) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)((total + 7) / 8 * 8)), block(64 * Sh::kWaves);
-    if (a.n % BK) hipLaunchKernelGGL((int8_tile_kernel<TM, TN, WM, WN, BK, S, MF, YT, GROUPED, true>), grid, block, 0, s, p);
-    else hipLaunchKernelGGL((int8_tile_kernel<TM, TN, WM, WN, BK, S, MF, YT, GROUPED, false>), grid, block, 0, s, p);
+    if (a.n % kBlock) hipLaunchKernelGGL((int8_tile_kernel<TM, TN, WM, WN, S, MF, YT, GROUPED, true>), grid, block, 0, s, p);
+    else hipLaunchKernelGGL((int8_tile_kernel<TM, TN, WM, WN, S, MF, YT, GROUPED, false>), grid, block, 0, s, p);
     return hipGetLastError();
 }
 
+// Tiles, and what one takes where each CU has one: microseconds before its first block and behind its last, and for
+// each block of 128 of the depth (measured, bfloat16 results: 1024 x 4096 x 4096 in tiles of 128 x 128 26 us, 2048 rows
+// in 128 x 256 38, 8192 in 256 x 256 129; 8 experts of 1024 x 4096 with 37 rows each in tiles of 16, 32 and 64 rows 15,
+// 18 and 19).  Where two tiles share a CU they take about twice as long.
+struct Kind {
+    int rows, cols;
+    double fixed, block;
+    bool shared;
+};
+constexpr Kind kKinds[] = {{16, 128, 4, 0.34, true},  {32, 128, 4, 0.43, true},  {64, 128, 4, 0.48, true},
+                           {128, 128, 5, 0.62, false}, {128, 256, 8, 0.85, false}, {256, 256, 15, 1.45, false}};
+
 }  // namespace
 
-Int8Tile int8_tile(int64_t M, int64_t E, int64_t out, bool grouped) {
-    auto count = [&](int64_t t) { return (M + t - 1) / t * ((out + t - 1) / t); };
-    if (!grouped) return count(256) >= 160 ? Int8Tile{256, 256} : (count(128) >= 160 ? Int8Tile{128, 128} : Int8Tile{64, 64});
-    const double per = (double)M / (double)E, spread = std::sqrt(per);
-    if (per + 2 * spread <= 16) return {16, 128};
-    if (per + spread <= 32) return {32, 128};
-    if (per + 2 * spread <= 64) return {64, 128};
-    return per >= 192 && count(256) >= 160 ? Int8Tile{256, 256} : Int8Tile{128, 128};
+// The kind whose rounds over the 256 CUs take the shortest by that, or as long as the weights from memory; the one of
+// the fewest rows of those within 5 % of it.  (Experts' last tiles are half full in the mean.)
+Int8Tile int8_tile(int64_t M, int64_t E, int64_t out, int64_t n, bool grouped) {
+    const double blocks = (double)((n + 127) / 128), used = grouped ? (double)std::min(M, E) : 0.0;
+    const double bytes = std::max(used, 1.0) * (double)(out * n) / 5.3e6;
+    auto us = [&](const Kind& k) {
+        const double rows = grouped ? (double)M / k.rows + used / 2 : (double)((M + k.rows - 1) / k.rows);
+        const double rounds = rows * (double)((out + k.cols - 1) / k.cols) / 256;
+        return std::max(bytes, (k.shared ? std::max(rounds, 1.0) : std::ceil(rounds)) * (k.fixed + k.block * blocks));
+    };
+    double best = us(kKinds[0]);
+    for (const Kind& k : kKinds) best = std::min(best, us(k));
+    for (const Kind& k : kKinds)
+        if (us(k) <= 1.05 * best) return Int8Tile{k.rows, k.cols};
+    return Int8Tile{256, 256};
 }
 
 hipError_t launch_int8_tile(const Int8Launch& a, const Int8Tile& t, hipStream_t s) {
     hipError_t e = hipSuccess;
     by_float(a.y_dtype, [&](auto yt) {
-        constexpr int YT = decltype(yt)::value;
-        if (a.offsets) {
-            if (t.rows == 16) e = tile_launch<16, 128, 16, 32, 128, 4, 16, YT, true>(a, s);
-            else if (t.rows == 32) e = tile_launch<32, 128, 32, 32, 128, 3, 16, YT, true>(a, s);
-            else if (t.rows == 64) e = tile_launch<64, 128, 32, 64, 128, 2, 32, YT, true>(a, s);
-            else if (t.rows == 128) e = tile_launch<128, 128, 64, 64, 128, 2, 32, YT, true>(a, s);
-            else e = tile_launch<256, 256, 128, 128, 64, 4, 32, YT, true>(a, s);
-        } else {
-            if (t.rows == 64) e = tile_launch<64, 64, 32, 32, 128, 4, 32, YT, false>(a, s);
-            else if (t.rows == 128) e = tile_launch<128, 128, 64, 64, 128, 2, 32, YT, false>(a, s);
-            else e = tile_launch<256, 256, 128, 128, 64, 4, 32, YT, false>(a, s);
-        }
+        auto go = [&](auto grouped) {
+            constexpr int YT = decltype(yt)::value;
+            constexpr bool G = decltype(grouped)::value;
+            if (t.rows == 16) e = tile_launch<16, 128, 16, 32, 4, 16, YT, G>(a, s);
+            else if (t.rows == 32) e = tile_launch<32, 128, 32, 32, 3, 16, YT, G>(a, s);
+            else if (t.rows == 64) e = tile_launch<64, 128, 32, 64, 3, 32, YT, G>(a, s);
+            else if (t.cols == 128) e = tile_launch<128, 128, 64, 64, 4, 32, YT, G>(a, s);
+            else if (t.rows == 128) e = tile_launch<128, 256, 64, 64, 3, 32, YT, G>(a, s);
+            else e = tile_launch<256, 256, 64, 128, 2, 32, YT, G>(a, s);
+        };
+        if (a.offsets) go(std::true_type{});
+        else go(std::false_type{});
     });
     return e;
 }

@@ -548,8 +548,9 @@ int iqk_int8_grouped(const iqk_int8_weights* w, const void* x, int x_dtype, cons
                      void* stream);
 
 /* Which kernel a product of `rows` rows runs on, for tests and profiles: path
- * (host, 3 values): [0] 0 = few rows, x quantized by every workgroup, 1 = tiles;
- * and for 1: [1] rows of x and [2] weight rows in a tile; else 0. */
+ * (host, 3 values): [0] 0 = few rows, x quantized by every workgroup, 1 = up to 32
+ * dense rows in a pass over the weights, 2 = tiles; and for 2: [1] rows of x and
+ * [2] weight rows in a tile; else 0. */
 int iqk_int8_path(const iqk_int8_weights* w, int64_t rows, int grouped, int32_t* path);
 
 /* ------------------------------------------------------------------------

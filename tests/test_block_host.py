@@ -118,7 +118,7 @@ def test_product_workspaces():
     for dtype, want in ((BF16, 100 * 512 + 512), (INT8, 0)):
         assert L.iqk_int8_linear_workspace(ctypes.byref(w), 100, dtype, ctypes.byref(need)) == 0 and need.value == want
         assert L.iqk_int8_grouped_workspace(ctypes.byref(w), 100, dtype, ctypes.byref(need)) == 0 and need.value == want + 256
-    assert L.iqk_int8_linear_workspace(ctypes.byref(w), 16, BF16, ctypes.byref(need)) == 0 and need.value == 0
+    assert L.iqk_int8_linear_workspace(ctypes.byref(w), 4, BF16, ctypes.byref(need)) == 0 and need.value == 0
     assert L.iqk_int8_linear_workspace(ctypes.byref(w), 16, E4M3, ctypes.byref(need)) == E_ARG
     assert L.iqk_int8_linear_workspace(ctypes.byref(w), 16, BF16, None) == E_ARG
 

@@ -84,11 +84,14 @@ def test_quantize_shapes_and_no_rows():
 # dense product
 # ---------------------------------------------------------------------------
 
-# sizes at which each kernel of the dense product runs
-DENSE = [((1, 33, 16), ("few",)), ((8, 64, 4096), ("few",)), ((9, 40, 4096), ("tiles", 64, 64)), ((16, 17, 1040), ("few",)),
-         ((1, 20, 33000 // 16 * 16), ("few",)), ((1, 20, 65536), ("tiles", 64, 64)), ((17, 257, 144), ("tiles", 64, 64)),
-         ((77, 130, 512), ("tiles", 64, 64)), ((65, 63, 2064), ("tiles", 64, 64)), ((2000, 1290, 272), ("tiles", 128, 128)),
-         ((1301, 2101, 128), ("tiles", 128, 128)), ((2600, 4100, 400), ("tiles", 256, 256)), ((4097, 2600, 128), ("tiles", 256, 256))]
+# sizes (rows, out, in) at which each kernel of the dense product runs
+DENSE = [((1, 33, 16), ("few",)), ((4, 64, 4096), ("few",)), ((3, 17, 1040), ("few",)), ((1, 20, 32992), ("few",)),
+         ((1, 20, 65536), ("rows",)), ((5, 257, 144), ("rows",)), ((16, 40, 2064), ("rows",)), ((17, 100, 4096), ("rows",)),
+         ((32, 33, 16), ("rows",)), ((7, 9000, 64), ("tiles", 16, 128)), ((34, 116, 64), ("tiles", 16, 128)),
+         ((77, 130, 528), ("tiles", 16, 128)), ((48, 16391, 144), ("tiles", 32, 128)), ((2980, 131, 80), ("tiles", 32, 128)),
+         ((1869, 516, 64), ("tiles", 64, 128)), ((300, 4001, 2064), ("tiles", 64, 128)), ((2000, 1290, 272), ("tiles", 128, 128)),
+         ((1301, 2101, 128), ("tiles", 128, 128)), ((2382, 1743, 64), ("tiles", 128, 256)), ((2048, 4096, 272), ("tiles", 128, 256)),
+         ((2600, 4100, 400), ("tiles", 256, 256)), ((3202, 2505, 272), ("tiles", 256, 256))]
 
 
 @pytest.mark.parametrize("size,path", DENSE)
@@ -123,19 +126,19 @@ def test_linear(size, path, dtype):
 def test_largest_sums():
     """65536 products of -128 by -128: 2^30."""
     w = q.Int8Weights(torch.full((1, 70, 65536), -128, dtype=torch.int8, device="cuda"), torch.ones(1, 70, device="cuda"))
-    x = torch.full((20, 65536), -128, dtype=torch.int8, device="cuda")
-    for rows in (1, 20):
+    x = torch.full((40, 65536), -128, dtype=torch.int8, device="cuda")
+    for rows in (1, 20, 40):
         assert (q.int8_linear(w, x[:rows], torch.ones(rows, device="cuda")) == 2.0 ** 30).all()
 
 
 def test_rows_with_nan_or_infinity_keep_to_themselves():
-    for rows, n in ((6, 256), (300, 256), (300, 16)):
+    for rows, n in ((4, 256), (6, 256), (300, 256), (300, 16)):
         x = _x(rows, n, torch.float32, 1)
-        x[1, 3], x[4, 5] = float("nan"), float("inf")
+        x[1, 3], x[3, 5] = float("nan"), float("inf")
         w = _dev(*_w(1, 80, n))
         y = q.int8_linear(w, x.cuda()).cpu()
-        assert y.isnan().all(1).nonzero().flatten().tolist() == [1, 4]
-        assert torch.isfinite(y[[0, 2, 3, 5]]).all()
+        assert y.isnan().all(1).nonzero().flatten().tolist() == [1, 3]
+        assert torch.isfinite(y[[0, 2] + list(range(4, rows))]).all()
     scales = torch.full((1, 80), 1e-2)
     scales[0, 7], scales[0, 8] = float("nan"), float("inf")
     w = q.Int8Weights(w.codes, scales.cuda())
@@ -152,7 +155,7 @@ def test_leading_dimensions_and_no_rows():
 
 
 def test_a_rows_bits_do_not_depend_on_its_place():
-    for M, out, n in ((12, 100, 2048), (100, 100, 512), (2000, 1290, 272), (2600, 4100, 400)):
+    for M, out, n in ((4, 100, 2048), (29, 100, 2048), (100, 100, 512), (1869, 516, 64), (2000, 1290, 272), (2382, 1743, 64), (2600, 4100, 400)):
         x, w = _x(M, n, torch.bfloat16, 5).cuda(), _dev(*_w(1, out, n))
         perm = torch.randperm(M, generator=torch.Generator().manual_seed(1)).cuda()
         for dtype in TYPES:
@@ -176,13 +179,15 @@ def test_workspace_of_exactly_the_size_asked_for():
 # grouped product
 # ---------------------------------------------------------------------------
 
-# (experts, out, in, rows of each expert drawn from, rows of none) -> kernel
+# (experts, out, in, rows of each expert, rows of none) at which each kernel of the grouped product runs
 GROUPED = [((3, 33, 64, [2, 0, 1], 0), ("few",)), ((256, 40, 4096, [0] * 200 + [1] * 6 + [0] * 50, 2), ("few",)),
            ((4, 30, 2048, [30, 0, 0, 2], 0), ("few",)), ((2, 20, 65536, [1, 2], 1), ("tiles", 16, 128)),
-           ((60, 141, 272, [5] * 30 + [0, 9] * 15, 3), ("tiles", 16, 128)), ((8, 300, 144, [21, 25, 0, 40, 18, 22, 31, 1], 0), ("tiles", 32, 128)),
-           ((8, 300, 128, [47, 49, 64, 65, 0, 30, 41, 50], 20), ("tiles", 64, 128)), ((1, 130, 512, [200], 0), ("tiles", 128, 128)),
-           ((3, 257, 400, [129, 127, 128], 70), ("tiles", 128, 128)), ((5, 2600, 144, [1200, 0, 900, 257, 1300], 300), ("tiles", 256, 256)),
-           ((2, 50, 16, [0, 0], 50), ("tiles", 32, 128))]
+           ((60, 141, 272, [5] * 30 + [0, 9] * 15, 3), ("tiles", 16, 128)), ((3, 257, 400, [129, 127, 128], 70), ("tiles", 16, 128)),
+           ((2, 50, 16, [0, 0], 50), ("tiles", 16, 128)), ((16, 131, 64, [250, 0] * 4 + [149] * 8, 186), ("tiles", 32, 128)),
+           ((16, 1024, 2048, [50] * 10 + [0, 99] * 3, 3), ("tiles", 32, 128)), ((40, 262, 64, [0, 115, 57] * 13 + [40], 19), ("tiles", 64, 128)),
+           ((40, 711, 80, [61, 0, 64, 65, 100] * 8, 0), ("tiles", 128, 128)), ((8, 4100, 256, [300, 0, 250, 290, 310, 280, 340, 250], 9), ("tiles", 128, 128)),
+           ((16, 1000, 512, [300, 255, 129, 0] * 4, 2000), ("tiles", 128, 256)),
+           ((16, 2997, 144, [257, 130, 0, 390] * 4, 0), ("tiles", 256, 256))]
 
 
 @pytest.mark.parametrize("size,path", GROUPED)

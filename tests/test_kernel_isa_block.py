@@ -22,4 +22,4 @@ def test_no_scratch(src, tmp_path):
     assert bool(at) == (src == "iqk_int8_tile.hip")
     for i in at:
         assert lines[i].startswith("s_mov_b32 m0, s") and lines[i + 1] == "s_nop 0", lines[i:i + 3]
-        assert lines[i + 2].startswith("global_load_lds_dword"), lines[i:i + 3]
+        assert re.match(r"buffer_load_dwordx4 .* lds$", lines[i + 2]), lines[i:i + 3]
