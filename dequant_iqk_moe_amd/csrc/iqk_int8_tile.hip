@@ -8,7 +8,7 @@
 #include <cmath>
 
 #include "iqk_block.h"
-#include "iqk_fp8_device.h"
+#include "iqk_rows_device.h"
 
 namespace iqk {
 namespace {
@@ -56,33 +56,6 @@ template <int MF>
 __device__ __forceinline__ int xkey_of(int r) { return MF == 32 ? (r >> 1) & 7 : xkey(r); }
 template <int MF>
 __device__ __forceinline__ int wkey_of(int r) { return MF == 32 ? (r >> 1) & 7 : (r & 3) | ((r >> 1) & 4); }
-
-// Two results as 16-bit values, rounded to nearest even (the hardware's conversions).
-template <int YT>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    if constexpr (YT == IQK_F16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
-}
-
-// min(left, 8) results
-template <int YT>
-__device__ __forceinline__ void store_eight(void* y, int64_t i, const float (&v)[8], int left) {
-    if constexpr (YT == IQK_F32) {
-        store8<YT>(y, i, v, left);
-    } else {
-        uint32_t w[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] = pack2<YT>(v[2 * q], v[2 * q + 1]);
-        if (left >= 8) {
-            __builtin_memcpy((uint16_t*)y + i, w, 16);
-        } else {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < left) ((uint16_t*)y)[i + q] = (uint16_t)(w[q / 2] >> (16 * (q & 1)));
-        }
-    }
-}
 
 // Matrix instructions of side MF (32: depth 32, 16: depth 64) and their accumulators.
 template <int MF>
@@ -285,7 +258,7 @@ __global__ __launch_bounds__(64 * (TM / WM) * (TN / WN), (TileShape<TM, TN, WM, 
                     float v[8];
 #pragma unroll
                     for (int q = 0; q < 8; ++q) v[q] = value(h, j, q, sx[j] * sw[h][q]);
-                    if (i < rows && o < p.out) store_eight<YT>(p.y, (begin + m0 + i) * p.out + o, v, p.out - o);
+                    if (i < rows && o < p.out) store_some<YT>(p.y, (begin + m0 + i) * p.out + o, v, p.out - o);
                 }
                 __builtin_amdgcn_sched_barrier(0);  // (else all of the tile's values are wanted at once)
             }

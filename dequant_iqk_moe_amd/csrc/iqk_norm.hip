@@ -16,6 +16,10 @@
 //
 // Bound: bytes.  A team (a wave, or a workgroup) holds a row in registers as it
 // lies in memory; sums go through float32, lanes and waves in a fixed order.
+// Chunks of eight values are read where every row begins at a multiple of 16 bytes,
+// single values elsewhere: either way a chunk is in its row or past it, where a
+// buffer's loads give zeros and its stores are dropped, so no path has a branch for
+// the end of a row.
 #include <algorithm>
 
 #include "iqk_block.h"
@@ -71,94 +75,155 @@ __device__ __forceinline__ float inv_rms(float squares, const NormParams& p) {
     return 1.f / sqrtf(squares / (float)p.n + p.eps);
 }
 
-// The gate's values at chunk c of row t (1 without a gate).
-template <int V>
-__device__ __forceinline__ void gate_at(const NormParams& p, int64_t t, int c, int left, float (&g)[V]) {
-    if (p.g_kind == IQK_GATE_NONE || left <= 0) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) g[j] = 1.f;
-    } else if (p.g_kind == IQK_GATE_TOKEN) {
-        float one[4];
-        load_any(p.g, p.g_dtype, t, 1, one);
-#pragma unroll
-        for (int j = 0; j < V; ++j) g[j] = one[0];
-    } else {
-        load_any(p.g, p.g_dtype, p.g_kind == IQK_GATE_ELEMENT ? t * p.n + c : c, left, g);
-    }
+// V values of a row as they lie in memory.
+template <int DT, int V>
+struct Piece {
+    static constexpr int kWords = V == 1 ? 1 : (DT == IQK_F32 ? V : V / 2);
+    uint32_t w[kWords];
+};
+template <int DT>
+constexpr int kSizeOf = DT == IQK_F32 ? 4 : 2;
+
+__device__ __forceinline__ int size_of(int dtype) { return dtype == IQK_F32 ? 4 : 2; }
+
+// Row t (the same in every lane) of n values
+__device__ __forceinline__ Rsrc row_of(const void* p, int64_t t, int n, int size) {
+    return make_rsrc((const char*)p + t * n * size, p ? (uint32_t)(n * size) : 0u);
 }
 
-// r's values from x's and y's, and u's
-template <int V>
-__device__ __forceinline__ void mix(const NormParams& p, const float (&x)[V], const float (&y)[V], const float (&wp)[V], float s,
-                                    const float (&g)[V], float (&u)[V], float (&r)[V]) {
+// the V values from value c on
+template <int DT, int V>
+__device__ __forceinline__ Piece<DT, V> load_piece(Rsrc r, int c) {
+    Piece<DT, V> p;
+    const uint32_t off = (uint32_t)c * kSizeOf<DT>;
+    if constexpr (V == 1) {
+        p.w[0] = DT == IQK_F32 ? ld32(r, off) : ld16(r, off);
+    } else {
+#pragma unroll
+        for (int i = 0; i < Piece<DT, V>::kWords; i += 4) {
+            const uint4 u = ld128(r, off + 4 * i);
+            p.w[i] = u.x, p.w[i + 1] = u.y, p.w[i + 2] = u.z, p.w[i + 3] = u.w;
+        }
+    }
+    return p;
+}
+template <int DT, int V>
+__device__ __forceinline__ void widen_piece(const Piece<DT, V>& p, float (&v)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        u[j] = p.wp ? y[j] * s * wp[j] : y[j];
-        r[j] = __builtin_fmaf(p.beta * g[j], u[j], p.alpha * x[j]);
+        if constexpr (DT == IQK_F32) v[j] = __uint_as_float(p.w[j]);
+        else if constexpr (DT == IQK_BF16) v[j] = __uint_as_float(j % 2 ? p.w[j / 2] & 0xFFFF0000u : p.w[j / 2] << 16);
+        else v[j] = half_to_float(j % 2 ? p.w[j / 2] >> 16 : p.w[j / 2] & 0xFFFFu);
     }
+}
+template <int DT, int V>
+__device__ __forceinline__ void store_piece(Rsrc r, int c, const float (&v)[V]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t off = (uint32_t)c * kSizeOf<DT>;
+    if constexpr (V == 1) {
+        if constexpr (DT == IQK_F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), r, off, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack2<DT>(v[0], v[0]), r, off, 0, 0);
+    } else if constexpr (DT == IQK_F32) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])},
+                                                   r, off + 4 * i, 0, 0);
+    } else {
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])},
+                                               r, off, 0, 0);
+    }
+}
+// The same for a type known at run time only (the same in every lane).
+template <int V>
+__device__ __forceinline__ void load_typed(Rsrc r, int dtype, int c, float (&v)[V]) {
+    if (dtype == IQK_F32) widen_piece(load_piece<IQK_F32, V>(r, c), v);
+    else if (dtype == IQK_BF16) widen_piece(load_piece<IQK_BF16, V>(r, c), v);
+    else widen_piece(load_piece<IQK_F16, V>(r, c), v);
+}
+template <int V>
+__device__ __forceinline__ void store_typed(Rsrc r, int dtype, int c, const float (&v)[V]) {
+    if (dtype == IQK_F32) store_piece<IQK_F32>(r, c, v);
+    else if (dtype == IQK_BF16) store_piece<IQK_BF16>(r, c, v);
+    else store_piece<IQK_F16>(r, c, v);
+}
+// The value of a gate of tokens at row t
+__device__ __forceinline__ float token_gate(const NormParams& p, int64_t t) {
+    float one[1];
+    load_typed(row_of(p.g, t, 1, size_of(p.g_dtype)), p.g_dtype, 0, one);
+    return one[0];
 }
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 
-template <int XT, int YT, int TEAM, int NV>
+template <int XT, int YT, int TEAM, int V, int NV>
 __global__ __launch_bounds__(Team<TEAM>::kThreads) void norm_kernel(NormParams p) {
     using Tm = Team<TEAM>;
     __shared__ float lds[2 * Tm::kWaves][2];
     const int tid = threadIdx.x % TEAM;
-    const int64_t t = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * Tm::kTeams + threadIdx.x / TEAM;
+    const int64_t t = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * Tm::kTeams + __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
     if (t >= p.T) return;  // (whole teams: no barrier misses a wave)
-    Raw<XT> x[NV];
-    Raw<YT> y[NV];
-    auto chunk = [&](int i) { return (i * TEAM + tid) * 8; };
+    Piece<XT, V> x[NV];
+    Piece<YT, V> y[NV];
+    auto chunk = [&](int i) { return (i * TEAM + tid) * V; };
+    const Rsrc xr = row_of(p.x, t, p.n, kSizeOf<XT>), yr = row_of(p.y, t, p.n, kSizeOf<YT>);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = chunk(i);
-        if (p.y) y[i] = load_raw<YT>(p.y, t * p.n + c, p.n - c);
-        x[i] = load_raw<XT>(p.x, t * p.n + c, p.n - c);
-    }
+    for (int i = 0; i < NV; ++i) y[i] = load_piece<YT, V>(yr, chunk(i));  // (zeros without y)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = load_piece<XT, V>(xr, chunk(i));
     float s[1] = {0.f};
     if (p.wp) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float v[8];
-            widen_raw(y[i], v);
+            float v[V];
+            widen_piece(y[i], v);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) s[0] = __builtin_fmaf(v[j], v[j], s[0]);
+            for (int j = 0; j < V; ++j) s[0] = __builtin_fmaf(v[j], v[j], s[0]);
         }
         team_sum<TEAM, 1>(s, lds, 0);
         s[0] = inv_rms(s[0], p);
     }
-    float r[NV][8], q[1] = {0.f};
+    const Rsrc wpr = row_of(p.wp, 0, p.n, size_of(p.w_dtype)), wnr = row_of(p.wn, 0, p.n, size_of(p.w_dtype));
+    const Rsrc gr = row_of(p.g, p.g_kind == IQK_GATE_ELEMENT ? t : 0, p.n, size_of(p.g_dtype));
+    const Rsrc rr = row_of(p.r, t, p.n, kSizeOf<XT>), hr = row_of(p.h, t, p.n, kSizeOf<XT>);
+    const float beta = p.g_kind == IQK_GATE_TOKEN ? p.beta * token_gate(p, t) : p.beta;
+    float r[NV][V], q[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = chunk(i), left = p.n - c;
-        widen_raw(x[i], r[i]);
+        const int c = chunk(i);
+        widen_piece(x[i], r[i]);
         if (p.y) {
-            float g[8], wp[8], u[8], yv[8], xv[8];
-            gate_at(p, t, c, left, g);
-            if (p.wp) load_any(p.wp, p.w_dtype, c, left, wp);
-            widen_raw(y[i], yv);
+            float u[V], w[V];
+            widen_piece(y[i], u);
+            if (p.wp) {
+                load_typed(wpr, p.w_dtype, c, w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) xv[j] = r[i][j];
-            mix(p, xv, yv, wp, s[0], g, u, r[i]);
-            store_some<XT>(p.r, t * p.n + c, r[i], left);
+                for (int j = 0; j < V; ++j) u[j] = u[j] * s[0] * w[j];
+            }
+            if (p.g_kind == IQK_GATE_CHANNEL || p.g_kind == IQK_GATE_ELEMENT) {
+                load_typed(gr, p.g_dtype, c, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) r[i][j] = __builtin_fmaf(beta * w[j], u[j], p.alpha * r[i][j]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) r[i][j] = __builtin_fmaf(beta, u[j], p.alpha * r[i][j]);
+            }
+            store_piece<XT>(rr, c, r[i]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[0] = __builtin_fmaf(r[i][j], r[i][j], q[0]);
+        for (int j = 0; j < V; ++j) q[0] = __builtin_fmaf(r[i][j], r[i][j], q[0]);
     }
     if (!p.h) return;
     team_sum<TEAM, 1>(q, lds, 1);
     q[0] = inv_rms(q[0], p);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int c = chunk(i), left = p.n - c;
-        float w[8];
-        load_any(p.wn, p.w_dtype, c, left, w);
+        float w[V];
+        load_typed(wnr, p.w_dtype, chunk(i), w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] *= r[i][j] * q[0];
-        store_some<XT>(p.h, t * p.n + c, w, left);
+        for (int j = 0; j < V; ++j) w[j] *= r[i][j] * q[0];
+        store_piece<XT>(hr, chunk(i), w);
     }
 }
 
@@ -166,15 +231,8 @@ __global__ __launch_bounds__(Team<TEAM>::kThreads) void norm_kernel(NormParams p
 // gradient
 // ---------------------------------------------------------------------------
 
-template <int XT, int YT, int NV>
-struct GradRow {
-    Raw<XT> x[NV], dr[NV], dh[NV];
-    Raw<YT> y[NV];
-};
-
-// What the compiler knows of a row's values ends here: it would keep every
-// pass's float32 values for the next instead of widening them again (200
-// registers where 128 do).
+// What the compiler knows of a row's values ends here: it would keep a pass's
+// float32 values for the next one instead of widening them again.
 template <class R>
 __device__ __forceinline__ void forget(R& r) {
 #pragma unroll
@@ -182,196 +240,175 @@ __device__ __forceinline__ void forget(R& r) {
 }
 
 // A team takes every teams-th row, so its threads meet the same columns in each:
-// its parts of the parameters' gradients stay in registers, and another launch
-// joins the teams' parts in their order.  So do the parameters' values.
-// HOLD: the row stays in registers; else each pass reads it again, from the L2.
-// AHEAD: the next row is asked for while this one is taken.
-template <int XT, int YT, int TEAM, int NV, bool HOLD, bool AHEAD>
-__global__ __launch_bounds__(Team<TEAM>::kThreads) void norm_grad_kernel(NormParams p) {
+// the parameters' values and its parts of their gradients stay in registers, and
+// another launch joins the teams' parts in their order.  What is not there is taken
+// as what changes nothing (weights and gates one, y, dr and dh zero), so that every
+// form is one straight path.
+template <int XT, int YT, int TEAM, int V, int NV>
+__global__ __launch_bounds__(Team<TEAM>::kThreads) __attribute__((amdgpu_waves_per_eu(V == 8 && NV == 1 && YT != IQK_F32 ? 4 : 2))) void
+norm_grad_kernel(NormParams p) {
     using Tm = Team<TEAM>;
     __shared__ float lds[6 * Tm::kWaves][2];  // (a row's sums and the next one's take turns)
     const int tid = threadIdx.x % TEAM;
-    const int64_t team = (int64_t)blockIdx.x * Tm::kTeams + threadIdx.x / TEAM, teams = (int64_t)gridDim.x * Tm::kTeams;
-    const int64_t n = p.n;
-    auto chunk = [&](int i) { return (i * TEAM + tid) * 8; };
-    float wp[NV][8], wn[NV][8], gc[NV][8];  // (ones where there are none)
-    float awp[NV][8], awn[NV][8], agc[NV][8];  // sums of their gradients
-    auto params = [&](int i) {
-        const int c = chunk(i), left = p.n - c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wp[i][j] = wn[i][j] = gc[i][j] = 1.f;
-        if (p.wp) load_any(p.wp, p.w_dtype, c, left, wp[i]);
-        if (p.wn) load_any(p.wn, p.w_dtype, c, left, wn[i]);
-        if (p.g_kind == IQK_GATE_CHANNEL) load_any(p.g, p.g_dtype, c, left, gc[i]);
+    const int64_t team = (int64_t)blockIdx.x * Tm::kTeams + __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+    const int64_t teams = (int64_t)gridDim.x * Tm::kTeams;
+    auto chunk = [&](int i) { return (i * TEAM + tid) * V; };
+    struct Params {
+        float wp[V], wn[V], bg[V];  // bg: of beta and the gate what all rows share
     };
+    auto load_params = [&](int i) {
+        Params a;
+#pragma unroll
+        for (int j = 0; j < V; ++j) a.wp[j] = a.wn[j] = a.bg[j] = 1.f;
+        if (p.wp) load_typed(row_of(p.wp, 0, p.n, size_of(p.w_dtype)), p.w_dtype, chunk(i), a.wp);
+        if (p.wn) load_typed(row_of(p.wn, 0, p.n, size_of(p.w_dtype)), p.w_dtype, chunk(i), a.wn);
+        if (p.g_kind == IQK_GATE_CHANNEL) load_typed(row_of(p.g, 0, p.n, size_of(p.g_dtype)), p.g_dtype, chunk(i), a.bg);
+#pragma unroll
+        for (int j = 0; j < V; ++j) a.bg[j] *= p.g_kind == IQK_GATE_ELEMENT ? 1.f : p.beta;
+        return a;
+    };
+    // (sixteen single values leave no registers for them)
+    constexpr bool KEEP = V > 1 || NV <= 8;
+    Params kept[KEEP ? NV : 1];
+    auto params = [&](int i) { return KEEP ? kept[KEEP ? i : 0] : load_params(i); };
+    // Sums over the rows: of what is wn's gradient, and of b D y s, b being what is a row's own of beta and the gate,
+    // which is d_wp but for bg, and dg of a gate of channels (b = 1) but for beta and wp.
+    float awp[NV][V], awn[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        if (KEEP) kept[KEEP ? i : 0] = load_params(i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) awp[i][j] = awn[i][j] = agc[i][j] = 0.f;
-        params(i);
-    }
-    using Row = GradRow<XT, YT, NV>;
-    auto load = [&](Row& a, int64_t t, int i) {
-        const int c = chunk(i), left = p.n - c;
-        const int64_t at = t * n + c;
-        a.x[i] = load_raw<XT>(p.x, at, left);
-        if (p.y) a.y[i] = load_raw<YT>(p.y, at, left);
-        if (p.dr) a.dr[i] = load_raw<XT>(p.dr, at, left);
-        if (p.dh) a.dh[i] = load_raw<XT>(p.dh, at, left);
-    };
-    Row cur, ahead;
-    for (Row* a : {&cur, &ahead}) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            for (auto& w : a->y[i].w) w = 0;
-            for (auto& w : a->dr[i].w) w = 0;
-            for (auto& w : a->dh[i].w) w = 0;
-        }
-    }
-    if (AHEAD && team < p.T) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) load(ahead, team, i);
+        for (int j = 0; j < V; ++j) awp[i][j] = awn[i][j] = 0.f;
     }
     int odd = 0;
     for (int64_t t = team; t < p.T; t += teams, odd = 3 - odd) {
-        if constexpr (AHEAD) {
-            cur = ahead;
-            if (t + teams < p.T) {
+        struct Row {
+            Piece<XT, V> x[NV], dr[NV], dh[NV];
+            Piece<YT, V> y[NV];
+        } row;
+        const Rsrc xr = row_of(p.x, t, p.n, kSizeOf<XT>), yr = row_of(p.y, t, p.n, kSizeOf<YT>);
+        const Rsrc drr = row_of(p.dr, t, p.n, kSizeOf<XT>), dhr = row_of(p.dh, t, p.n, kSizeOf<XT>);
 #pragma unroll
-                for (int i = 0; i < NV; ++i) load(ahead, t + teams, i);
-            }
-        } else if constexpr (HOLD) {
+        for (int i = 0; i < NV; ++i) row.y[i] = load_piece<YT, V>(yr, chunk(i));  // (zeros without them)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) load(cur, t, i);
-        }
-        float gt[4] = {1.f, 0.f, 0.f, 0.f};
-        if (p.g_kind == IQK_GATE_TOKEN) load_any(p.g, p.g_dtype, t, 1, gt);
-        // a chunk's gate and u, and r, widened anew in every pass
-        auto gate = [&](int i, float (&g)[8]) {
+        for (int i = 0; i < NV; ++i) row.x[i] = load_piece<XT, V>(xr, chunk(i));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) row.dh[i] = load_piece<XT, V>(dhr, chunk(i));
+#pragma unroll
+        for (int i = 0; i < NV; ++i) row.dr[i] = load_piece<XT, V>(drr, chunk(i));
+        const float gt = p.g_kind == IQK_GATE_TOKEN ? token_gate(p, t) : 1.f;
+        const Rsrc gr = row_of(p.g, t, p.n, size_of(p.g_dtype)), dgr = row_of(p.dg, t, p.n, size_of(p.g_dtype));
+        // b at a chunk
+        auto gate = [&](int i, float (&b)[V]) {
             if (p.g_kind == IQK_GATE_ELEMENT) {
-                load_any(p.g, p.g_dtype, t * n + chunk(i), p.n - chunk(i), g);
+                load_typed(gr, p.g_dtype, chunk(i), b);
+#pragma unroll
+                for (int j = 0; j < V; ++j) b[j] *= p.beta;
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = gc[i][j] * gt[0];
-            }
-        };
-        auto open = [&](int i, float s, const float (&g)[8], float (&u)[8], float (&r)[8]) {
-            float y[8];
-            forget(cur.y[i]);
-            forget(cur.x[i]);
-            widen_raw(cur.y[i], y);
-            widen_raw(cur.x[i], r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                u[j] = p.wp ? y[j] * s * wp[i][j] : y[j];
-                r[j] = __builtin_fmaf(p.beta * g[j], u[j], p.alpha * r[j]);
+                for (int j = 0; j < V; ++j) b[j] = gt;
             }
         };
         float s[1] = {0.f};
         if (p.wp) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if constexpr (!HOLD) load(cur, t, i);
-                float v[8];
-                widen_raw(cur.y[i], v);
+                float v[V];
+                widen_piece(row.y[i], v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s[0] = __builtin_fmaf(v[j], v[j], s[0]);
+                for (int j = 0; j < V; ++j) s[0] = __builtin_fmaf(v[j], v[j], s[0]);
             }
             team_sum<TEAM, 1>(s, lds, odd);
             s[0] = inv_rms(s[0], p);
+        } else {
+            s[0] = 1.f;
         }
-        float two[2] = {0.f, 0.f};  // r^2, wn dh r
-        if (p.dh) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if constexpr (!HOLD) load(cur, t, i);
-                float g[8], u[8], r[8], dh[8];
-                gate(i, g);
-                open(i, s[0], g, u, r);
-                widen_raw(cur.dh[i], dh);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    two[0] = __builtin_fmaf(r[j], r[j], two[0]);
-                    two[1] = __builtin_fmaf(r[j], wn[i][j] * dh[j], two[1]);
-                }
-            }
-            team_sum<TEAM, 2>(two, lds, odd + 1);
-        }
-        // (without dh its values are zero, and so is back)
-        const float q = inv_rms(two[0], p), back = q * q * q / (float)p.n * two[1];
-        // D, and beta D
-        auto grown = [&](int i, const float (&r)[8], float (&d)[8], bool first) {
-            float dr[8], dh[8];
-            forget(cur.dr[i]);
-            forget(cur.dh[i]);
-            widen_raw(cur.dr[i], dr);
-            widen_raw(cur.dh[i], dh);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] = dr[j] + (q * (wn[i][j] * dh[j]) - back * r[j]);
-                if (first) awn[i][j] = __builtin_fmaf(dh[j], r[j] * q, awn[i][j]);
-            }
-        };
-        float end[2] = {0.f, 0.f};  // v y, beta D u
+        float r[NV][V], two[2] = {0.f, 0.f};  // r^2, wn dh r
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int c = chunk(i), left = p.n - c;
-            if constexpr (!HOLD) load(cur, t, i);
-            float g[8], u[8], r[8], d[8];
-            gate(i, g);
-            open(i, s[0], g, u, r);
-            grown(i, r, d, true);
-            if (p.dx) {
+            float b[V], y[V], dh[V];
+            const Params a = params(i);
+            gate(i, b);
+            forget(row.y[i]);
+            widen_piece(row.y[i], y);
+            widen_piece(row.x[i], r[i]);
+            widen_piece(row.dh[i], dh);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = p.alpha * d[j];
-                store_some<XT>(p.dx, t * n + c, r, left);
+            for (int j = 0; j < V; ++j) {
+                r[i][j] = __builtin_fmaf(a.bg[j] * b[j], y[j] * s[0] * a.wp[j], p.alpha * r[i][j]);
+                two[0] = __builtin_fmaf(r[i][j], r[i][j], two[0]);
+                two[1] = __builtin_fmaf(r[i][j], a.wn[j] * dh[j], two[1]);
             }
-            if (!p.y) continue;
-            float y[8];
-            widen_raw(cur.y[i], y);
+        }
+        if (p.dh) team_sum<TEAM, 2>(two, lds, odd + 1);
+        // (without dh its values are zero, and so is back)
+        const float q = inv_rms(two[0], p), back = p.dh ? q * q * q / (float)p.n * two[1] : 0.f;
+        const Rsrc dxr = row_of(p.dx, t, p.n, kSizeOf<XT>);
+        float end[2] = {0.f, 0.f};  // v y, D u
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] *= p.beta;
-                r[j] = d[j] * u[j];
-                end[1] += r[j];
-                agc[i][j] += r[j];
-                const float v = d[j] * g[j];
-                awp[i][j] = __builtin_fmaf(v, y[j] * s[0], awp[i][j]);
-                end[0] = __builtin_fmaf(v * wp[i][j], y[j], end[0]);
+        for (int i = 0; i < NV; ++i) {
+            float b[V], y[V], dr[V], dh[V], d[V];
+            const Params a = params(i);
+            gate(i, b);
+            forget(row.y[i]);
+            forget(row.dh[i]);
+            widen_piece(row.y[i], y);
+            widen_piece(row.dr[i], dr);
+            widen_piece(row.dh[i], dh);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                d[j] = dr[j] + (q * (a.wn[j] * dh[j]) - back * r[i][j]);
+                awn[i][j] = __builtin_fmaf(dh[j], r[i][j] * q, awn[i][j]);
+                dr[j] = p.alpha * d[j];
             }
-            if (p.dg && p.g_kind == IQK_GATE_ELEMENT && left > 0) store_any(p.dg, p.g_dtype, t * n + c, r, left);
+            store_piece<XT>(dxr, chunk(i), dr);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float ys = y[j] * s[0], du = d[j] * (ys * a.wp[j]), bd = b[j] * d[j];
+                end[1] += du;
+                awp[i][j] = __builtin_fmaf(bd, ys, awp[i][j]);
+                r[i][j] = bd * a.bg[j] * a.wp[j];  // (v of the formula, where r was)
+                end[0] = __builtin_fmaf(r[i][j], y[j], end[0]);
+                d[j] = p.beta * du;
+            }
+            if (p.dg && p.g_kind == IQK_GATE_ELEMENT) store_typed(dgr, p.g_dtype, chunk(i), d);
         }
         const bool token = p.dg && p.g_kind == IQK_GATE_TOKEN;
         if (p.wp || token) team_sum<TEAM, 2>(end, lds, odd + 2);
         if (token && tid == 0) {
-            const float one[4] = {end[1], 0.f, 0.f, 0.f};
-            store_any(p.dg, p.g_dtype, t, one, 1);
+            const float one[1] = {p.beta * end[1]};
+            store_typed(row_of(p.dg, t, 1, size_of(p.g_dtype)), p.g_dtype, 0, one);
         }
         if (!p.dy) continue;
-        const float off = p.wp ? s[0] * s[0] * s[0] / (float)p.n * end[0] : 0.f, by = p.wp ? s[0] : 1.f;
+        const float off = p.wp ? s[0] * s[0] * s[0] / (float)p.n * end[0] : 0.f;
+        const Rsrc dyr = row_of(p.dy, t, p.n, kSizeOf<YT>);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if constexpr (!HOLD) load(cur, t, i);
-            float g[8], u[8], r[8], d[8], y[8];
-            gate(i, g);
-            open(i, s[0], g, u, r);
-            grown(i, r, d, false);
-            widen_raw(cur.y[i], y);
+            float y[V];
+            forget(row.y[i]);
+            widen_piece(row.y[i], y);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) d[j] = by * (p.beta * d[j] * g[j] * wp[i][j]) - off * y[j];
-            store_some<YT>(p.dy, t * n + chunk(i), d, p.n - chunk(i));
+            for (int j = 0; j < V; ++j) y[j] = s[0] * r[i][j] - off * y[j];
+            store_piece<YT>(dyr, chunk(i), y);
         }
     }
-    float* sums = p.sums + team * p.columns * n;
-    auto put = [&](int has, const float (&a)[NV][8]) {
+    float* sums = p.sums + team * p.columns * p.n;
+    auto put = [&](int has, auto value) {
         if (!has) return;
+        const Rsrc to = row_of(sums, 0, p.n, 4);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) store_some<IQK_F32>(sums, chunk(i), a[i], p.n - chunk(i));
-        sums += n;
+        for (int i = 0; i < NV; ++i) {
+            const Params a = params(i);
+            float o[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) o[j] = value(a, i, j);
+            store_piece<IQK_F32>(to, chunk(i), o);
+        }
+        sums += p.n;
     };
-    put(p.has_dwp, awp);
-    put(p.has_dwn, awn);
-    put(p.has_dgc, agc);
+    put(p.has_dwp, [&](const Params& a, int i, int j) { return a.bg[j] * awp[i][j]; });
+    put(p.has_dwn, [&](const Params&, int i, int j) { return awn[i][j]; });
+    put(p.has_dgc, [&](const Params& a, int i, int j) { return p.beta * a.wp[j] * awp[i][j]; });
 }
 
 // Sums of the teams' parts, column by column: 64 columns by 16 runs of teams,
@@ -439,32 +476,48 @@ void by_types(const iqk_block& b, F f) {
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// f(threads of a team, chunks of a thread) for rows of n values
+// f(threads of a team, values of a chunk, chunks of a thread) for rows of n values
 template <class F>
-void by_row(int64_t n, F f) {
-    if (n <= 512) f(Int<64>{}, Int<1>{});
-    else if (n <= 1024) f(Int<64>{}, Int<2>{});
-    else if (n <= 2048) f(Int<256>{}, Int<1>{});
-    else if (n <= 4096) f(Int<256>{}, Int<2>{});
-    else f(Int<512>{}, Int<2>{});
+void by_row(int64_t n, bool wide, F f) {
+    auto go = [&](auto team, auto values) {
+        constexpr int N = decltype(values)::value;  // of a thread
+        if (wide) f(team, Int<8>{}, Int<N / 8>{});
+        else f(team, Int<1>{}, values);
+    };
+    if (n <= 512) go(Int<64>{}, Int<8>{});
+    else if (n <= 1024) go(Int<64>{}, Int<16>{});
+    else if (n <= 2048) go(Int<256>{}, Int<8>{});
+    else if (n <= 4096) go(Int<256>{}, Int<16>{});
+    else go(Int<512>{}, Int<16>{});
 }
 
-// The gradient, whose parts of the parameters' gradients take three registers a
-// value: eight values of a thread as far as 512 threads reach, which is as many
-// as have the 200 registers that it needs.
+// The gradient, whose parts of the parameters' gradients and their values take six
+// registers a value: eight values of a thread as far as 512 threads reach.
 template <class F>
-void by_grad_row(int64_t n, F f) {
-    if (n <= 512) f(Int<64>{}, Int<1>{});
-    else if (n <= 1024) f(Int<128>{}, Int<1>{});
-    else if (n <= 2048) f(Int<256>{}, Int<1>{});
-    else if (n <= 4096) f(Int<512>{}, Int<1>{});
-    else f(Int<512>{}, Int<2>{});
+void by_grad_row(int64_t n, bool wide, F f) {
+    auto go = [&](auto team, auto values) {
+        constexpr int N = decltype(values)::value;
+        if (wide) f(team, Int<8>{}, Int<N / 8>{});
+        else f(team, Int<1>{}, values);
+    };
+    if (n <= 512) go(Int<64>{}, Int<8>{});
+    else if (n <= 1024) go(Int<128>{}, Int<8>{});
+    else if (n <= 2048) go(Int<256>{}, Int<8>{});
+    else if (n <= 4096) go(Int<512>{}, Int<8>{});
+    else go(Int<512>{}, Int<16>{});
 }
 
 int team_size(int64_t n) {
     int team = 0;
-    by_grad_row(n, [&](auto t, auto) { team = decltype(t)::value; });
+    by_grad_row(n, true, [&](auto t, auto, auto) { team = decltype(t)::value; });
     return team;
+}
+
+// Whether chunks of eight values lie at multiples of 16 bytes in all of these
+bool wide_rows(int64_t n, std::initializer_list<const void*> all) {
+    bool wide = n % 8 == 0;
+    for (const void* p : all) wide = wide && (uintptr_t)p % 16 == 0;
+    return wide;
 }
 
 // Teams of the gradient: the 512 threads that a CU holds of it.
@@ -489,10 +542,10 @@ hipError_t launch_norm(const iqk_block& b, void* r, void* h, hipStream_t s) {
     p.r = r;
     p.h = h;
     by_types(b, [&](auto xt, auto yt) {
-        by_row(b.n, [&](auto team, auto nv) {
+        by_row(b.n, wide_rows(b.n, {b.x, b.y, b.post_weight, b.gate, b.next_weight, r, h}), [&](auto team, auto v, auto nv) {
             constexpr int TEAM = decltype(team)::value;
             using Tm = Team<TEAM>;
-            hipLaunchKernelGGL((norm_kernel<decltype(xt)::value, decltype(yt)::value, TEAM, decltype(nv)::value>),
+            hipLaunchKernelGGL((norm_kernel<decltype(xt)::value, decltype(yt)::value, TEAM, decltype(v)::value, decltype(nv)::value>),
                                grid_of((p.T + Tm::kTeams - 1) / Tm::kTeams), dim3(Tm::kThreads), 0, s, p);
         });
     });
@@ -513,12 +566,11 @@ hipError_t launch_norm_grad(const iqk_block& b, const NormGradOut& o, float* sum
     p.columns = p.has_dwp + p.has_dwn + p.has_dgc;
     const int64_t teams = grad_teams(p.T, p.n);
     by_types(b, [&](auto xt, auto yt) {
-        by_grad_row(b.n, [&](auto team, auto nv) {
-            constexpr int TEAM = decltype(team)::value, XT = decltype(xt)::value, YT = decltype(yt)::value;
-            constexpr int NV = decltype(nv)::value;
+        const bool wide = wide_rows(b.n, {b.x, b.y, b.post_weight, b.gate, b.next_weight, o.dr, o.dh, o.dx, o.dy, o.d_gate, sums});
+        by_grad_row(b.n, wide, [&](auto team, auto v, auto nv) {
+            constexpr int TEAM = decltype(team)::value;
             using Tm = Team<TEAM>;
-            constexpr bool HOLD = NV == 1, AHEAD = HOLD && XT != IQK_F32;
-            hipLaunchKernelGGL((norm_grad_kernel<XT, YT, TEAM, NV, HOLD, AHEAD>),
+            hipLaunchKernelGGL((norm_grad_kernel<decltype(xt)::value, decltype(yt)::value, TEAM, decltype(v)::value, decltype(nv)::value>),
                                dim3((unsigned)(teams / Tm::kTeams)), dim3(Tm::kThreads), 0, s, p);
         });
     });

@@ -51,25 +51,34 @@ __device__ __forceinline__ void load_any(const void* p, int dtype, int64_t i, in
     else widen_raw(load_raw<IQK_F16, V>(p, i, left), v);
 }
 
-// min(left, V) values of v to y + i
+// Two values in 16 bits, rounded to nearest even (the hardware's conversions).
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if constexpr (DT == IQK_F16) return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// min(left, V) values of v to y + i (any address)
 template <int DT, int V>
 __device__ __forceinline__ void store_some(void* y, int64_t i, const float (&v)[V], int left) {
-    if (left <= 0) return;
-    if constexpr (V == 8) {
-        store8<DT>(y, i, v, left);
-    } else if (left >= V) {
-        if constexpr (DT == IQK_F32) {
-            __builtin_memcpy((float*)y + i, v, 4 * V);
-        } else {
-            uint16_t w[V];
+    Raw<DT, V> r;
+    if constexpr (DT == IQK_F32) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) store_y<DT>(w, j, v[j]);
-            __builtin_memcpy((uint16_t*)y + i, w, 2 * V);
-        }
+        for (int j = 0; j < V; ++j) r.w[j] = __float_as_uint(v[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j < left) store_y<DT>(y, i + j, v[j]);
+        for (int j = 0; j < V / 2; ++j) r.w[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
+    }
+    if (left >= V) {
+        __builtin_memcpy((char*)y + i * (DT == IQK_F32 ? 4 : 2), r.w, sizeof(r.w));
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (j >= left) continue;
+        if constexpr (DT == IQK_F32) ((uint32_t*)y)[i + j] = r.w[j];
+        else ((uint16_t*)y)[i + j] = (uint16_t)(r.w[j / 2] >> (j % 2 * 16));
     }
 }
 template <int V>
