@@ -523,7 +523,7 @@ bool wide_rows(int64_t n, std::initializer_list<const void*> all) {
 // Teams of the gradient: the 512 threads that a CU holds of it.
 int64_t grad_teams(int64_t T, int64_t n) {
     const int team = team_size(n), per = team == 64 ? 4 : 1;
-    const int64_t most = 256 * 512 / team;
+    const int64_t most = 256 * (n <= 4096 ? 1024 : 512) / team;
     return (std::min(std::max<int64_t>(T, 1), most) + per - 1) / per * per;
 }
 

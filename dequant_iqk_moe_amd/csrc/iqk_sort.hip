@@ -242,107 +242,137 @@ struct UnsortParams {
     float* d_w;
 };
 
+// Rows of at least eight values are taken in chunks of eight, the last of which
+// ends with the row: what it shares with the one before is made twice, with the same
+// bits.  So no load has a branch for the row's end.  Shorter rows are one chunk.
+struct Chunk {
+    int64_t c;       // its first value
+    int left, twice;  // its values, and how many of them are the one before's too
+};
+template <bool LONG>
+__device__ __forceinline__ Chunk chunk_at(int64_t c, int64_t n) {
+    if constexpr (LONG) {
+        const int64_t at = min(c, n - 8);
+        return {at, 8, (int)(c - at)};
+    }
+    return {c, (int)(n - c), 0};
+}
+
+// kAhead of a token's slots: their places and weights, read before any row.
+constexpr int kAhead = kKeys;
+struct Slots {
+    int32_t row[kAhead];
+    float w[kAhead];
+};
+__device__ __forceinline__ Slots load_slots(const UnsortParams& p, int64_t t, int j0) {
+    Slots s;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        const int64_t at = t * p.k + min(j0 + j, p.k - 1);
+        s.row[j] = p.place[at];
+        s.w[j] = p.w ? p.w[at] : 1.f;
+    }
+    return s;
+}
+__device__ __forceinline__ bool known(const UnsortParams& p, int32_t row) { return (uint32_t)row < (uint64_t)p.P; }
 // A row of ys to read for a pair: its own, or row 0, which is then not used.
-__device__ __forceinline__ int64_t known(const UnsortParams& p, int32_t row) { return (uint32_t)row < (uint64_t)p.P ? row : 0; }
+__device__ __forceinline__ int64_t row_to_read(const UnsortParams& p, int32_t row) { return known(p, row) ? row : 0; }
 
 // Slots are added in their order, each product rounded by itself, as iqk_combine
 // does: the two agree bit for bit.
-template <int ST, int YT>
+template <int ST, int YT, bool LONG>
 __global__ __launch_bounds__(kThreads) void unsort_kernel(UnsortParams p) {
-    const int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 8;
-    if (c >= p.n) return;
-    const int left = (int)min(p.n - c, (int64_t)8);
-    constexpr int kAhead = 8;  // rows asked for together
+    const int64_t c0 = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 8;
+    if (c0 >= p.n) return;
+    const Chunk c = chunk_at<LONG>(c0, p.n);
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int32_t* place = p.place + t * p.k;
         float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+            const Slots s = load_slots(p, t, j0);
             Raw<ST> r[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (j0 + j < p.k) r[j] = load_raw<ST>(p.ys, known(p, place[j0 + j]) * p.n + c, left);
+                if (j0 + j < p.k) r[j] = load_raw<ST>(p.ys, row_to_read(p, s.row[j]) * p.n + c.c, LONG ? 8 : c.left);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 if (j0 + j >= p.k) continue;
                 float v[8];
                 widen_raw(r[j], v);
-                const float w = p.w ? p.w[t * p.k + j0 + j] : 1.f;
-                const bool there = (uint32_t)place[j0 + j] < (uint64_t)p.P;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float m = __fmul_rn(w, there ? v[i] : 0.f);
+                    const float m = __fmul_rn(s.w[j], known(p, s.row[j]) ? v[i] : 0.f);
                     acc[i] = j0 + j == 0 ? m : __fadd_rn(acc[i], m);
                 }
             }
         }
-        store_some<YT>(p.y, t * p.n + c, acc, left);
+        store_some<YT>(p.y, t * p.n + c.c, acc, LONG ? 8 : c.left);
     }
 }
 
 // A workgroup owns a token: dy's chunks are read once for all of its pairs (of
-// up to kKeys; further ones read them again), whose dot products are summed over
+// up to kAhead; further ones read them again), whose dot products are summed over
 // lanes and waves in a fixed order.
-template <int ST, int YT>
+template <int ST, int YT, bool LONG>
 __global__ __launch_bounds__(kThreads) void unsort_grad_kernel(UnsortParams p) {
-    __shared__ float part[kWaves][kKeys];
+    __shared__ float part[kWaves][kAhead];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        for (int j0 = 0; j0 < p.k; j0 += kKeys) {
-            const int32_t* place = p.place + t * p.k + j0;
-            const float* weight = p.w ? p.w + t * p.k + j0 : nullptr;
-            const int slots = min(kKeys, p.k - j0);
-            float dot[kKeys];
+        for (int j0 = 0; j0 < p.k; j0 += kAhead) {
+            const Slots s = load_slots(p, t, j0);
+            const int slots = min(kAhead, p.k - j0);
+            float dot[kAhead];
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) dot[j] = 0.f;
-            for (int64_t c = (int64_t)threadIdx.x * 8; c < p.n; c += kThreads * 8) {
-                const int left = (int)min(p.n - c, (int64_t)8);
+            for (int j = 0; j < kAhead; ++j) dot[j] = 0.f;
+            for (int64_t c0 = (int64_t)threadIdx.x * 8; c0 < p.n; c0 += kThreads * 8) {
+                const Chunk c = chunk_at<LONG>(c0, p.n);
+                const int left = LONG ? 8 : c.left;
                 float d[8];
-                const Raw<YT> dr = load_raw<YT>(p.dy, t * p.n + c, left);
-                Raw<ST> r[kKeys];
+                const Raw<YT> dr = load_raw<YT>(p.dy, t * p.n + c.c, left);
+                Raw<ST> r[kAhead];
                 if (p.d_w) {
 #pragma unroll
-                    for (int j = 0; j < kKeys; ++j)
-                        if (j < slots) r[j] = load_raw<ST>(p.ys, known(p, place[j]) * p.n + c, left);
+                    for (int j = 0; j < kAhead; ++j)
+                        if (j < slots) r[j] = load_raw<ST>(p.ys, row_to_read(p, s.row[j]) * p.n + c.c, left);
                 }
                 widen_raw(dr, d);
                 if (p.d_ys) {
 #pragma unroll
-                    for (int j = 0; j < kKeys; ++j) {
+                    for (int j = 0; j < kAhead; ++j) {
                         if (j >= slots) continue;
-                        const int64_t row = place[j], to = row < 0 ? -1 - row : row;
+                        const int64_t row = s.row[j], to = row < 0 ? -1 - row : row;
                         if (to >= p.P) continue;
-                        const float w = weight ? weight[j] : 1.f;
                         float v[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = row < 0 ? 0.f : w * d[i];
-                        store_some<ST>(p.d_ys, to * p.n + c, v, left);
+                        for (int i = 0; i < 8; ++i) v[i] = row < 0 ? 0.f : s.w[j] * d[i];
+                        store_some<ST>(p.d_ys, to * p.n + c.c, v, left);
                     }
                 }
                 if (p.d_w) {
 #pragma unroll
-                    for (int j = 0; j < kKeys; ++j) {
+                    for (int i = 0; i < 8; ++i) d[i] = LONG && i < c.twice ? 0.f : d[i];
+#pragma unroll
+                    for (int j = 0; j < kAhead; ++j) {
                         if (j >= slots) continue;
                         float v[8];
                         widen_raw(r[j], v);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], v[i], dot[j]);
+                        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(d[i], LONG && i < c.twice ? 0.f : v[i], dot[j]);
                     }
                 }
             }
             if (!p.d_w) continue;
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) dot[j] = wave_sum(dot[j]);
+            for (int j = 0; j < kAhead; ++j) dot[j] = wave_sum(dot[j]);
             if (lane == 0) {
 #pragma unroll
-                for (int j = 0; j < kKeys; ++j) part[wave][j] = dot[j];
+                for (int j = 0; j < kAhead; ++j) part[wave][j] = dot[j];
             }
             __syncthreads();
             if ((int)threadIdx.x < slots) {
                 float v = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWaves; ++w) v += part[w][threadIdx.x];
-                const bool there = (uint32_t)place[threadIdx.x] < (uint64_t)p.P;
-                p.d_w[t * p.k + j0 + threadIdx.x] = there ? v : 0.f;
+                p.d_w[t * p.k + j0 + threadIdx.x] = known(p, p.place[t * p.k + j0 + threadIdx.x]) ? v : 0.f;
             }
             __syncthreads();
         }
@@ -421,7 +451,9 @@ hipError_t launch_unsort(const UnsortLaunch& a, hipStream_t s) {
     const dim3 grid(token_groups(a.T), (unsigned)((a.n + 8 * kThreads - 1) / (8 * kThreads)));
     by_float(a.ys_dtype, [&](auto st) {
         by_float(a.y_dtype, [&](auto yt) {
-            hipLaunchKernelGGL((unsort_kernel<decltype(st)::value, decltype(yt)::value>), grid, dim3(kThreads), 0, s, p);
+            constexpr int ST = decltype(st)::value, YT = decltype(yt)::value;
+            if (p.n >= 8) hipLaunchKernelGGL((unsort_kernel<ST, YT, true>), grid, dim3(kThreads), 0, s, p);
+            else hipLaunchKernelGGL((unsort_kernel<ST, YT, false>), grid, dim3(kThreads), 0, s, p);
         });
     });
     return hipGetLastError();
@@ -441,8 +473,9 @@ hipError_t launch_unsort_grad(const UnsortGradLaunch& a, hipStream_t s) {
     p.d_w = a.d_weights;
     by_float(a.ys_dtype, [&](auto st) {
         by_float(a.dy_dtype, [&](auto yt) {
-            hipLaunchKernelGGL((unsort_grad_kernel<decltype(st)::value, decltype(yt)::value>), dim3(token_groups(a.T)),
-                               dim3(kThreads), 0, s, p);
+            constexpr int ST = decltype(st)::value, YT = decltype(yt)::value;
+            if (p.n >= 8) hipLaunchKernelGGL((unsort_grad_kernel<ST, YT, true>), dim3(token_groups(a.T)), dim3(kThreads), 0, s, p);
+            else hipLaunchKernelGGL((unsort_grad_kernel<ST, YT, false>), dim3(token_groups(a.T)), dim3(kThreads), 0, s, p);
         });
     });
     return hipGetLastError();
