@@ -47,22 +47,28 @@ template <class At>
 __device__ __forceinline__ void copy_row(const SortParams& p, int64_t t, int part, int parts, At at) {
     const int64_t chunks = p.row / 16;
     const uint8_t* src = p.x + t * p.row;
-    for (int64_t c = (int64_t)part * kThreads + threadIdx.x; c < chunks; c += (int64_t)parts * kThreads) {
-        uint4 v;
-        __builtin_memcpy(&v, src + 16 * c, 16);
-        for (int j = 0; j < p.k; ++j) {
-            const int32_t to = at(j);
-            const uint4 z = to < 0 ? make_uint4(0, 0, 0, 0) : v;
-            __builtin_memcpy(p.xs + (int64_t)(to < 0 ? -1 - to : to) * p.row + 16 * c, &z, 16);
+    for (int j0 = 0; j0 < p.k; j0 += kKeys) {
+        int32_t to[kKeys];  // (all before the first store)
+#pragma unroll
+        for (int j = 0; j < kKeys; ++j) to[j] = at(min(j0 + j, p.k - 1));
+        auto row = [&](int j) { return p.xs + (int64_t)(to[j] < 0 ? -1 - to[j] : to[j]) * p.row; };
+        for (int64_t c = (int64_t)part * kThreads + threadIdx.x; c < chunks; c += (int64_t)parts * kThreads) {
+            uint4 v;
+            __builtin_memcpy(&v, src + 16 * c, 16);
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j) {
+                if (j0 + j >= p.k) continue;
+                const uint4 z = to[j] < 0 ? make_uint4(0, 0, 0, 0) : v;
+                __builtin_memcpy(row(j) + 16 * c, &z, 16);
+            }
         }
-    }
-    // what no 16 bytes hold, two at a time
-    const int64_t tail = 16 * chunks + 2 * threadIdx.x;
-    if (part == parts - 1 && tail < p.row) {
-        const uint16_t v = *(const uint16_t*)(src + tail);
-        for (int j = 0; j < p.k; ++j) {
-            const int32_t to = at(j);
-            *(uint16_t*)(p.xs + (int64_t)(to < 0 ? -1 - to : to) * p.row + tail) = to < 0 ? 0 : v;
+        // what no 16 bytes hold, two at a time
+        const int64_t tail = 16 * chunks + 2 * threadIdx.x;
+        if (part == parts - 1 && tail < p.row) {
+            const uint16_t v = *(const uint16_t*)(src + tail);
+#pragma unroll
+            for (int j = 0; j < kKeys; ++j)
+                if (j0 + j < p.k) *(uint16_t*)(row(j) + tail) = to[j] < 0 ? 0 : v;
         }
     }
 }
@@ -164,40 +170,52 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortParams p) {
     for (int64_t q = r0 + lane; q < r1; q += 64) atomicAdd(&next[wave * stride + expert_of(p, q)], 1);
     __syncthreads();
     int before = 0;  // pairs of the experts below those of this pass
-    for (int base = 0; base < stride; base += kThreads) {
-        const int e = base + threadIdx.x;
-        int total = 0, earlier = 0;
-        if (e < stride) {
-#pragma unroll 16
-            for (int s = 0; s < p.slices; ++s) {
-                const int v = p.hist[(int64_t)s * stride + e];
-                total += v;
-                earlier += s < (int)blockIdx.x ? v : 0;
-            }
-        }
-        int upto = total;  // inclusive sum over the wave
+    constexpr int kEach = 2, kTogether = 16;  // experts of a thread, slices asked for at once: a batch costs a memory latency
+    for (int base = 0; base < stride; base += kEach * kThreads) {
+        int total[kEach] = {}, earlier[kEach] = {};
+        for (int s0 = 0; s0 < p.slices; s0 += kTogether) {
+            int v[kTogether][kEach];
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int o = __shfl_up(upto, d);
-            if (lane >= d) upto += o;
+            for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+                for (int u = 0; u < kEach; ++u)
+                    v[i][u] = p.hist[(uint32_t)(min(s0 + i, p.slices - 1) * stride + min(base + u * kThreads + (int)threadIdx.x, p.E))];
+#pragma unroll
+            for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+                for (int u = 0; u < kEach; ++u) {
+                    total[u] += s0 + i < p.slices ? v[i][u] : 0;
+                    earlier[u] += s0 + i < (int)blockIdx.x ? v[i][u] : 0;
+                }
         }
-        if (lane == 63) sums[wave] = upto;
-        __syncthreads();
-        int at = before + upto - total;
-        for (int w = 0; w < kWaves; ++w) {
-            if (w < wave) at += sums[w];
-            before += sums[w];
-        }
-        if (e < stride) {
-            if (blockIdx.x == 0) p.offsets[e] = at;
-            at += earlier;
-            for (int w = 0; w < kWaves; ++w) {
-                const int v = next[w * stride + e];
-                next[w * stride + e] = at;
-                at += v;
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            const int e = base + u * kThreads + threadIdx.x;
+            const int mine = e < stride ? total[u] : 0;
+            int upto = mine;  // inclusive sum over the wave
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const int o = __shfl_up(upto, d);
+                if (lane >= d) upto += o;
             }
+            if (lane == 63) sums[wave] = upto;
+            __syncthreads();
+            int at = before + upto - mine;
+            for (int w = 0; w < kWaves; ++w) {
+                if (w < wave) at += sums[w];
+                before += sums[w];
+            }
+            if (e < stride) {
+                if (blockIdx.x == 0) p.offsets[e] = at;
+                at += earlier[u];
+                for (int w = 0; w < kWaves; ++w) {
+                    const int v = next[w * stride + e];
+                    next[w * stride + e] = at;
+                    at += v;
+                }
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
     const int bits = 32 - __builtin_clz(p.E);  // an expert index, E among them
     for (int64_t q = r0; q < r1; q += 64) {
