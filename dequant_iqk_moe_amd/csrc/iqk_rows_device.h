@@ -6,26 +6,26 @@
 
 namespace iqk {
 
-// V (4 or 8) consecutive values as they lie in memory.
-template <int DT, int V = 8>
+// Eight consecutive values as they lie in memory.
+template <int DT>
 struct Raw {
-    uint32_t w[DT == IQK_F32 ? V : V / 2];
+    uint32_t w[DT == IQK_F32 ? 8 : 4];
 };
 
-// Values i .. i + V - 1 of p, of which `left` are there; the others are zero.
+// Values i .. i + 7 of p, of which `left` are there; the others are zero.
 // (Rows begin wherever their length puts them: loads take any address.)
-template <int DT, int V = 8>
-__device__ __forceinline__ Raw<DT, V> load_raw(const void* p, int64_t i, int left) {
-    Raw<DT, V> r;
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void* p, int64_t i, int left) {
+    Raw<DT> r;
     constexpr int kSize = DT == IQK_F32 ? 4 : 2;
-    if (left >= V) {
-        __builtin_memcpy(r.w, (const char*)p + i * kSize, V * kSize);
+    if (left >= 8) {
+        __builtin_memcpy(r.w, (const char*)p + i * kSize, 8 * kSize);
         return r;
     }
 #pragma unroll
-    for (int j = 0; j < V * kSize / 4; ++j) r.w[j] = 0;
+    for (int j = 0; j < 2 * kSize; ++j) r.w[j] = 0;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < 8; ++j) {
         if (j >= left) continue;
         if constexpr (DT == IQK_F32) r.w[j] = ((const uint32_t*)p)[i + j];
         else r.w[j / 2] |= (uint32_t)((const uint16_t*)p)[i + j] << (j % 2 * 16);
@@ -33,22 +33,14 @@ __device__ __forceinline__ Raw<DT, V> load_raw(const void* p, int64_t i, int lef
     return r;
 }
 
-template <int DT, int V>
-__device__ __forceinline__ void widen_raw(const Raw<DT, V>& r, float (&v)[V]) {
+template <int DT>
+__device__ __forceinline__ void widen_raw(const Raw<DT>& r, float (&v)[8]) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < 8; ++j) {
         if constexpr (DT == IQK_F32) v[j] = __uint_as_float(r.w[j]);
         else if constexpr (DT == IQK_BF16) v[j] = __uint_as_float(j % 2 ? r.w[j / 2] & 0xFFFF0000u : r.w[j / 2] << 16);
         else v[j] = half_to_float(j % 2 ? r.w[j / 2] >> 16 : r.w[j / 2] & 0xFFFFu);
     }
-}
-
-// The same for a type known at run time only (the same in every lane).
-template <int V>
-__device__ __forceinline__ void load_any(const void* p, int dtype, int64_t i, int left, float (&v)[V]) {
-    if (dtype == IQK_F32) widen_raw(load_raw<IQK_F32, V>(p, i, left), v);
-    else if (dtype == IQK_BF16) widen_raw(load_raw<IQK_BF16, V>(p, i, left), v);
-    else widen_raw(load_raw<IQK_F16, V>(p, i, left), v);
 }
 
 // Two values in 16 bits, rounded to nearest even (the hardware's conversions).
@@ -59,33 +51,27 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
 }
 
-// min(left, V) values of v to y + i (any address)
-template <int DT, int V>
-__device__ __forceinline__ void store_some(void* y, int64_t i, const float (&v)[V], int left) {
-    Raw<DT, V> r;
+// min(left, 8) values of v to y + i (any address)
+template <int DT>
+__device__ __forceinline__ void store_some(void* y, int64_t i, const float (&v)[8], int left) {
+    Raw<DT> r;
     if constexpr (DT == IQK_F32) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) r.w[j] = __float_as_uint(v[j]);
+        for (int j = 0; j < 8; ++j) r.w[j] = __float_as_uint(v[j]);
     } else {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) r.w[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) r.w[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
     }
-    if (left >= V) {
+    if (left >= 8) {
         __builtin_memcpy((char*)y + i * (DT == IQK_F32 ? 4 : 2), r.w, sizeof(r.w));
         return;
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
+    for (int j = 0; j < 8; ++j) {
         if (j >= left) continue;
         if constexpr (DT == IQK_F32) ((uint32_t*)y)[i + j] = r.w[j];
         else ((uint16_t*)y)[i + j] = (uint16_t)(r.w[j / 2] >> (j % 2 * 16));
     }
-}
-template <int V>
-__device__ __forceinline__ void store_any(void* y, int dtype, int64_t i, const float (&v)[V], int left) {
-    if (dtype == IQK_F32) store_some<IQK_F32>(y, i, v, left);
-    else if (dtype == IQK_BF16) store_some<IQK_BF16>(y, i, v, left);
-    else store_some<IQK_F16>(y, i, v, left);
 }
 
 // x summed over the wave, in every lane: rotations within each 16 lanes, then
