@@ -1172,6 +1172,8 @@ def _block(x, y, post_weight, gate, next_weight, alpha, beta, eps) -> _Block:
     ydt = dt
     if y is not None:
         ydt = _float_dtype(y, "y")
+        if y.dim() == 0 or y.shape[-1] != n:
+            raise IqkValueError(_E_SIZE, f"y must be [..., {n}]")
     weights = [t for t in (post_weight, next_weight) if t is not None]
     if len(weights) == 2 and weights[0].dtype != weights[1].dtype:
         raise IqkValueError(_E_ARG, "post_weight and next_weight must be of one type")

@@ -340,9 +340,17 @@ norm_grad_kernel(NormParams p) {
                 two[1] = __builtin_fmaf(r[i][j], a.wn[j] * dh[j], two[1]);
             }
         }
-        if (p.dh) team_sum<TEAM, 2>(two, lds, odd + 1);
-        // (without dh its values are zero, and so is back)
-        const float q = inv_rms(two[0], p), back = p.dh ? q * q * q / (float)p.n * two[1] : 0.f;
+        float q = 0.f, back = 0.f;
+        if (p.dh) {
+            team_sum<TEAM, 2>(two, lds, odd + 1);
+            q = inv_rms(two[0], p);
+            back = q * q * q / (float)p.n * two[1];
+        } else {  // D is dr, whatever r
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) r[i][j] = 0.f;
+        }
         const Rsrc dxr = row_of(p.dx, t, p.n, kSizeOf<XT>);
         float end[2] = {0.f, 0.f};  // v y, D u
 #pragma unroll
@@ -384,12 +392,14 @@ norm_grad_kernel(NormParams p) {
         const Rsrc dyr = row_of(p.dy, t, p.n, kSizeOf<YT>);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float y[V];
-            forget(row.y[i]);
-            widen_piece(row.y[i], y);
+            if (p.wp) {  // (else it is v, whatever y)
+                float y[V];
+                forget(row.y[i]);
+                widen_piece(row.y[i], y);
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = s[0] * r[i][j] - off * y[j];
-            store_piece<YT>(dyr, chunk(i), y);
+                for (int j = 0; j < V; ++j) r[i][j] = s[0] * r[i][j] - off * y[j];
+            }
+            store_piece<YT>(dyr, chunk(i), r[i]);
         }
     }
     float* sums = p.sums + team * p.columns * p.n;
@@ -520,7 +530,7 @@ bool wide_rows(int64_t n, std::initializer_list<const void*> all) {
     return wide;
 }
 
-// Teams of the gradient: the 512 threads that a CU holds of it.
+// Teams of the gradient: the threads that the card's CUs hold of it (1024 of up to 128 registers, 512 of more).
 int64_t grad_teams(int64_t T, int64_t n) {
     const int team = team_size(n), per = team == 64 ? 4 : 1;
     const int64_t most = 256 * (n <= 4096 ? 1024 : 512) / team;

@@ -485,7 +485,8 @@ int iqk_moe_sort(const void* x, int dtype, const int32_t* ids, int64_t T, int k,
  * counts as a row of zeros, so that the devices of a group sum up to the whole;
  * its weight is still applied: a NaN weight (iqk_router_topk's for a row it
  * could not choose for) makes the row NaN.  float32 sums in slot order, each
- * product rounded by itself as in iqk_combine, one rounding to y_dtype. */
+ * product rounded by itself as in iqk_combine, one rounding to y_dtype.  y
+ * overlaps no input. */
 int iqk_moe_unsort(const void* ys, int ys_dtype, const int32_t* place, const float* weights, int64_t T, int k,
                    int64_t n, void* y, int y_dtype, void* stream);
 
@@ -494,7 +495,8 @@ int iqk_moe_unsort(const void* ys, int ys_dtype, const int32_t* place, const flo
  * of no expert; d_weights device float32 [T, k], the dot product of dy[t] and
  * ys[place[t, j]] (0 for a pair of no expert), float32 sums, the same every time.
  * Either result may be null and is then not computed (ys may be null without
- * d_weights).  place holds every row once, as iqk_moe_sort makes it. */
+ * d_weights).  place holds every row once, as iqk_moe_sort makes it; the results
+ * overlap no input. */
 int iqk_moe_unsort_grad(const void* dy, int dy_dtype, const void* ys, int ys_dtype, const int32_t* place,
                         const float* weights, int64_t T, int k, int64_t n, void* d_ys, float* d_weights,
                         void* stream);
@@ -587,8 +589,9 @@ int iqk_block_norm(const iqk_block* b, void* r, void* h, void* stream);
  * dh must be null where next_weight is): dx of dtype, dy of y_dtype, d_post and
  * d_next [n] of weight_dtype, d_gate as gate.  Each result may be null and is then
  * not computed; those of null inputs must be.  r is computed again from x and
- * y.  Parameters' gradients are float32 sums over the tokens, in an order that
- * depends on T and n alone, rounded once; results overlap no input.  workspace (16-byte aligned,
+ * y.  Without dh, dx = alpha * dr and, without post_weight, dy = beta * gate * dr
+ * whatever x and y hold (infinities and NaN among it).  Parameters' gradients are float32 sums over the tokens, in an order that depends on T and n
+ * alone, rounded once; results overlap no input.  workspace (16-byte aligned,
  * iqk_block_norm_grad_workspace bytes) holds parts of those sums; it may be null
  * where none are asked for. */
 int iqk_block_norm_grad_workspace(const iqk_block* b, size_t* bytes);

@@ -204,6 +204,7 @@ def test_binding_refuses_wrong_sizes():
             lambda: q.int8_linear(_weights(), f(3, 16), x_scales=f(2)), lambda: q.int8_linear(_weights(), f(3, 16), y=f(3, 5)),
             lambda: q.int8_grouped(_weights(), f(3, 16), f(4, dtype=i32)), lambda: q.int8_grouped(_weights(), f(3, 16), f(3)),
             lambda: q.int8_grouped(_weights(), f(16), f(3, dtype=i32)),
+            lambda: q.block_norm(f(3, 8), f(8, 3), r=f(3, 8)), lambda: q.block_norm(f(3, 8), f(24), r=f(3, 8)),
             lambda: q.block_norm(f(3, 8), f(3, 7), r=f(3, 8)), lambda: q.block_norm(f(3, 8), f(3, 8), r=f(3, 7)),
             lambda: q.block_norm(f(3, 8), f(3, 8), post_weight=f(7)), lambda: q.block_norm(f(3, 8), f(3, 8), gate=f(3)),
             lambda: q.block_norm(f(3, 8), f(3, 8), gate=f(8, 3)),

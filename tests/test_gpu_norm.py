@@ -87,7 +87,7 @@ def _check_forward(v, a):
         f["h"].check(h)
 
 
-def _check_grad(v, a, dr, dh):
+def _check_grad(v, a, dr, dh, cuda=_cuda):
     f = _forward(v, **a)
     T, n = f["x"].v.shape
     columns = T / 256 + 1 + T / 16 + 1 + 16
@@ -116,7 +116,7 @@ def _check_grad(v, a, dr, dh):
             cube = f["s"] * f["s"] * f["s"] * Ev(1.0 / n)
             D = f["s"] * w - cube * (w * f["y"]).sum(1, ROW + 1) * f["y"]
         bounds["y"] = D
-    c = _cuda(v)
+    c = cuda(v)
     got = q.block_norm_grad(c["x"], c["y"], None if dr is None else dr.cuda(), None if dh is None else dh.cuda(),
                             post_weight=c["post_weight"], gate=c["gate"], next_weight=c["next_weight"], **a)
     d = lambda t: None if t is None else t.double().numpy()
@@ -307,3 +307,55 @@ def test_results_are_the_same_every_time():
     first = q.block_norm_grad(v["x"], v["y"], dr, dr, **args)
     for _ in range(3):
         assert all(torch.equal(s, t) for s, t in zip(first, q.block_norm_grad(v["x"], v["y"], dr, dr, **args)))
+
+
+@pytest.mark.parametrize("n", [64, 1024, 2048, 4096, 8192])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_tensors_that_begin_anywhere(n, dtype):
+    """Rows of whole chunks whose first value lies at no multiple of 16 bytes, one tensor of the call at a time and all
+    of them: each value as where it does, and nothing beside a result is written."""
+    T = 5
+
+    def shifted(t, fill=None):
+        buf = torch.full((t.numel() + 16,), 7.0, dtype=t.dtype, device="cuda")
+        v = buf[1:t.numel() + 1].view(t.shape)
+        if fill is None:
+            v.copy_(t)
+        return buf, v
+
+    v, a = _inputs(T, n, dtype, y_dtype=F32), _args(0.5, 0.7)
+    c = _cuda(v)
+    dr, dh = (_inputs(T, n, dtype, seed=s)["x"] for s in (1, 2))
+    f = _forward(v, **a)
+    for moved in (*[(m,) for m in c], tuple(c)):
+        w = {m: shifted(t)[1] if m in moved else t for m, t in c.items()}
+        (rb, r), (hb, h) = shifted(c["x"], 0), shifted(c["x"], 0)
+        q.block_norm(**w, **a, r=r, h=h)
+        f["r"].check(r)
+        f["h"].check(h)
+        for b in (rb, hb):
+            assert b[0] == 7 and (b[-15:] == 7).all()
+        _check_grad(v, a, dr, dh, cuda=lambda _: w)
+
+
+@pytest.mark.parametrize("n", [33, 520, 4096, 8192])
+@pytest.mark.parametrize("gate", [None, "channel", "token", "element"])
+def test_no_gradient_through_values_without_a_norm(n, gate):
+    """Without a norm behind them, infinities and NaN in x and y have no part in their gradients."""
+    v, a = _cuda(_inputs(4, n, F32, post=False, gate=gate, nxt=False)), _args(0.5, 2.0)
+    dr = torch.randn(4, n, device="cuda")
+    args = dict(gate=v["gate"], **a)
+    clean = q.block_norm_grad(v["x"], v["y"], dr, None, **args)
+    x, y = v["x"].clone(), v["y"].clone()
+    x[0, 3], x[1, 4], y[1, 5], y[2, 6], x[2, 6] = float("nan"), float("inf"), float("nan"), float("-inf"), float("inf")
+    dx, dy, _, dg, _ = q.block_norm_grad(x, y, dr, None, **args)
+    assert torch.equal(dx, 0.5 * dr) and torch.equal(dx, clean[0]) and torch.equal(dy, clean[1])
+    if gate == "element":
+        there = torch.isfinite(y)
+        assert torch.equal(dg[there], clean[3][there])
+    # a norm of y alone: a row of x has no part in dy, nor y in dx
+    w = torch.ones(n, device="cuda")
+    got = q.block_norm_grad(x, v["y"], dr, None, post_weight=w, **args)
+    want = q.block_norm_grad(v["x"], v["y"], dr, None, post_weight=w, **args)
+    assert all(torch.equal(s, t) for s, t in zip(got[:3], want[:3]))
+    assert torch.equal(q.block_norm_grad(x, y, dr, None, post_weight=w, **args)[0], 0.5 * dr)
