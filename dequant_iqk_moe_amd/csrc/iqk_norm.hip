@@ -21,6 +21,7 @@
 // buffer's loads give zeros and its stores are dropped, so no path has a branch for
 // the end of a row.
 #include <algorithm>
+#include <cmath>
 
 #include "iqk_block.h"
 #include "iqk_rows_device.h"
@@ -530,11 +531,17 @@ bool wide_rows(int64_t n, std::initializer_list<const void*> all) {
     return wide;
 }
 
-// Teams of the gradient: the threads that the card's CUs hold of it (1024 of up to 128 registers, 512 of more).
+// Teams of the gradient, at most the threads that the card's CUs hold of it (1024 of up to 128 registers, 512 of
+// more).  A team's time grows with its rows and the join's with the teams, so the sum is least where rows grow with
+// the root of T, and with powers of two, which leave the CUs equal shares: 4095 x 512 takes 29 us with a team for each
+// row, 19.5 with one for two rows, 16.2 for four, 18.5 for eight; 300 rows 8.9, 8.5, 11.1, 15.4; 8192 rows 28, 28, 22
+// and 22, and 24.5 with six.
 int64_t grad_teams(int64_t T, int64_t n) {
     const int team = team_size(n), per = team == 64 ? 4 : 1;
     const int64_t most = 256 * (n <= 4096 ? 1024 : 512) / team;
-    return (std::min(std::max<int64_t>(T, 1), most) + per - 1) / per * per;
+    const int64_t rows = (int64_t)std::exp2(std::max(0.0, std::round(std::log2(std::sqrt((double)T) / 12))));
+    const int64_t teams = std::max<int64_t>(1, (T + rows - 1) / rows);
+    return (std::min(teams, most) + per - 1) / per * per;
 }
 
 // A grid of `groups` workgroups; a launch of more than 2^32 threads goes out as a plane.
