@@ -900,7 +900,7 @@ def _on(stream):
 
 @functools.lru_cache(maxsize=1024)
 def moe_sort_workspace_bytes(T: int, k: int, E: int) -> int:
-    """Workspace moe_sort needs for T tokens of k slots (0 up to 8192 pairs)."""
+    """Workspace moe_sort needs for T tokens of k slots (0: none, few pairs are sorted in one launch)."""
     b = ctypes.c_size_t()
     _check(_lib.iqk_moe_sort_workspace(T, k, E, ctypes.byref(b)))
     return b.value

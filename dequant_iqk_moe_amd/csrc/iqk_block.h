@@ -15,7 +15,7 @@ struct SortLaunch {
     int64_t T;
     int k, E;
     int64_t n;
-    int32_t* hist;  // [sort_slices(T * k), E + 1], where those are more than 0
+    int32_t* hist;  // [sort_slices(T, k), E + 1], where those are more than 0
     void* xs;       // [T * k, n]
     int32_t *offsets, *place;  // [E + 1], [T, k]
 };
@@ -47,8 +47,8 @@ struct UnsortGradLaunch {
     float* d_weights;  // [T, k], or null
 };
 
-// Slices of P pairs that a large sort counts by themselves (0: none).
-int sort_slices(int64_t P);
+// Slices of its pairs that a large sort counts by themselves (0: none, it goes in one launch).
+int sort_slices(int64_t T, int k);
 hipError_t launch_sort(const SortLaunch& a, hipStream_t s);
 hipError_t launch_unsort(const UnsortLaunch& a, hipStream_t s);
 hipError_t launch_unsort_grad(const UnsortGradLaunch& a, hipStream_t s);

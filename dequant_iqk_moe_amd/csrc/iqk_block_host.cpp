@@ -39,7 +39,7 @@ int check_experts(int64_t E) {
     return IQK_OK;
 }
 
-size_t sort_bytes(int64_t T, int k, int64_t E) { return (size_t)iqk::sort_slices(T * k) * (size_t)(E + 1) * 4; }
+size_t sort_bytes(int64_t T, int k, int64_t E) { return (size_t)iqk::sort_slices(T, k) * (size_t)(E + 1) * 4; }
 
 int check_block(const iqk_block* b) {
     if (!b) return fail(IQK_E_ARG, "null block descriptor");

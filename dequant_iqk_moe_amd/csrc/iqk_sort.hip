@@ -30,7 +30,6 @@ struct SortParams {
     int32_t* hist;
     int slices;
     int64_t slice;
-    int tokens, share;  // direct: tokens and offsets of a workgroup
     uint8_t* xs;
     int32_t *offsets, *place;
 };
@@ -41,35 +40,33 @@ __device__ __forceinline__ int expert_of(const SortParams& p, int64_t pair) {
     return (unsigned)e < (unsigned)p.E ? e : p.E;
 }
 
-// Copies part `part` of `parts` of token t's row to its pairs' rows (zeros where
-// they have no expert); at(j) is place[t, j].
+// Copies part `part` of `parts` of token t's row to the rows of its slots from j0 on,
+// kKeys of them (zeros where they have no expert); at(j) is place[t, j].
 template <class At>
-__device__ __forceinline__ void copy_row(const SortParams& p, int64_t t, int part, int parts, At at) {
+__device__ __forceinline__ void copy_slots(const SortParams& p, int64_t t, int j0, int part, int parts, At at) {
     const int64_t chunks = p.row / 16;
     const uint8_t* src = p.x + t * p.row;
-    for (int j0 = 0; j0 < p.k; j0 += kKeys) {
-        int32_t to[kKeys];  // (all before the first store)
+    int32_t to[kKeys];  // (all before the first store)
 #pragma unroll
-        for (int j = 0; j < kKeys; ++j) to[j] = at(min(j0 + j, p.k - 1));
-        auto row = [&](int j) { return p.xs + (int64_t)(to[j] < 0 ? -1 - to[j] : to[j]) * p.row; };
-        for (int64_t c = (int64_t)part * kThreads + threadIdx.x; c < chunks; c += (int64_t)parts * kThreads) {
-            uint4 v;
-            __builtin_memcpy(&v, src + 16 * c, 16);
+    for (int j = 0; j < kKeys; ++j) to[j] = at(min(j0 + j, p.k - 1));
+    auto row = [&](int j) { return p.xs + (int64_t)(to[j] < 0 ? -1 - to[j] : to[j]) * p.row; };
+    for (int64_t c = (int64_t)part * kThreads + threadIdx.x; c < chunks; c += (int64_t)parts * kThreads) {
+        uint4 v;
+        __builtin_memcpy(&v, src + 16 * c, 16);
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j) {
-                if (j0 + j >= p.k) continue;
-                const uint4 z = to[j] < 0 ? make_uint4(0, 0, 0, 0) : v;
-                __builtin_memcpy(row(j) + 16 * c, &z, 16);
-            }
+        for (int j = 0; j < kKeys; ++j) {
+            if (j0 + j >= p.k) continue;
+            const uint4 z = to[j] < 0 ? make_uint4(0, 0, 0, 0) : v;
+            __builtin_memcpy(row(j) + 16 * c, &z, 16);
         }
-        // what no 16 bytes hold, two at a time
-        const int64_t tail = 16 * chunks + 2 * threadIdx.x;
-        if (part == parts - 1 && tail < p.row) {
-            const uint16_t v = *(const uint16_t*)(src + tail);
+    }
+    // what no 16 bytes hold, two at a time
+    const int64_t tail = 16 * chunks + 2 * threadIdx.x;
+    if (part == parts - 1 && tail < p.row) {
+        const uint16_t v = *(const uint16_t*)(src + tail);
 #pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-                if (j0 + j < p.k) *(uint16_t*)(row(j) + tail) = to[j] < 0 ? 0 : v;
-        }
+        for (int j = 0; j < kKeys; ++j)
+            if (j0 + j < p.k) *(uint16_t*)(row(j) + tail) = to[j] < 0 ? 0 : v;
     }
 }
 
@@ -77,47 +74,52 @@ __device__ __forceinline__ void copy_row(const SortParams& p, int64_t t, int par
 // few pairs: one launch
 // ---------------------------------------------------------------------------
 
-// The place of pair p is the number of pairs q with (expert, q) below its own,
-// which every workgroup counts for its own pairs: P^2 / 64 comparisons of a
-// wave in all, on the whole card, and no pass that waits for another.  offsets[e]
-// is the count of pairs below (e, 0).
-constexpr int64_t kDirect = 8192;  // pairs up to which the ids go this way
-constexpr int kShift = 13;         // (a key holds a pair's index below 2^13 and its expert)
-constexpr int kMost = 64 + kKeys;  // places and offsets of a workgroup, whole groups of keys
+// The place of pair p is the number of pairs q with (expert, q) below its own, and
+// offsets[e] the number below (e, 0).  A workgroup counts up to kKeys of these, the
+// pairs of a token or offsets: P^2 / 64 comparisons of a wave in all, on the whole
+// card, and no pass that waits for another.  Each is a compare, a bit count and an
+// addition, the latter two on the scalar unit that a CU's waves share.
+constexpr int64_t kDirect = 8192;         // pairs that a key holds the index of
+constexpr int kShift = 13;                // (its lower bits; the expert is above)
+constexpr int64_t kDirectWork = 8 << 20;  // comparisons of a lane with kKeys keys up to which the ids go this way
+constexpr int kBatch = 2;                 // ids of a thread that are asked for together (768 x 8 pairs: one 16.0 us, two 9.9, four
+                                          // 13.6, whose comparisons wait for scalar registers)
 
 __global__ __launch_bounds__(kThreads) void sort_direct_kernel(SortParams p) {
-    __shared__ int32_t part[kWaves][kMost];
-    __shared__ int32_t at[kMost];
+    __shared__ int32_t part[kWaves][kKeys];
+    __shared__ int32_t at[kKeys];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t t0 = (int64_t)blockIdx.x * p.tokens, t1 = min(t0 + p.tokens, p.T);
-    const int pairs = t0 < t1 ? (int)(t1 - t0) * p.k : 0;
-    // offsets: the first workgroups of the launch, `share` each
-    const int wg = blockIdx.y * gridDim.x + blockIdx.x;
-    const int e0 = wg * p.share, e1 = min(e0 + p.share, p.E + 1);
-    const int count = pairs + max(e1 - e0, 0);
-    const int p0 = (int)t0 * p.k;
-    for (int i0 = 0; i0 < count; i0 += kKeys) {
-        uint32_t key[kKeys];
-        int below[kKeys];
+    const int groups = (p.k + kKeys - 1) / kKeys, rows = (int)p.T * groups;  // workgroups that have rows
+    const bool pairs = (int)blockIdx.x < rows;
+    if (!pairs && blockIdx.y > 0) return;
+    const int t = blockIdx.x / groups, j0 = ((int)blockIdx.x - t * groups) * kKeys, e0 = ((int)blockIdx.x - rows) * kKeys;
+    const int count = pairs ? min(kKeys, p.k - j0) : min(kKeys, p.E + 1 - e0), p0 = t * p.k + j0;
+    uint32_t key[kKeys];
+    int below[kKeys];
 #pragma unroll
-        for (int i = 0; i < kKeys; ++i) {
-            const int u = i0 + i;
-            uint32_t v = 0;
-            if (u < pairs) v = (uint32_t)expert_of(p, p0 + u) << kShift | (uint32_t)(p0 + u);
-            else if (u < count) v = (uint32_t)(e0 + u - pairs) << kShift;
-            key[i] = __builtin_amdgcn_readfirstlane(v);
-            below[i] = 0;
-        }
-        for (int64_t q0 = wave * 64; q0 < p.P; q0 += kThreads) {
-            const int64_t q = q0 + lane;
-            const uint32_t v = q < p.P ? (uint32_t)expert_of(p, q) << kShift | (uint32_t)q : 0xFFFFFFFFu;
+    for (int i = 0; i < kKeys; ++i) {
+        uint32_t v = 0;
+        if (i < count) v = pairs ? (uint32_t)expert_of(p, p0 + i) << kShift | (uint32_t)(p0 + i) : (uint32_t)(e0 + i) << kShift;
+        key[i] = __builtin_amdgcn_readfirstlane(v);
+        below[i] = 0;
+    }
+    const int P = (int)p.P;
+    for (int q0 = wave * 64; q0 < P; q0 += kBatch * kThreads) {
+        uint32_t v[kBatch];
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) below[i] += __builtin_popcountll(__ballot(v < key[i]));
+        for (int b = 0; b < kBatch; ++b) {
+            const int q = q0 + b * kThreads + lane;
+            const uint32_t e = (uint32_t)expert_of(p, min(q, P - 1));
+            v[b] = q < P ? e << kShift | (uint32_t)q : 0xFFFFFFFFu;
         }
-        if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < kKeys; ++i) part[wave][i0 + i] = below[i];
-        }
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int i = 0; i < kKeys; ++i) below[i] += __builtin_popcountll(__ballot(v[b] < key[i]));
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i) part[wave][i] = below[i];
     }
     __syncthreads();
     if ((int)threadIdx.x < count) {
@@ -125,17 +127,16 @@ __global__ __launch_bounds__(kThreads) void sort_direct_kernel(SortParams p) {
         int32_t v = 0;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) v += part[w][u];
-        if (u < pairs) {
+        if (pairs) {
             if (expert_of(p, p0 + u) == p.E) v = -1 - v;
             at[u] = v;
             if (blockIdx.y == 0) p.place[p0 + u] = v;
         } else {
-            p.offsets[e0 + u - pairs] = v;
+            p.offsets[e0 + u] = v;
         }
     }
     __syncthreads();
-    for (int64_t t = t0; t < t1; ++t)
-        copy_row(p, t, blockIdx.y, gridDim.y, [&](int j) { return __builtin_amdgcn_readfirstlane(at[(int)(t - t0) * p.k + j]); });
+    if (pairs) copy_slots(p, t, j0, blockIdx.y, gridDim.y, [&](int j) { return __builtin_amdgcn_readfirstlane(at[j - j0]); });
 }
 
 // ---------------------------------------------------------------------------
@@ -240,7 +241,7 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(SortParams p) {
 __global__ __launch_bounds__(kThreads) void sort_copy_kernel(SortParams p) {
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
         const int32_t* place = p.place + t * p.k;
-        copy_row(p, t, blockIdx.y, gridDim.y, [&](int j) { return place[j]; });
+        for (int j0 = 0; j0 < p.k; j0 += kKeys) copy_slots(p, t, j0, blockIdx.y, gridDim.y, [&](int j) { return place[j]; });
     }
 }
 
@@ -411,8 +412,10 @@ unsigned token_groups(int64_t T) { return (unsigned)std::min<int64_t>(T, 1 << 22
 
 }  // namespace
 
-int sort_slices(int64_t P) {
-    if (P <= kDirect) return 0;
+// Three launches take 12.5 us and the rows' bytes, whatever the pairs are: one is as fast at 1000 tokens of 8 slots (12.2).
+int sort_slices(int64_t T, int k) {
+    const int64_t P = T * k;
+    if (P <= kDirect && T * ((k + kKeys - 1) / kKeys) * P <= kDirectWork) return 0;
     return (int)std::min(kSlices, (P + kSlicePairs - 1) / kSlicePairs);
 }
 
@@ -429,18 +432,11 @@ hipError_t launch_sort(const SortLaunch& a, hipStream_t s) {
     p.xs = (uint8_t*)a.xs;
     p.offsets = a.offsets;
     p.place = a.place;
-    p.slices = sort_slices(p.P);
+    p.slices = sort_slices(a.T, a.k);
     const int64_t chunks = p.row / 16;
     if (p.slices == 0) {
-        p.tokens = 1;  // (kDirect tokens at most)
-        const int64_t groups = std::max<int64_t>(a.T, 1), parts = row_parts(a.T, chunks);
-        // (kKeys at least, and no more than the kMost - 64 + 64 / k .. entries a workgroup keeps: E <= 2048)
-        p.share = (int)std::max<int64_t>(kKeys, (a.E + groups * parts) / (groups * parts));
-        dim3 grid((unsigned)groups, (unsigned)parts);
-        if (p.share > kMost - a.k) {  // few workgroups and many experts: more of them, without rows
-            p.share = kKeys;
-            grid.x = (unsigned)std::max<int64_t>(groups, (a.E + kKeys) / kKeys);
-        }
+        const int64_t groups = a.T * ((a.k + kKeys - 1) / kKeys);
+        const dim3 grid((unsigned)(groups + (a.E + kKeys) / kKeys), row_parts(groups, chunks));
         hipLaunchKernelGGL(sort_direct_kernel, grid, dim3(kThreads), 0, s, p);
         return hipGetLastError();
     }

@@ -470,7 +470,7 @@ int iqk_fp8_path(const iqk_fp8_weights* w, int64_t T, int k, int y_dtype, int32_
  * device int32 [E + 1], offsets[e] = first row of expert e and offsets[E] = rows
  * that have one; place device int32 [T, k], the pair's row, or -1 - row where it
  * has no expert.  dtype IQK_F32, IQK_F16 or IQK_BF16, for x and xs.  workspace:
- * iqk_moe_sort_workspace bytes (0 up to 8192 pairs; it may be null there),
+ * iqk_moe_sort_workspace bytes (0 for few pairs; it may be null there),
  * 4-byte aligned; its contents before the call make no difference.
  * T >= 0, k in [1, 64], T * k <= 2^24, E <= 2048, n in [1, 2^20], n of any
  * size (IQK_E_ARG); rows and pointers are aligned to their type. */

@@ -28,8 +28,10 @@ def test_sort_refuses(change, code):
 
 
 def test_sort_workspace():
-    assert q.moe_sort_workspace_bytes(2048, 4, 64) == 0
-    assert q.moe_sort_workspace_bytes(2049, 4, 64) == 9 * 65 * 4  # a slice per 1024 pairs
+    for T, k in ((0, 1), (1, 64), (1024, 8), (2048, 2), (2896, 1), (128, 64)):
+        assert q.moe_sort_workspace_bytes(T, k, 64) == 0
+    for T, k, slices in ((1025, 8, 9), (2049, 2, 5), (2897, 1, 3), (129, 64, 9), (2049, 4, 9)):
+        assert q.moe_sort_workspace_bytes(T, k, 64) == slices * 65 * 4  # a slice per 1024 pairs
     assert q.moe_sort_workspace_bytes(1 << 22, 4, 2048) == 128 * 2049 * 4
     for bad in ((-1, 4, 64), (4, 0, 64), (4, 4, 0), (1 << 24, 2, 64)):
         with pytest.raises(q.IqkValueError):

@@ -50,7 +50,9 @@ def _check_sort(x, ids, E, got):
 @pytest.mark.parametrize("T,k,E,n,invalid", [
     (1, 1, 1, 1, 0), (1, 6, 256, 4096, 0), (1, 6, 256, 7, 1.0), (2, 64, 3, 33, 0.1), (5, 3, 2048, 8, 0), (37, 8, 60, 129, 0.3),
     (64, 2, 1, 2048, 0), (700, 5, 16, 24, 0.5), (8192, 1, 7, 5, 0.1), (1024, 8, 160, 10, 0),  # the last in one launch
-    (1025, 8, 160, 10, 0), (8193, 1, 2048, 3, 0.2), (1500, 6, 256, 264, 0.9), (2049, 4, 3, 17, 1.0), (513, 64, 2, 6, 0)])
+    (1025, 8, 160, 10, 0), (8193, 1, 2048, 3, 0.2), (1500, 6, 256, 264, 0.9), (2049, 4, 3, 17, 1.0), (513, 64, 2, 6, 0),
+    (96, 64, 300, 40, 0.2), (128, 64, 2048, 9, 0), (129, 64, 40, 130, 0.1), (2048, 2, 33, 12, 0.3), (2049, 2, 33, 12, 0.3), (2896, 1, 9, 17, 0),
+    (2897, 1, 9, 17, 0)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_sort(T, k, E, n, invalid, dtype):
     announce(f"sort {T} x {k} of {E}, {n} {dtype}")
