@@ -114,7 +114,7 @@ __device__ __forceinline__ void make_plan(const PrepParams& p) {
 
 // A team of 64 or 256 threads takes a row; rows of up to 32 values a thread stay in
 // registers between the largest value and the codes, longer ones are read again.
-// Bound: bytes.
+// Bound: bytes (bfloat16 rows of 4096: 8192 in 17 us, 5.9 TB/s; 24576 in 48, 6.3).
 constexpr int kChunks = 4;
 
 template <int XT, int TEAM, bool HOLD>
@@ -177,7 +177,8 @@ __global__ __launch_bounds__(kThreads) void int8_prep_kernel(PrepParams p) {
 // block, the 16 values at 16 * (l >> 4) and the 16 at 64 + 16 * (l >> 4).
 // Grouped: workgroup column s starts at row s, and takes part if an expert's rows
 // begin there, or its next ones that do not fit a workgroup.
-// Bound: bytes of the weights, and a launch's start.
+// Bound: bytes of the weights, and a launch's start (one row by 4096 x 4096: 5.1 us
+// in the kernel, 3.3 TB/s, of which 3.5 us is what the smallest kernel takes).
 constexpr int kFewWaves = 8, kFewThreads = 64 * kFewWaves;
 constexpr int kFewAhead = 4;          // blocks of the depth a wave requests together
 constexpr int kFewBytes = 33 * 1024;  // most codes of x a workgroup keeps
@@ -357,7 +358,8 @@ __global__ __launch_bounds__(kFewThreads) void int8_few_kernel(FewParams p) {
 // As above, with x's fragments straight from memory (the L2, after the first
 // workgroups): each is used by one wave of the workgroup.  The next blocks are asked
 // for while the last ones are multiplied.
-// Bound: the fragments of x, which every 16 weight rows read again.
+// Bound: the fragments of x, which every 16 weight rows read again (17 rows by 4096
+// x 4096 with their quantization 10.9 us, 32 rows 11).
 template <int NT, int YT>
 __global__ __launch_bounds__(kFewThreads) void int8_rows_kernel(FewParams p) {
     __shared__ int red[kFewWaves][NT][64][4];

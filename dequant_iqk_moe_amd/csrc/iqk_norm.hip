@@ -15,7 +15,10 @@
 // not read beside them.
 //
 // Bound: bytes.  A team (a wave, or a workgroup) holds a row in registers as it
-// lies in memory; sums go through float32, lanes and waves in a fixed order.
+// lies in memory, so each row is read once; sums go through float32, lanes and
+// waves in a fixed order.  8192 x 4096 bfloat16: 52 us (268 MB, 5.2 TB/s; a large
+// copy runs at 4.8); the gradient of 4095 rows 52 us, of which 46 the rows (201 MB,
+// 4.4 TB/s, and 25 MB of parts of the parameters' gradients) and 5 their join.
 // Chunks of eight values are read where every row begins at a multiple of 16 bytes,
 // single values elsewhere: either way a chunk is in its row or past it, where a
 // buffer's loads give zeros and its stores are dropped, so no path has a branch for
@@ -487,7 +490,12 @@ void by_types(const iqk_block& b, F f) {
 template <int V>
 using Int = std::integral_constant<int, V>;
 
-// f(threads of a team, values of a chunk, chunks of a thread) for rows of n values
+// f(threads of a team, values of a chunk, chunks of a thread) for rows of n values.
+// Eight values a thread to 2048, sixteen beyond (bfloat16, with 8, 16 and 32 of them:
+// 16384 x 512 14.2, 16.6 and 21.6 us; 16384 x 1024 27.9, 28.7 and 32.2; 2048 x 2048 7.6,
+// 7.5 and 8.3; 2048 x 4096 14.6, 13.2 and 14.1; 2048 x 8192 31.1, 28.5 and 29.0; 256 x
+// 2048 3.6, 4.3 and 5.7; 256 x 4096 4.0, 4.7 and 6.1).  The rows' number has no part in
+// it: a row's results do not depend on what it is called with.
 template <class F>
 void by_row(int64_t n, bool wide, F f) {
     auto go = [&](auto team, auto values) {
@@ -496,14 +504,16 @@ void by_row(int64_t n, bool wide, F f) {
         else f(team, Int<1>{}, values);
     };
     if (n <= 512) go(Int<64>{}, Int<8>{});
-    else if (n <= 1024) go(Int<64>{}, Int<16>{});
+    else if (n <= 1024) go(Int<128>{}, Int<8>{});
     else if (n <= 2048) go(Int<256>{}, Int<8>{});
     else if (n <= 4096) go(Int<256>{}, Int<16>{});
     else go(Int<512>{}, Int<16>{});
 }
 
 // The gradient, whose parts of the parameters' gradients and their values take six
-// registers a value: eight values of a thread as far as 512 threads reach.
+// registers a value: eight values of a thread as far as 512 threads reach, in 122
+// registers, so that a CU holds two teams of 4096 values (rows of 4095 x 4096 46 us;
+// 60 with branches for a row's end and 256 threads of sixteen values).
 template <class F>
 void by_grad_row(int64_t n, bool wide, F f) {
     auto go = [&](auto team, auto values) {

@@ -9,7 +9,11 @@
 // -1 - row(t, j) for those, whose rows count as zeros.
 //
 // Bound: bytes.  All row kernels go token by token, so a token's own row is
-// read or written once for its k expert rows.
+// read or written once for its k expert rows, in pieces of 16 bytes a lane; its
+// places are read before any row.  Measured, bfloat16 rows of 4096 (a large copy
+// runs at 4.8 TB/s): 8192 tokens of 6 slots sorted in 105 us, 85 of them the
+// copy (5.5 TB/s); 500 tokens of float32 rows unsorted in 10 us (5 TB/s); the
+// gradient of 4096 tokens in 92 us, 85 in the kernel (5.1 TB/s).
 #include <algorithm>
 
 #include "iqk_block.h"
@@ -143,6 +147,9 @@ __global__ __launch_bounds__(kThreads) void sort_direct_kernel(SortParams p) {
 // many pairs: slices are counted, then placed, then the rows are copied
 // ---------------------------------------------------------------------------
 
+// A thousand pairs a slice: the counts of 48 slices (49152 pairs, 256 experts) are
+// summed in 2 of the placing kernel's 7.7 us, which ranks 256 pairs a wave; slices
+// of 512 rank half as many and sum twice as many counts, in the same time.
 constexpr int64_t kSlices = 128, kSlicePairs = 1024;
 
 __global__ __launch_bounds__(kThreads) void sort_count_kernel(SortParams p) {
@@ -263,7 +270,10 @@ struct UnsortParams {
 
 // Rows of at least eight values are taken in chunks of eight, the last of which
 // ends with the row: what it shares with the one before is made twice, with the same
-// bits.  So no load has a branch for the row's end.  Shorter rows are one chunk.
+// bits.  So no load has a branch for the row's end, and all of a token's rows are
+// asked for together (gradient of 4096 x 6 rows of 4096: 109 us with the branches,
+// 85 without; 1025 x 8 rows of 2047 float32 values back 16 and 13).  Shorter rows
+// are one chunk.
 struct Chunk {
     int64_t c;       // its first value
     int left, twice;  // its values, and how many of them are the one before's too
