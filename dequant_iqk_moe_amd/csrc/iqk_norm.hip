@@ -6,11 +6,13 @@
 //   h = r s(r) wn            from r before its rounding
 //
 // Gradient, from dr and dh, with s = s(y), q = s(r):
-//   D    = dr + q wn dh - r q^3 / n sum(wn dh r)
+//   D    = dr + q (wn dh - r q m), m = q / n sum(wn dh r)
 //   dx   = alpha D           d_wn = sum_t dh r q
 //   dg   = beta D u          (summed over tokens or over the row with g's kind)
 //   v    = beta g D wp       d_wp = sum_t beta g D y s
-//   dy   = s v - y s^3 / n sum(v y)     (beta g D without wp)
+//   dy   = s (v - y s / n sum(v y s))   (beta g D without wp)
+// Each factor of s or q meets a row's values by itself: a cube of them leaves
+// float32 from rows of 1e12 on, and beside zeros and an eps below 1e-25.
 // r is computed again from x and y, so it is not rounded there either, and is
 // not read beside them.
 //
@@ -344,11 +346,11 @@ norm_grad_kernel(NormParams p) {
                 two[1] = __builtin_fmaf(r[i][j], a.wn[j] * dh[j], two[1]);
             }
         }
-        float q = 0.f, back = 0.f;
+        float q = 0.f, mean = 0.f;  // m of the formula
         if (p.dh) {
             team_sum<TEAM, 2>(two, lds, odd + 1);
             q = inv_rms(two[0], p);
-            back = q * q * q / (float)p.n * two[1];
+            mean = two[1] * q / (float)p.n;
         } else {  // D is dr, whatever r
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -356,7 +358,7 @@ norm_grad_kernel(NormParams p) {
                 for (int j = 0; j < V; ++j) r[i][j] = 0.f;
         }
         const Rsrc dxr = row_of(p.dx, t, p.n, kSizeOf<XT>);
-        float end[2] = {0.f, 0.f};  // v y, D u
+        float end[2] = {0.f, 0.f};  // v y s, D u
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float b[V], y[V], dr[V], dh[V], d[V];
@@ -369,8 +371,9 @@ norm_grad_kernel(NormParams p) {
             widen_piece(row.dh[i], dh);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                d[j] = dr[j] + (q * (a.wn[j] * dh[j]) - back * r[i][j]);
-                awn[i][j] = __builtin_fmaf(dh[j], r[i][j] * q, awn[i][j]);
+                const float rq = r[i][j] * q;
+                d[j] = __builtin_fmaf(q, a.wn[j] * dh[j] - rq * mean, dr[j]);
+                awn[i][j] = __builtin_fmaf(dh[j], rq, awn[i][j]);
                 dr[j] = p.alpha * d[j];
             }
             store_piece<XT>(dxr, chunk(i), dr);
@@ -380,7 +383,7 @@ norm_grad_kernel(NormParams p) {
                 end[1] += du;
                 awp[i][j] = __builtin_fmaf(bd, ys, awp[i][j]);
                 r[i][j] = bd * a.bg[j] * a.wp[j];  // (v of the formula, where r was)
-                end[0] = __builtin_fmaf(r[i][j], y[j], end[0]);
+                end[0] = __builtin_fmaf(r[i][j], ys, end[0]);
                 d[j] = p.beta * du;
             }
             if (p.dg && p.g_kind == IQK_GATE_ELEMENT) store_typed(dgr, p.g_dtype, chunk(i), d);
@@ -392,7 +395,7 @@ norm_grad_kernel(NormParams p) {
             store_typed(row_of(p.dg, t, 1, size_of(p.g_dtype)), p.g_dtype, 0, one);
         }
         if (!p.dy) continue;
-        const float off = p.wp ? s[0] * s[0] * s[0] / (float)p.n * end[0] : 0.f;
+        const float off = end[0] / (float)p.n;
         const Rsrc dyr = row_of(p.dy, t, p.n, kSizeOf<YT>);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -401,7 +404,7 @@ norm_grad_kernel(NormParams p) {
                 forget(row.y[i]);
                 widen_piece(row.y[i], y);
 #pragma unroll
-                for (int j = 0; j < V; ++j) r[i][j] = s[0] * r[i][j] - off * y[j];
+                for (int j = 0; j < V; ++j) r[i][j] = s[0] * (r[i][j] - y[j] * s[0] * off);
             }
             store_piece<YT>(dyr, chunk(i), r[i]);
         }

@@ -571,7 +571,8 @@ int iqk_int8_path(const iqk_int8_weights* w, int64_t rows, int grouped, int32_t*
  * with IQK_GATE_NONE.  Float types all.  y may be null: then r = x, alpha must
  * be 1, post_weight and gate null, and no r is written (the norm before the first
  * block).  float32 arithmetic, one rounding to each result; squares are summed in
- * float32, so rows of values beyond 1e17 are out of its range.  n in [1, 8192],
+ * float32, so rows of values beyond 1e17 are out of its range, and so are, beside
+ * an eps below 1e-36, rows of values below 1e-18 that are not zero.  n in [1, 8192],
  * n of any size; T <= 2^24; eps > 0; pointers aligned to their types. */
 typedef struct iqk_block {
     int64_t T, n;
