@@ -267,7 +267,7 @@ norm_grad_kernel(NormParams p) {
 #pragma unroll
         for (int j = 0; j < V; ++j) a.wp[j] = a.wn[j] = a.bg[j] = 1.f;
         if (p.wp) load_typed(row_of(p.wp, 0, p.n, size_of(p.w_dtype)), p.w_dtype, chunk(i), a.wp);
-        if (p.wn) load_typed(row_of(p.wn, 0, p.n, size_of(p.w_dtype)), p.w_dtype, chunk(i), a.wn);
+        if (p.wn && p.dh) load_typed(row_of(p.wn, 0, p.n, size_of(p.w_dtype)), p.w_dtype, chunk(i), a.wn);  // (no part without dh)
         if (p.g_kind == IQK_GATE_CHANNEL) load_typed(row_of(p.g, 0, p.n, size_of(p.g_dtype)), p.g_dtype, chunk(i), a.bg);
 #pragma unroll
         for (int j = 0; j < V; ++j) a.bg[j] *= p.g_kind == IQK_GATE_ELEMENT ? 1.f : p.beta;
