@@ -498,7 +498,9 @@ using Int = std::integral_constant<int, V>;
 // 16384 x 512 14.2, 16.6 and 21.6 us; 16384 x 1024 27.9, 28.7 and 32.2; 2048 x 2048 7.6,
 // 7.5 and 8.3; 2048 x 4096 14.6, 13.2 and 14.1; 2048 x 8192 31.1, 28.5 and 29.0; 256 x
 // 2048 3.6, 4.3 and 5.7; 256 x 4096 4.0, 4.7 and 6.1).  The rows' number has no part in
-// it: a row's results do not depend on what it is called with.
+// it, so a row's results are the same alone and among others.  Where one of the call's
+// rows or parameters begins at no multiple of 16 bytes, or n is no multiple of 8, a
+// thread has other values of the row, whose sums then go in another order.
 template <class F>
 void by_row(int64_t n, bool wide, F f) {
     auto go = [&](auto team, auto values) {
@@ -537,10 +539,15 @@ int team_size(int64_t n) {
     return team;
 }
 
-// Whether chunks of eight values lie at multiples of 16 bytes in all of these
-bool wide_rows(int64_t n, std::initializer_list<const void*> all) {
-    bool wide = n % 8 == 0;
-    for (const void* p : all) wide = wide && (uintptr_t)p % 16 == 0;
+// Whether chunks of eight values lie at multiples of 16 bytes in all that a call reads
+// or writes by rows: its inputs, and `more`.  (A gate of tokens is read one value at a
+// time.)
+bool wide_rows(const iqk_block& b, std::initializer_list<const void*> more) {
+    bool wide = b.n % 8 == 0;
+    auto take = [&](const void* p) { wide = wide && (uintptr_t)p % 16 == 0; };
+    for (const void* p : {b.x, b.y, b.post_weight, b.next_weight}) take(p);
+    if (b.gate_kind != IQK_GATE_TOKEN) take(b.gate);
+    for (const void* p : more) take(p);
     return wide;
 }
 
@@ -572,7 +579,7 @@ hipError_t launch_norm(const iqk_block& b, void* r, void* h, hipStream_t s) {
     p.r = r;
     p.h = h;
     by_types(b, [&](auto xt, auto yt) {
-        by_row(b.n, wide_rows(b.n, {b.x, b.y, b.post_weight, b.gate, b.next_weight, r, h}), [&](auto team, auto v, auto nv) {
+        by_row(b.n, wide_rows(b, {r, h}), [&](auto team, auto v, auto nv) {
             constexpr int TEAM = decltype(team)::value;
             using Tm = Team<TEAM>;
             hipLaunchKernelGGL((norm_kernel<decltype(xt)::value, decltype(yt)::value, TEAM, decltype(v)::value, decltype(nv)::value>),
@@ -596,7 +603,8 @@ hipError_t launch_norm_grad(const iqk_block& b, const NormGradOut& o, float* sum
     p.columns = p.has_dwp + p.has_dwn + p.has_dgc;
     const int64_t teams = grad_teams(p.T, p.n);
     by_types(b, [&](auto xt, auto yt) {
-        const bool wide = wide_rows(b.n, {b.x, b.y, b.post_weight, b.gate, b.next_weight, o.dr, o.dh, o.dx, o.dy, o.d_gate, sums});
+        // (the gradients of a gate of channels or tokens are written one value at a time)
+        const bool wide = wide_rows(b, {o.dr, o.dh, o.dx, o.dy, b.gate_kind == IQK_GATE_ELEMENT ? o.d_gate : nullptr, sums});
         by_grad_row(b.n, wide, [&](auto team, auto v, auto nv) {
             constexpr int TEAM = decltype(team)::value;
             using Tm = Team<TEAM>;
