@@ -17,6 +17,10 @@ bool is_float(int dt) { return dt == IQK_F32 || dt == IQK_F16 || dt == IQK_BF16;
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
 size_t size_of(int dt) { return dt == IQK_F32 ? 4 : 2; }
 bool typed(const void* p, int dt) { return aligned(p, size_of(dt)); }
+// whether two ranges of memory overlap (null: none)
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    return a && b && (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
 
 constexpr int64_t kMaxRows = 1LL << 24;
 constexpr int64_t kMaxWidth = 1LL << 20;
@@ -148,6 +152,14 @@ int iqk_block_norm(const iqk_block* b, void* r, void* h, void* stream) {
     if ((h != nullptr) != (b->next_weight != nullptr)) return fail(IQK_E_ARG, "h goes with next_weight, and only with it");
     if (r == h) return fail(IQK_E_ARG, "r and h must differ");
     if (!typed(r, b->dtype) || !typed(h, b->dtype)) return fail(IQK_E_ARG, "r and h must be aligned to their type");
+    const size_t values = (size_t)(b->T * b->n), bytes = values * size_of(b->dtype), y_bytes = values * size_of(b->y_dtype);
+    for (const void* p : {r, h}) {
+        // (row by row a result may take its input's place; moved by part of a row, or in a type of another size, it would
+        // lie over rows that another workgroup has yet to read)
+        if ((p != b->x && overlap(p, bytes, b->x, bytes)) || ((p != b->y || b->y_dtype != b->dtype) && overlap(p, bytes, b->y, y_bytes)))
+            return fail(IQK_E_ARG, "r and h may be x, or y of x's type, but not overlap them otherwise");
+    }
+    if (overlap(r, bytes, h, bytes)) return fail(IQK_E_ARG, "r and h must not overlap");
     hipError_t e = iqk::launch_norm(*b, r, h, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "norm launch");
     return ok();

@@ -583,7 +583,8 @@ typedef struct iqk_block {
 
 /* r: null exactly where y is; h: null exactly where next_weight is.  r may be x
  * or y, and h as well (rows are read before they are written), where the types
- * are the same; r and h differ. */
+ * are the same; other overlaps with x or y, and of r with h, are refused
+ * (IQK_E_ARG).  They overlap none of the other inputs. */
 int iqk_block_norm(const iqk_block* b, void* r, void* h, void* stream);
 
 /* Gradient of the above from dr and dh [T, n] of dtype (either may be null: zero;
