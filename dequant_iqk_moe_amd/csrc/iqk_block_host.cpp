@@ -103,6 +103,9 @@ int iqk_moe_sort(const void* x, int dtype, const int32_t* ids, int64_t T, int k,
     if (ws_bytes < need || (need && !workspace))
         return fail(IQK_E_SIZE, "workspace needs %zu bytes (got %zu)", need, workspace ? ws_bytes : 0);
     if (!aligned(workspace, 4)) return fail(IQK_E_ARG, "workspace must be 4-byte aligned");
+    const size_t rows = (size_t)(T * n) * size_of(dtype), pairs = (size_t)(T * k) * 4;
+    if (overlap(xs, rows * k, x, rows) || overlap(place, pairs, ids, pairs))
+        return fail(IQK_E_ARG, "xs must not overlap x, nor place ids");
     iqk::SortLaunch L{x, dtype, ids, T, k, (int)E, n, (int32_t*)workspace, xs, offsets, place};
     hipError_t e = iqk::launch_sort(L, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "sort launch");

@@ -14,7 +14,11 @@ int hip_fail(hipError_t e, const char* where) { return fail(IQK_E_HIP, "%s: %s",
 size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 bool is_float(int dt) { return dt == IQK_F32 || dt == IQK_F16 || dt == IQK_BF16; }
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
-size_t size_of(int dt) { return dt == IQK_F32 ? 4 : 2; }
+size_t size_of(int dt) { return dt == IQK_F32 ? 4 : dt == IQK_INT8 ? 1 : 2; }
+// whether two ranges of memory overlap
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+    return (uintptr_t)a < (uintptr_t)b + bn && (uintptr_t)b < (uintptr_t)a + an;
+}
 
 constexpr int64_t kMaxRows = 1LL << 24;
 constexpr int64_t kMaxDepth = 1LL << 16;  // (products of -128 by -128 sum to 2^30)
@@ -95,6 +99,8 @@ int product(const iqk_int8_weights* w, const void* x, int x_dtype, const float* 
     if (ws_bytes < need || (need && !workspace))
         return fail(IQK_E_SIZE, "workspace needs %zu bytes (got %zu)", need, workspace ? ws_bytes : 0);
     if (!aligned(workspace, 16)) return fail(IQK_E_ARG, "workspace must be 16-byte aligned");
+    if (overlap(y, (size_t)(rows * w->out) * size_of(y_dtype), x, (size_t)(rows * w->in) * size_of(x_dtype)))
+        return fail(IQK_E_ARG, "y must not overlap x");
     hipStream_t s = (hipStream_t)stream;
     iqk::Int8Launch L{w->experts, w->out, w->in, (const int8_t*)w->codes, w->scales, x, x_dtype, x_scales, rows,
                       grouped ? offsets : nullptr, nullptr, y, y_dtype};
@@ -135,6 +141,8 @@ int iqk_int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, int8_
     if (!x || !codes || !scales) return fail(IQK_E_ARG, "null pointer");
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 4))
         return fail(IQK_E_ARG, "x and codes must be 16-byte and scales 4-byte aligned");
+    if (overlap(codes, (size_t)(rows * n), x, (size_t)(rows * n) * size_of(x_dtype)))
+        return fail(IQK_E_ARG, "codes must not overlap x");
     hipError_t e = iqk::launch_int8_prep(iqk::Int8QuantLaunch{x, x_dtype, rows, n, codes, scales}, iqk::Int8Plan{}, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "quantize launch");
     return ok();

@@ -473,7 +473,8 @@ int iqk_fp8_path(const iqk_fp8_weights* w, int64_t T, int k, int y_dtype, int32_
  * iqk_moe_sort_workspace bytes (0 for few pairs; it may be null there),
  * 4-byte aligned; its contents before the call make no difference.
  * T >= 0, k in [1, 64], T * k <= 2^24, E <= 2048, n in [1, 2^20], n of any
- * size (IQK_E_ARG); rows and pointers are aligned to their type. */
+ * size (IQK_E_ARG); rows and pointers are aligned to their type.  Results overlap
+ * no input (xs over x and place over ids: IQK_E_ARG). */
 int iqk_moe_sort_workspace(int64_t T, int k, int64_t E, size_t* bytes);
 int iqk_moe_sort(const void* x, int dtype, const int32_t* ids, int64_t T, int k, int64_t E, int64_t n,
                  void* workspace, size_t ws_bytes, void* xs, int32_t* offsets, int32_t* place, void* stream);
@@ -523,7 +524,7 @@ typedef struct iqk_int8_weights {
  * rounded to float32, the code to the nearest whole number, ties to even.  A row
  * with a NaN or an infinity gets the scale NaN and codes zero.  n % 16 == 0
  * (IQK_E_SHAPE), n <= 2^16, rows <= 2^24 (IQK_E_ARG); x and codes 16-byte
- * aligned. */
+ * aligned.  Results overlap no input (codes over x: IQK_E_ARG). */
 int iqk_int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, int8_t* codes, float* scales,
                       void* stream);
 
@@ -534,7 +535,8 @@ int iqk_int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t n, int8_
  * x_scales [M], or a float type with x_scales null, which the call quantizes as
  * iqk_int8_quantize does.  workspace (16-byte aligned, iqk_int8_linear_workspace
  * bytes, 0 for a few rows) holds the quantized x, which IQK_INT8 x does without;
- * it may be null where 0 bytes are needed.  x 16-byte aligned; M <= 2^24. */
+ * it may be null where 0 bytes are needed.  x 16-byte aligned; M <= 2^24.  y
+ * overlaps no input (x: IQK_E_ARG). */
 int iqk_int8_linear_workspace(const iqk_int8_weights* w, int64_t M, int x_dtype, size_t* bytes);
 int iqk_int8_linear(const iqk_int8_weights* w, const void* x, int x_dtype, const float* x_scales, int64_t M,
                     void* workspace, size_t ws_bytes, void* y, int y_dtype, void* stream);
@@ -543,7 +545,8 @@ int iqk_int8_linear(const iqk_int8_weights* w, const void* x, int x_dtype, const
  * and offsets): rows offsets[e] .. offsets[e + 1] - 1 of x device [rows, in] by
  * expert e's weights -> y device [rows, out].  offsets device int32 [experts +
  * 1], from 0, not falling, up to rows at most (others are cut to [0, rows]);
- * rows from offsets[experts] on have no expert and get zeros.  rows <= 2^24. */
+ * rows from offsets[experts] on have no expert and get zeros.  rows <= 2^24.  y
+ * overlaps no input, as above. */
 int iqk_int8_grouped_workspace(const iqk_int8_weights* w, int64_t rows, int x_dtype, size_t* bytes);
 int iqk_int8_grouped(const iqk_int8_weights* w, const void* x, int x_dtype, const float* x_scales,
                      const int32_t* offsets, int64_t rows, void* workspace, size_t ws_bytes, void* y, int y_dtype,

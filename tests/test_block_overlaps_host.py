@@ -31,3 +31,38 @@ BYTES = T * N * 2
 def test_norm_refuses_overlaps(r, h, types):
     assert _norm(r, h, *types) == E_ARG
     assert b"overlap" in q._lib.iqk_last_error()
+
+
+INT8 = 4
+SX, IDS, XS, OFF, PLACE = 1 * FAR, 2 * FAR, 3 * FAR, 4 * FAR, 5 * FAR
+
+
+@pytest.mark.parametrize("k,xs,place", [
+    (1, SX, PLACE), (4, SX, PLACE), (4, SX - 4 * BYTES + 2, PLACE), (2, SX + BYTES - 2, PLACE),
+    (1, XS, IDS), (4, XS, IDS + 4 * (4 * T - 1)), (4, XS, IDS - 4 * (4 * T - 1))])
+def test_sort_refuses_overlaps(k, xs, place):
+    """In place, or over the end or the beginning of it."""
+    assert q._lib.iqk_moe_sort(SX, BF16, IDS, T, k, 8, N, None, 0, xs, OFF, place, None) == E_ARG
+    assert b"overlap" in q._lib.iqk_last_error()
+
+
+@pytest.mark.parametrize("codes", [X, X + T * N * 4 - 16, X - T * N + 16])
+def test_quantize_refuses_overlaps(codes):
+    assert q._lib.iqk_int8_quantize(X, F32, T, N, codes, R, None) == E_ARG
+    assert b"overlap" in q._lib.iqk_last_error()
+
+
+@pytest.mark.parametrize("rows", [1, T, 100])
+@pytest.mark.parametrize("x_dtype,scales", [(F32, None), (BF16, None), (INT8, R)])
+@pytest.mark.parametrize("at", ["in place", "end", "beginning"])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_products_refuse_overlaps(rows, x_dtype, scales, at, grouped):
+    size = {F32: 4, BF16: 2, INT8: 1}[x_dtype]
+    y = {"in place": X, "end": X + rows * N * size - 4, "beginning": X - rows * N * 4 + 4}[at]
+    w = q._Int8Weights(1, N, N, 3 * FAR, N * N, 4 * FAR, N)
+    tail = (rows, 7 * FAR, 1 << 19, y, F32, None)
+    if grouped:
+        rc = q._lib.iqk_int8_grouped(ctypes.byref(w), X, x_dtype, scales, 8 * FAR, *tail)
+    else:
+        rc = q._lib.iqk_int8_linear(ctypes.byref(w), X, x_dtype, scales, *tail)
+    assert rc == E_ARG and b"overlap" in q._lib.iqk_last_error()
