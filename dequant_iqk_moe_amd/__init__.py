@@ -1123,7 +1123,7 @@ def int8_linear(w: Int8Weights, x: torch.Tensor, x_scales: torch.Tensor | None =
     n = w.in_features
     if x.dim() == 0 or x.shape[-1] != n:
         raise IqkValueError(_E_SIZE, f"x must be [..., {n}]")
-    _one_device(x, w.codes, x_scales, workspace, y)
+    _one_device(x, w.codes, w.scales, x_scales, workspace, y)
     M = x.numel() // n
     xp, xdt, sp = _int8_x(x, x_scales, M, n)
     cw = w._c()
@@ -1146,7 +1146,7 @@ def int8_grouped(w: Int8Weights, x: torch.Tensor, offsets: torch.Tensor, x_scale
     expert's are zeros.  x as in int8_linear."""
     if x.dim() != 2 or x.shape[1] != w.in_features:
         raise IqkValueError(_E_SIZE, f"x must be [rows, {w.in_features}]")
-    _one_device(x, w.codes, offsets, x_scales, workspace, y)
+    _one_device(x, w.codes, w.scales, offsets, x_scales, workspace, y)
     rows, n = x.shape
     xp, xdt, sp = _int8_x(x, x_scales, rows, n)
     op = _at(offsets, "offsets", torch.int32, w.experts + 1)
