@@ -28,3 +28,54 @@ def test_products_refuse_another_device(grouped, which, monkeypatch):
     (given[which] if which in given else getattr(w, which)).at = 1
     with pytest.raises(q.IqkValueError, match="cuda:1"):
         (q.int8_grouped if grouped else q.int8_linear)(w, **given)
+
+
+class FakeDual(Fake):
+    """a dual tensor of forward-mode differentiation"""
+
+    tangent = 1
+
+
+@pytest.fixture
+def dual_level(monkeypatch):
+    """An open level in which FakeDual has a tangent; ordinary tensors are looked at as they are."""
+    real = q._forward_ad.unpack_dual
+    fake = lambda t: t if isinstance(t, FakeDual) else real(t) if isinstance(t, torch.Tensor) else FakeNone()
+    monkeypatch.setattr(q._forward_ad, "unpack_dual", fake)
+    with q._forward_ad.dual_level():
+        yield
+
+
+class FakeNone:
+    tangent = None
+
+
+def _calls(x):
+    """Calls that carry gradients, with x in each place that one is carried from."""
+    like = lambda *shape, dtype=F32: Fake(shape, dtype)
+    ids, place = like(4, 2, dtype=I32), like(2, 2, dtype=I32)
+    return (lambda: q.moe_sort(x, ids, 4), lambda: q.moe_unsort(x, place), lambda: q.moe_unsort(like(4, 64), place, x),
+            lambda: q.block_norm(x, next_weight=like(64)), lambda: q.block_norm(like(4, 64), x), lambda: q.block_norm(like(4, 64), like(4, 64), x),
+            lambda: q.block_norm(like(4, 64), like(4, 64), gate=x), lambda: q.block_norm(like(4, 64), next_weight=x), lambda: q.router_topk(x, 2))
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_forward_mode_is_refused(which, dual_level):
+    """A tangent would be lost without a word, with gradients switched off too."""
+    for context in (torch.enable_grad, torch.no_grad):
+        with context(), pytest.raises(q.IqkValueError, match="tangent"):
+            _calls(FakeDual((4, 64), F32))[which]()
+
+
+def test_forward_mode_of_real_tensors():
+    x, v = torch.randn(4, 64), torch.randn(4, 64)
+    with q._forward_ad.dual_level():
+        dual = q._forward_ad.make_dual(x, v)
+        for call in (lambda: q.block_norm(dual, dual), lambda: q.moe_unsort(dual, torch.zeros(2, 2, dtype=I32))):
+            with pytest.raises(q.IqkValueError, match="tangent"):
+                call()
+        assert not q._wants_grad(x, None, dual.detach())  # (what has none is no one's loss)
+        assert q._wants_grad(x, v.clone().requires_grad_())
+        with torch.inference_mode():
+            assert not q._wants_grad(dual)  # (no operation carries one there)
+    assert not q._wants_grad(x)
