@@ -892,6 +892,10 @@ def _wants_grad(*tensors: torch.Tensor | None) -> bool:
     return False
 
 
+def _refuse_grad(call: str):
+    raise IqkValueError(_E_ARG, f"{call} has no gradient: detach what requires one, or call it under torch.no_grad()")
+
+
 def _written(*given: torch.Tensor | None):
     """Caller's buffers that a call wrote: a gradient of an earlier call that still needs one can tell."""
     for t in given:
@@ -1064,7 +1068,7 @@ class Int8Weights:
         if self.codes.numel() == 0:
             raise IqkValueError(_E_ARG, "codes hold no values")
         self.experts, self.out, self.in_features = self.codes.shape
-        if self.scales.dtype != torch.float32 or tuple(self.scales.shape) != (self.experts, self.out):
+        if self.scales.dtype != torch.float32 or self.scales.shape != (self.experts, self.out):
             raise IqkValueError(_E_SIZE, "scales must be float32 [experts, out]")
 
     def _c(self) -> _Int8Weights:
@@ -1073,11 +1077,14 @@ class Int8Weights:
 
 
 def int8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None, stream=None):
-    """x [..., n] -> (codes int8 [..., n], scales float32 [...]), one scale per row."""
+    """x [..., n] -> (codes int8 [..., n], scales float32 [...]), one scale per
+    row.  It has no gradient: x that requires one is refused."""
     dt = _float_dtype(x, "x")
     if x.dim() == 0 or x.shape[-1] == 0:
         raise IqkValueError(_E_ARG, "x must be [..., n] with n > 0")
     _one_device(x, codes, scales)
+    if _wants_grad(x):
+        _refuse_grad("int8_quantize")
     n = x.shape[-1]
     rows = x.numel() // n
     xp = _at(x, "x")
@@ -1127,11 +1134,14 @@ def int8_linear(w: Int8Weights, x: torch.Tensor, x_scales: torch.Tensor | None =
                 workspace: torch.Tensor | None = None, y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y [..., out] = x [..., in] times 8-bit integer weights.  x in a float type
     is quantized on the way (as int8_quantize does); codes come with their
-    x_scales."""
+    x_scales.  The product has no gradient: x and scales that require one are
+    refused."""
     n = w.in_features
     if x.dim() == 0 or x.shape[-1] != n:
         raise IqkValueError(_E_SIZE, f"x must be [..., {n}]")
     _one_device(x, w.codes, w.scales, x_scales, workspace, y)
+    if _wants_grad(x, w.scales, x_scales):
+        _refuse_grad("int8_linear")
     M = x.numel() // n
     xp, xdt, sp = _int8_x(x, x_scales, M, n)
     cw = w._c()
@@ -1139,10 +1149,11 @@ def int8_linear(w: Int8Weights, x: torch.Tensor, x_scales: torch.Tensor | None =
     if y is None:
         y = _new(x, (*x.shape[:-1], w.out), out_dtype, stream)
     need = _int8_bytes("iqk_int8_linear_workspace", w.experts, w.out, n, M, xdt)
-    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream) if need or workspace is not None else (None, None, 0)
     _check(_lib.iqk_int8_linear(ctypes.byref(cw), xp, xdt, sp, M, wp, nbytes, _at(y, "y", None, M * w.out),
                                 _float_dtype(y, "y"), _stream(stream)))
-    _written(given)
+    if given is not None:
+        _written(given)
     return y
 
 
@@ -1155,6 +1166,8 @@ def int8_grouped(w: Int8Weights, x: torch.Tensor, offsets: torch.Tensor, x_scale
     if x.dim() != 2 or x.shape[1] != w.in_features:
         raise IqkValueError(_E_SIZE, f"x must be [rows, {w.in_features}]")
     _one_device(x, w.codes, w.scales, offsets, x_scales, workspace, y)
+    if _wants_grad(x, w.scales, x_scales):
+        _refuse_grad("int8_grouped")
     rows, n = x.shape
     xp, xdt, sp = _int8_x(x, x_scales, rows, n)
     op = _at(offsets, "offsets", torch.int32, w.experts + 1)
@@ -1163,10 +1176,11 @@ def int8_grouped(w: Int8Weights, x: torch.Tensor, offsets: torch.Tensor, x_scale
     if y is None:
         y = _new(x, (rows, w.out), out_dtype, stream)
     need = _int8_bytes("iqk_int8_grouped_workspace", w.experts, w.out, n, rows, xdt)
-    ws, wp, nbytes = _workspace(workspace, need, x.device, stream)
+    ws, wp, nbytes = _workspace(workspace, need, x.device, stream) if need or workspace is not None else (None, None, 0)
     _check(_lib.iqk_int8_grouped(ctypes.byref(cw), xp, xdt, sp, op, rows, wp, nbytes,
                                  _at(y, "y", None, rows * w.out), _float_dtype(y, "y"), _stream(stream)))
-    _written(given)
+    if given is not None:
+        _written(given)
     return y
 
 

@@ -79,3 +79,46 @@ def test_forward_mode_of_real_tensors():
         with torch.inference_mode():
             assert not q._wants_grad(dual)  # (no operation carries one there)
     assert not q._wants_grad(x)
+
+
+class FakeLeaf(Fake):
+    requires_grad = True
+
+
+@pytest.mark.parametrize("which", ["x", "x_scales", "scales"])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_products_refuse_what_requires_a_gradient(which, grouped, monkeypatch):
+    """They have none to give, and a result without one would pass for a constant."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    w = _weights()
+    given = dict(x=Fake((3, 16), I8), x_scales=Fake((3,), F32), workspace=Fake((1 << 20,), torch.uint8), y=Fake((3, 4), F32))
+    if grouped:
+        given["offsets"] = Fake((3,), I32)
+    if which == "scales":
+        w.scales = FakeLeaf((2, 4), F32)
+    else:
+        given[which] = FakeLeaf(given[which].shape, F32)
+    call = q.int8_grouped if grouped else q.int8_linear
+    with pytest.raises(q.IqkValueError, match="no gradient"):
+        call(w, **given)
+    given["y"] = Fake((3, 5), F32)  # where gradients are off the call goes on, to the next mistake
+    with torch.no_grad(), pytest.raises(q.IqkValueError) as e:
+        call(w, **given)
+    assert "no gradient" not in str(e.value)
+
+
+def test_quantization_refuses_what_requires_a_gradient():
+    x = torch.randn(3, 32, requires_grad=True)
+    with pytest.raises(q.IqkValueError, match="no gradient"):
+        q.int8_quantize(x)
+    for context, v in ((torch.no_grad, x), (torch.enable_grad, x.detach())):
+        with context(), pytest.raises(q.IqkValueError, match="device tensor"):
+            q.int8_quantize(v)
+
+
+def test_products_refuse_forward_mode(dual_level):
+    with torch.no_grad():
+        for call in (lambda: q.int8_linear(_weights(), FakeDual((3, 16), F32)), lambda: q.int8_quantize(FakeDual((3, 16), F32)),
+                     lambda: q.int8_grouped(_weights(), FakeDual((3, 16), F32), Fake((3,), I32))):
+            with pytest.raises(q.IqkValueError, match="tangent"):
+                call()
