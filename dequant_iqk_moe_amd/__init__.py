@@ -1010,9 +1010,14 @@ def moe_unsort(ys: torch.Tensor, place: torch.Tensor, weights: torch.Tensor | No
 
 
 class _Unsort(torch.autograd.Function):
+    """Rows are kept for the weights' gradient only, and weights for the rows': a layer's largest tensor may go, or be
+    written over, where the router is not trained."""
+
     @staticmethod
     def forward(ctx, ys, place, weights, out_dtype):
-        ctx.save_for_backward(ys, place, weights)
+        want_ys, _, want_w = ctx.needs_input_grad[:3]
+        ctx.save_for_backward(ys if want_w else None, place, weights if want_ys else None)
+        ctx.rows, ctx.weights = (ys.shape, ys.dtype), None if weights is None else weights.shape
         return _unsort(ys.detach(), place, None if weights is None else weights.detach(), out_dtype, None, None)
 
     @staticmethod
@@ -1020,8 +1025,19 @@ class _Unsort(torch.autograd.Function):
     def backward(ctx, dy):
         ys, place, weights = ctx.saved_tensors
         want_ys, _, want_w = ctx.needs_input_grad[:3]
-        d_ys, d_w = moe_unsort_grad(dy.contiguous(), ys, place, weights, want_ys=want_ys, want_weights=want_w)
+        (rows, n), dtype = ctx.rows
+        d_ys = dy.new_empty((rows, n), dtype=dtype) if want_ys else None
+        d_w = dy.new_empty(ctx.weights, dtype=torch.float32) if want_w else None
+        T, k = place.shape
+        _unsort_grad(dy.contiguous(), None if ys is None else ys.data_ptr(), _DT[dtype], place.data_ptr(),
+                     None if weights is None else weights.data_ptr(), T, k, n, dtype, d_ys, d_w, None)
         return d_ys, None, d_w, None
+
+
+def _unsort_grad(dy, yp, dt, pp, wp, T, k, n, dtype, d_ys, d_weights, stream):
+    _check(_lib.iqk_moe_unsort_grad(_at(dy, "dy", None, T * n), _float_dtype(dy, "dy"), yp, dt, pp, wp, T, k, n,
+                                    _at(d_ys, "d_ys", dtype, T * k * n), _at(d_weights, "d_weights", torch.float32, T * k),
+                                    _stream(stream)))
 
 
 def moe_unsort_grad(dy: torch.Tensor, ys: torch.Tensor, place: torch.Tensor, weights: torch.Tensor | None = None,
@@ -1031,8 +1047,7 @@ def moe_unsort_grad(dy: torch.Tensor, ys: torch.Tensor, place: torch.Tensor, wei
     d_weights float32 [T, k]); None for one that is not wanted, and for d_weights
     where weights is None."""
     _one_device(dy, ys, place, weights, d_ys, d_weights)
-    yp, dt, pp, wp, T, k, n = _check_unsort(ys, place, weights)
-    dp, ddt = _at(dy, "dy", None, T * n), _float_dtype(dy, "dy")
+    checked = _check_unsort(ys, place, weights)
     want_weights = want_weights and weights is not None
     if not want_ys and not want_weights:
         raise IqkValueError(_E_ARG, "neither gradient is wanted")
@@ -1041,8 +1056,7 @@ def moe_unsort_grad(dy: torch.Tensor, ys: torch.Tensor, place: torch.Tensor, wei
         d_ys = _like(ys, stream)
     if want_weights and d_weights is None:
         d_weights = _like(weights, stream)
-    _check(_lib.iqk_moe_unsort_grad(dp, ddt, yp, dt, pp, wp, T, k, n, _at(d_ys, "d_ys", ys.dtype, T * k * n),
-                                    _at(d_weights, "d_weights", torch.float32, T * k), _stream(stream)))
+    _unsort_grad(dy, *checked, ys.dtype, d_ys, d_weights, stream)
     _written(*given)
     return d_ys, d_weights
 
