@@ -568,14 +568,20 @@ def moe_prefill_fused(w: Weights, x: torch.Tensor, ids: torch.Tensor, values=Non
     return y
 
 
+def _stream_object(stream):
+    """The stream given as an object or as a handle.  The handle 0 is the default stream's (ExternalStream(0) is a new
+    stream that nothing orders behind the others)."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
     """A new tensor of the stream the call runs on (the caching allocator may
     give a tensor's memory away while another stream still writes it)."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
+    with torch.cuda.stream(_stream_object(stream)):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -907,7 +913,7 @@ def _on(stream):
     """The given stream as the current one (backward passes run on the stream of their forward call)."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    return torch.cuda.stream(_stream_object(stream))
 
 
 @functools.lru_cache(maxsize=1024)
