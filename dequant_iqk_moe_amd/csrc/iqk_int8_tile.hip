@@ -7,11 +7,12 @@
 // and the scales are applied once at the end.
 //
 // Bound: the matrix instructions run at 3.2 POP/s by themselves on such values (their
-// power; 4.4 on zeros), and a tile of 256 x 256 needs 64 KiB from the L2 for each 33.6
-// MOP.  8192 x 4096 x 4096 takes 127 us (2.16 POP/s; 2.10 in a library's product
-// without scales): without copies 85, without the results' stores 113, with codes of
-// zero 115.  Smaller tiles copy more for a product: 24576 rows by 64 experts of 2048 x
-// 4096 take 276 us (1.5 POP/s, 8 % of the products on rows that are not there).
+// power; 4.4 on zeros), and a tile of 256 x 256 needs 64 KiB from the L2 for each 16.8
+// MOP.  8192 x 4096 x 4096 takes 127 us (2.16 POP/s beside copies at 8.5 TB/s; 2.10
+// POP/s in a library's product without scales): without copies 85, without the
+// results' stores 113, with codes of zero 115.  Smaller tiles copy more for a product:
+// 128 x 256 need 48 KiB for 8.4 MOP, and 24576 rows by 64 experts of 2048 x 4096 take
+// 276 us (1.5 POP/s, 8 % of the products on rows that are not there).
 // Two stages of a tile of 256 x 256 are 128 KiB of LDS, so a CU has one: eight waves,
 // two a SIMD, whose sums are 128 of their 256 registers.
 #include <algorithm>

@@ -515,10 +515,11 @@ void by_row(int64_t n, bool wide, F f) {
     else go(Int<512>{}, Int<16>{});
 }
 
-// The gradient, whose parts of the parameters' gradients and their values take six
-// registers a value: eight values of a thread as far as 512 threads reach, in 122
-// registers, so that a CU holds two teams of 4096 values (rows of 4095 x 4096 46 us;
-// 60 with branches for a row's end and 256 threads of sixteen values).
+// The gradient, whose parts of the parameters' gradients and their values take five
+// registers a value: eight values of a thread as far as 512 threads reach, in 108 to
+// 117 registers, so that a CU holds two teams of 4096 values (rows of 4095 x 4096 46
+// us; 60 with branches for a row's end and 256 threads of sixteen values).  In single
+// values they take 127 to 153, and a CU holds one team of 512 threads (4095 x 4095 77 us).
 template <class F>
 void by_grad_row(int64_t n, bool wide, F f) {
     auto go = [&](auto team, auto values) {
@@ -551,11 +552,12 @@ bool wide_rows(const iqk_block& b, std::initializer_list<const void*> more) {
     return wide;
 }
 
-// Teams of the gradient, at most the threads that the card's CUs hold of it (1024 of up to 128 registers, 512 of
-// more).  A team's time grows with its rows and the join's with the teams, so the sum is least where rows grow with
-// the root of T, and with powers of two, which leave the CUs equal shares: 4095 x 512 takes 29 us with a team for each
-// row, 19.5 with one for two rows, 16.2 for four, 18.5 for eight; 300 rows 8.9, 8.5, 11.1, 15.4; 8192 rows 28, 28, 22
-// and 22, and 24.5 with six.
+// Teams of the gradient, at most the threads that the card's CUs hold of it in chunks of eight values: 1024 of a CU up
+// to n = 4096 (up to 128 registers), 512 beyond.  Single values, which take more, go by the same number (it gives the
+// workspace's size, in which addresses have no part): a CU holds fewer of those teams at a time.  A team's time grows
+// with its rows and the join's with the teams, so the sum is least where rows grow with the root of T, and with powers
+// of two, which leave the CUs equal shares: 4095 x 512 takes 29 us with a team for each row, 19.5 with one for two rows,
+// 16.2 for four, 18.5 for eight; 300 rows 8.9, 8.5, 11.1, 15.4; 8192 rows 28, 28, 22 and 22, and 24.5 with six.
 int64_t grad_teams(int64_t T, int64_t n) {
     const int team = team_size(n), per = team == 64 ? 4 : 1;
     const int64_t most = 256 * (n <= 4096 ? 1024 : 512) / team;
