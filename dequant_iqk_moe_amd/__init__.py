@@ -618,7 +618,8 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
     T, E = logits.shape
     if not 1 <= k <= E:
         raise IqkValueError(_E_ARG, f"k = {k} outside [1, {E}]")
-    carries = _wants_grad(logits)
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        _refuse_tangents(logits)
     given = [t for t in (ids, weights) if t is not None]
     if ids is None:
         ids = _empty((T, k), torch.int32, logits.device, stream)
@@ -631,7 +632,7 @@ def router_topk(logits: torch.Tensor, k: int, scoring: str = "softmax", bias: to
     for t in given:  # a gradient of an earlier call that still needs a caller's buffer can tell
         if not t.is_inference():
             torch.autograd.graph.increment_version(t)
-    if carries:
+    if logits.requires_grad and torch.is_grad_enabled():
         weights = _RouterWeights.apply(logits, ids, weights.detach(), scoring, renorm, scale)
     return ids, weights
 
@@ -884,13 +885,19 @@ def _one_device(*tensors: torch.Tensor | None):
             raise IqkValueError(_E_ARG, f"a tensor on cuda:{at} where cuda:{here} is current")
 
 
+def _refuse_tangents(*tensors: torch.Tensor | None):
+    """No call has a forward-mode derivative, and a result without one would pass for a constant."""
+    if torch.is_inference_mode_enabled():
+        return
+    for t in tensors:
+        if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+            raise IqkValueError(_E_ARG, "a tensor carries a forward-mode tangent, which no call here hands on")
+
+
 def _wants_grad(*tensors: torch.Tensor | None) -> bool:
-    """Whether a result is to carry a gradient.  Forward-mode tangents are refused: no call has a derivative of that
-    kind, and a result without one would pass for a constant."""
-    if getattr(_forward_ad, "_current_level", 0) >= 0 and not torch.is_inference_mode_enabled():
-        for t in tensors:
-            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
-                raise IqkValueError(_E_ARG, "a tensor carries a forward-mode tangent, which no call here hands on")
+    """Whether a result is to carry a gradient."""
+    if getattr(_forward_ad, "_current_level", 0) >= 0:
+        _refuse_tangents(*tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
