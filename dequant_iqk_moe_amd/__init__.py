@@ -1122,7 +1122,8 @@ def int8_quantize(x: torch.Tensor, codes: torch.Tensor | None = None, scales: to
         scales = _new(x, x.shape[:-1], torch.float32, stream)
     _check(_lib.iqk_int8_quantize(xp, dt, rows, n, _at(codes, "codes", torch.int8, rows * n),
                                   _at(scales, "scales", torch.float32, rows), _stream(stream)))
-    _written(*given)
+    if given[0] is not None or given[1] is not None:
+        _written(*given)
     return codes, scales
 
 
