@@ -597,8 +597,8 @@ int iqk_block_norm(const iqk_block* b, void* r, void* h, void* stream);
  * y.  Without dh next_weight has no part in any result, dx = alpha * dr and,
  * without post_weight, dy = beta * gate * dr, whatever x, y and next_weight hold
  * (infinities and NaN among it).  Parameters' gradients are float32 sums over the
- * tokens, in an order that depends on T and n alone, rounded once; results overlap
- * no input.  workspace (16-byte aligned, iqk_block_norm_grad_workspace bytes) holds
+ * tokens, in an order of T, n and whether all rows and parameters begin at
+ * multiples of 16 bytes, rounded once; results overlap no input.  workspace (16-byte aligned, iqk_block_norm_grad_workspace bytes) holds
  * parts of those sums; it may be null where none are asked for. */
 int iqk_block_norm_grad_workspace(const iqk_block* b, size_t* bytes);
 int iqk_block_norm_grad(const iqk_block* b, const void* dr, const void* dh, void* dx, void* dy, void* d_post,
